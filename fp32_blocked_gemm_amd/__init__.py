@@ -24,6 +24,9 @@ OG_ERR_TOO_LARGE = -4
 EXACT = 0
 FAST = 1
 FAST_MFMA = 2  # fast under a stated tolerance (split k, fp32 matrix cores); see og.h
+F32 = 0
+BF16 = 1
+F16 = 2
 ACT_NONE = 0
 ACT_RELU = 1
 _ACTS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, ACT_NONE: ACT_NONE, ACT_RELU: ACT_RELU}
@@ -74,6 +77,11 @@ def lib() -> ctypes.CDLL:
     L.og_get_variant.restype = ctypes.c_int
     L.og_gemm_choice.argtypes = [_i64, _i64, _i64, ctypes.c_int]
     L.og_gemm_choice.restype = ctypes.c_int
+    L.og_newton_schulz.argtypes = ([_i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, ctypes.c_int]
+                                   + [ctypes.c_float] * 4 + [_vp, _i64, _i64, _vp, _i64])
+    L.og_newton_schulz.restype = ctypes.c_int
+    L.og_newton_schulz_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+    L.og_newton_schulz_workspace.restype = _i64
     L.og_last_error.argtypes = []
     L.og_last_error.restype = ctypes.c_char_p
     L.og_version.argtypes = []
@@ -277,4 +285,83 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0, 0, 0), dil=(1, 1), groups=1, mode="ex
                 pad[3], dil[0], dil[1], x.data_ptr(), w.data_ptr(),
                 None if bias is None else bias.data_ptr(), _ACTS[act],
                 None if residual is None else residual.data_ptr(), out.data_ptr(), _mode(mode)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators of language models around the N x K product.
+# ---------------------------------------------------------------------------
+
+def _type(t, allowed=(F32, BF16)) -> int:
+    torch = _torch()
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code not in allowed:
+        names = ", ".join(("float32", "bfloat16", "float16")[a] for a in allowed)
+        raise ValueError(f"a tensor of {t.dtype}: {names} expected")
+    return code
+
+
+def _one_device(*ts):
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _workspace(nbytes, workspace, dev):
+    """`workspace` (a CUDA byte tensor the caller keeps), or one of the allocator's
+    for this call, on the current stream."""
+    torch = _torch()
+    _check(min(nbytes, 0))
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
+    return workspace
+
+
+def newton_schulz_workspace(batch, m, n, dtype) -> int:
+    """Bytes newton_schulz needs for `batch` m x n matrices of `dtype` (F32 or BF16)."""
+    b = int(lib().og_newton_schulz_workspace(batch, m, n, dtype))
+    _check(min(b, 0))
+    return b
+
+
+def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None,
+                  workspace=None):
+    """The orthogonalised update of G (og_newton_schulz): X = G / (|G| + eps), then `steps`
+    times X <- a X + (b A + c A A) X with A = X X^T and (a, b, c) = coeffs.
+
+    G: float32 or bfloat16, [..., m, n], the last two dimensions a matrix with contiguous
+    rows; any leading dimensions are a batch (a view that does not reduce to one batch
+    stride is refused).  out may be G itself."""
+    torch = _torch()
+    if G.dim() < 2:
+        raise ValueError("expected a tensor of at least two dimensions")
+    code = _type(G)
+    if out is None:
+        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    if out.shape != G.shape or out.dtype != G.dtype:
+        raise ValueError("out must have G's shape and type")
+    dev = _one_device(G, out)
+    m, n = G.shape[-2:]
+    batch = G.shape[:-2].numel()
+    g3, o3 = G, out
+    if G.dim() != 3:
+        try:
+            g3, o3 = G.view(batch, m, n), out.view(batch, m, n)
+        except RuntimeError:
+            raise ValueError("the leading dimensions must reduce to one batch stride") from None
+    with torch.cuda.device(dev):
+        _use_stream_of(out)
+        ws = _workspace(int(lib().og_newton_schulz_workspace(batch, m, n, code)), workspace, dev)
+        a, b, c = coeffs
+        rows_g, rows_o = _ld(g3[0]) if batch else max(1, n), _ld(o3[0]) if batch else max(1, n)
+        _check(lib().og_newton_schulz(batch, m, n, g3.data_ptr(), rows_g,
+                                      g3.stride(0) if batch > 1 else 0, code, steps, a, b, c, eps,
+                                      o3.data_ptr(), rows_o, o3.stride(0) if batch > 1 else 0,
+                                      ws.data_ptr(), ws.numel()))
     return out

@@ -20,9 +20,10 @@ OBJDIR = os.path.join(HERE, "_build")
 API = os.path.join(CSRC, "og_api.hip")
 UNITS = os.path.join(CSRC, "og_units.hip")
 N_UNITS = 17  # kernel groups of og_units.hip, compiled in parallel
-SOURCES = [API, UNITS]
-HEADERS = [os.path.join(CSRC, "og_kernels.hpp"), os.path.join(CSRC, "og_launch.hpp"),
-           os.path.join(INCLUDE, "og.h")]
+OPERATORS = [os.path.join(CSRC, f) for f in ("og_ns.hip",)]  # one object each
+SOURCES = [API, UNITS, *OPERATORS]
+HEADERS = [os.path.join(CSRC, f) for f in ("og_host.hpp", "og_kernels.hpp", "og_launch.hpp",
+                                           "og_tile.hpp")] + [os.path.join(INCLUDE, "og.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -67,7 +68,8 @@ def build(verbose: bool = False) -> str:
     before = _digest()
     os.makedirs(OBJDIR, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
-    jobs = [(API, [], os.path.join(OBJDIR, "og_api.o"))]
+    jobs = [(src, [], os.path.join(OBJDIR, os.path.basename(src).replace(".hip", ".o")))
+            for src in [API, *OPERATORS]]
     jobs += [(UNITS, [f"-DOG_UNIT={u}"], os.path.join(OBJDIR, f"og_unit{u}.o"))
              for u in range(1, N_UNITS + 1)]
     cmds = [[HIPCC, *FLAGS, *inc, *defs, "-c", src, "-o", obj] for src, defs, obj in jobs]

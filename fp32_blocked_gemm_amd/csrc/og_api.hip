@@ -15,6 +15,7 @@
 #include <string>
 
 #include "og.h"
+#include "og_host.hpp"
 #include "og_kernels.hpp"
 #include "og_launch.hpp"
 
@@ -25,6 +26,15 @@ using namespace og::host;
 thread_local hipStream_t t_stream = nullptr;
 thread_local int t_variant = 0;
 thread_local std::string t_error;
+
+constexpr int kMaxDevices = 64;
+int g_device_state[kMaxDevices];  // 0 unknown, 1 gfx950, -1 other
+
+}  // namespace
+
+namespace og::host {
+
+hipStream_t current_stream() { return t_stream; }
 
 og_status fail(og_status code, const char *fmt, ...) {
   char buf[512];
@@ -40,9 +50,6 @@ og_status ok() {
   t_error.clear();
   return OG_OK;
 }
-
-constexpr int kMaxDevices = 64;
-int g_device_state[kMaxDevices];  // 0 unknown, 1 gfx950, -1 other
 
 // The current device must be a gfx950.
 og_status check_device() {
@@ -72,6 +79,9 @@ og_status check_launch(const char *what) {
   return ok();
 }
 
+}  // namespace og::host
+
+namespace {
 
 // The shape the kernel choice sees: a group's product (M x N x K) and, for
 // a convolution, the pixels of one output image and the window size (the

@@ -1,0 +1,369 @@
+// og_ns.hip -- og_newton_schulz_f32 / _bf16: the orthogonalised update of a
+// matrix by Newton-Schulz products.
+//
+//   X = G / (|G| + eps)   (the Frobenius norm; the shorter side as rows, r <= k)
+//   each step:  A = X X^T,  B = b A + c A A,  X <- a X + B X
+//
+// Every product runs on the bf16 matrix cores with its operands in planes
+// (og_tile.hpp): three planes for fp32 input (fp32 accuracy), two for bf16
+// input (16 bits: the polynomial's slope of up to a per step lifts a rounding
+// of X by a^steps, 484 at the usual coefficients, in the directions it
+// stretches most, so that X held in 8 bits, as one plane, would lose the
+// result's last bits; 16 bits keep the error two hundred times below the
+// rounding of the output).  A and A A are symmetric: only the tiles on and
+// below the diagonal are computed and each is stored to both places, a
+// quarter of the step's work at r = k.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "og.h"
+#include "og_host.hpp"
+#include "og_tile.hpp"
+
+namespace og::ns {
+
+using namespace og::tile;
+
+constexpr int kNormBlocks = 256;  // partial sums of squares per matrix
+
+struct Input {
+  const void *g;
+  int64_t ld, batch;
+  int m, n;  // of G
+};
+
+template <class T>
+__device__ __forceinline__ float load(const void *p, int64_t i) {
+  return (float)static_cast<const T *>(p)[i];
+}
+
+// Partial sums of squares of G, in 64 bits (no square of an fp32 value
+// overflows there).  One pass over G: bound by its bytes.
+template <class T>
+__global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
+  const int batch = blockIdx.y;
+  double s = 0;
+  const int64_t base = batch * in.batch;
+  const int64_t count = (int64_t)in.m * in.n;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += step) {
+    const int64_t row = i / in.n;
+    const double v = load<T>(in.g, base + row * in.ld + (i - row * in.n));
+    s += v * v;
+  }
+  __shared__ double sum[256];
+  sum[threadIdx.x] = s;
+  __syncthreads();
+  for (int h = 128; h > 0; h >>= 1) {
+    if (threadIdx.x < h) sum[threadIdx.x] += sum[threadIdx.x + h];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) part[batch * kNormBlocks + blockIdx.x] = sum[0];
+}
+
+// X's planes from G: 64 x 64 tiles through LDS (G is read along its rows
+// whichever way X lies), padded with zeros to ld columns.
+template <class T, int P, bool TALL>
+__global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part, int blocks,
+                                                   float eps, uint16_t *x, int64_t ld,
+                                                   int64_t plane) {
+  __shared__ float tile[64][65];
+  __shared__ float factor;
+  const int batch = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const int R = TALL ? in.n : in.m, C = TALL ? in.m : in.n;
+  if (threadIdx.x < 64) {
+    double s = 0;
+    for (int i = threadIdx.x; i < blocks; i += 64) s += part[batch * kNormBlocks + i];
+    for (int h = 32; h > 0; h >>= 1) s += __shfl_xor(s, h);
+    if (threadIdx.x == 0) factor = (float)(1.0 / ((double)(float)sqrt(s) + (double)eps));
+  }
+  const int64_t base = batch * in.batch;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int i = w; i < 64; i += 4) {
+    if (TALL) {
+      const int c = c0 + i, r = r0 + lane;
+      tile[lane][i] = c < C && r < R ? load<T>(in.g, base + (int64_t)c * in.ld + r) : 0.0f;
+    } else {
+      const int r = r0 + i, c = c0 + lane;
+      tile[i][lane] = r < R && c < C ? load<T>(in.g, base + (int64_t)r * in.ld + c) : 0.0f;
+    }
+  }
+  __syncthreads();
+  const float f = factor;
+  for (int q = threadIdx.x; q < 64 * 16; q += 256) {
+    const int i = q >> 4, j = (q & 15) * 4;
+    if (r0 + i >= R) continue;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = tile[i][j + e] * f;
+    bf16x4 out[P];
+    split4<P>(v, out);
+    uint16_t *to = x + batch * P * plane + (int64_t)(r0 + i) * ld + c0 + j;
+#pragma unroll
+    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * plane) = out[p];
+  }
+}
+
+template <int P>
+__device__ __forceinline__ f32x4 load_planes(const uint16_t *p, int64_t plane) {
+  f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int q = P - 1; q >= 0; --q) {
+    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(p + q * plane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += (float)h[e];
+  }
+  return v;
+}
+
+// Epilogue of the symmetric products: A = acc, or B = b A + c acc; each
+// tile below the diagonal is stored to its mirror too.
+struct SymArgs {
+  uint16_t *out;
+  const uint16_t *a;  // null: store acc itself
+  int64_t ld, plane, batch;
+  float b, c;
+};
+template <int P>
+struct Sym {
+  using Args = SymArgs;
+  static constexpr bool kSymmetric = true;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
+                                               const Args &e) {
+    uint16_t *out = e.out + t.batch * e.batch;
+    const uint16_t *a = e.a ? e.a + t.batch * e.batch : nullptr;
+    const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
+    const int width = (int)e.ld;
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = mr + 16 * i;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const int n = nc + 16 * j;
+        f32x4 v = acc[i][j];
+        if (a && m < t.M && n < width) {
+          const f32x4 was = load_planes<P>(a + (int64_t)m * e.ld + n, e.plane);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = fmaf(e.c, v[q], e.b * was[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (m >= t.M || n + q >= t.N) v[q] = 0;
+        bf16x4 h[P];
+        split4<P>(v, h);
+        if (m < t.M && n < width) {
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            *reinterpret_cast<bf16x4 *>(out + p * e.plane + (int64_t)m * e.ld + n) = h[p];
+        }
+        if (t.tile_m != t.tile_n && m < width) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < t.N) {
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+                reinterpret_cast<__bf16 *>(out)[p * e.plane + (int64_t)(n + q) * e.ld + m] = h[p][q];
+            }
+        }
+      }
+    }
+  }
+};
+
+// Epilogue of X <- a X + B X: planes of the next step's X, or the result in
+// its own type and orientation.
+struct NextArgs {
+  const uint16_t *x;
+  uint16_t *out;  // null after the last step
+  int64_t ld, plane, batch;
+  float a;
+  void *o;
+  int64_t ldo, batch_o;
+  int tall;
+};
+template <int P, class T>
+struct Next {
+  using Args = NextArgs;
+  static constexpr bool kSymmetric = false;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
+                                               const Args &e) {
+    const uint16_t *x = e.x + t.batch * e.batch;
+    const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
+    const int width = (int)e.ld;
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = mr + 16 * i;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const int n = nc + 16 * j;
+        if (m >= t.M || n >= width) continue;
+        f32x4 v = load_planes<P>(x + (int64_t)m * e.ld + n, e.plane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(e.a, v[q], acc[i][j][q]) : 0.0f;
+        if (e.out) {
+          bf16x4 h[P];
+          split4<P>(v, h);
+          uint16_t *to = e.out + t.batch * e.batch + (int64_t)m * e.ld + n;
+#pragma unroll
+          for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * e.plane) = h[p];
+        } else {
+          T *o = static_cast<T *>(e.o) + t.batch * e.batch_o;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < t.N) o[e.tall ? (int64_t)(n + q) * e.ldo + m : (int64_t)m * e.ldo + n + q] = (T)v[q];
+        }
+      }
+    }
+  }
+};
+
+struct Plan {
+  int r, k, planes;
+  int64_t rp, kp, x_plane, a_plane;       // leading dimensions, elements of a plane
+  int64_t x_bytes, a_bytes, norm_bytes;   // of one buffer, over the batch
+  int64_t total() const { return norm_bytes + 2 * x_bytes + 2 * a_bytes; }
+};
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
+  Plan p;
+  p.r = (int)std::min(m, n);
+  p.k = (int)std::max(m, n);
+  p.planes = type == OG_F32 ? 3 : 2;
+  p.rp = round_up(p.r, 64);
+  p.kp = round_up(p.k, 64);
+  p.x_plane = p.r * p.kp;
+  p.a_plane = p.r * p.rp;
+  p.x_bytes = round_up(batch * p.planes * p.x_plane * 2, 256);
+  p.a_bytes = round_up(batch * p.planes * p.a_plane * 2, 256);
+  p.norm_bytes = round_up(batch * kNormBlocks * 8, 256);
+  return p;
+}
+
+using T256 = Shape<256, 256, 2, 4, 2>;
+using T128 = Shape<128, 128, 2, 2, 2>;
+using T64 = Shape<64, 64, 2, 2, 4>;
+
+// The tile of a product: the largest whose blocks give every compute unit
+// work; below that the one with the least rounds x time of a block (a 256 x
+// 256 block takes 4 / 0.8 of a 128 x 128 one's time and 16 / 0.45 of a 64 x
+// 64 one's, two of which share a compute unit).
+int tile_choice(int64_t M, int64_t N, int64_t batch, bool sym) {
+  auto cost = [&](int64_t b, double t) {
+    const int64_t tm = (M + b - 1) / b, tn = (N + b - 1) / b;
+    const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
+    return (double)((n + 255) / 256) * t;
+  };
+  const double c256 = cost(256, 16), c128 = cost(128, 5), c64 = cost(64, 2.2);
+  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+}
+
+template <bool TA, bool TB, class Epi>
+void product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
+  switch (tile_choice(g.M, g.N, batch, Epi::kSymmetric)) {
+    case 256: return launch<T256, TA, TB, Epi>(g, e, batch, s);
+    case 128: return launch<T128, TA, TB, Epi>(g, e, batch, s);
+    default: return launch<T64, TA, TB, Epi>(g, e, batch, s);
+  }
+}
+
+template <class T, int P>
+void run(const Plan &p, const Input &in, int batch, int steps, float a, float b, float c, float eps,
+         void *o, int64_t ldo, int64_t stride_o, char *ws, hipStream_t s) {
+  double *norm = reinterpret_cast<double *>(ws);
+  uint16_t *x[2] = {reinterpret_cast<uint16_t *>(ws + p.norm_bytes),
+                    reinterpret_cast<uint16_t *>(ws + p.norm_bytes + p.x_bytes)};
+  uint16_t *A = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes);
+  uint16_t *B = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes + p.a_bytes);
+  const bool tall = in.m > in.n;
+  const int64_t count = (int64_t)in.m * in.n;
+  const int blocks = (int)std::min<int64_t>(kNormBlocks, (count + 2047) / 2048);
+  hipLaunchKernelGGL(norm_kernel<T>, dim3(blocks, batch), dim3(256), 0, s, in, norm);
+  const dim3 grid((unsigned)(p.kp / 64), (unsigned)(p.rp / 64), batch);
+  if (tall)
+    hipLaunchKernelGGL((pack_kernel<T, P, true>), grid, dim3(256), 0, s, in, norm, blocks, eps,
+                       x[0], p.kp, p.x_plane);
+  else
+    hipLaunchKernelGGL((pack_kernel<T, P, false>), grid, dim3(256), 0, s, in, norm, blocks, eps,
+                       x[0], p.kp, p.x_plane);
+  const int nseg = plane_products(P);
+  const int64_t xb = P * p.x_plane, ab = P * p.a_plane;
+  for (int i = 0; i < steps; ++i) {
+    uint16_t *from = x[i & 1], *to = i + 1 < steps ? x[(i + 1) & 1] : nullptr;
+    const Operand X{from, p.kp, p.x_plane, xb}, OA{A, p.rp, p.a_plane, ab}, OB{B, p.rp, p.a_plane, ab};
+    product<false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, nseg, kSegs, 0, 0},
+                                  SymArgs{A, nullptr, p.rp, p.a_plane, ab, 0, 0}, batch, s);
+    product<false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, nseg, kSegs, 0, 0},
+                                  SymArgs{B, A, p.rp, p.a_plane, ab, b, c}, batch, s);
+    product<false, true, Next<P, T>>(
+        Args{OB, X, p.r, p.k, p.r, nullptr, 0, nseg, kSegs, 0, 0},
+        NextArgs{from, to, p.kp, p.x_plane, xb, a, o, ldo, stride_o, tall}, batch, s);
+  }
+}
+
+og_status check_sizes(int64_t batch, int64_t m, int64_t n, int type) {
+  using og::host::fail;
+  if (type != OG_F32 && type != OG_BF16)
+    return fail(OG_ERR_INVALID_ARG, "type %d: newton_schulz takes OG_F32 or OG_BF16", type);
+  if (batch < 0 || m < 0 || n < 0)
+    return fail(OG_ERR_INVALID_ARG, "negative size: batch %lld, %lld x %lld", (long long)batch,
+                (long long)m, (long long)n);
+  if (m > (1 << 18) || n > (1 << 18) || batch > 65535)
+    return fail(OG_ERR_TOO_LARGE, "batch %lld of %lld x %lld: at most 65535 of 2^18 x 2^18",
+                (long long)batch, (long long)m, (long long)n);
+  return OG_OK;
+}
+
+}  // namespace og::ns
+
+extern "C" {
+
+int64_t og_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int type) {
+  const og_status st = og::ns::check_sizes(batch, m, n, type);
+  if (st != OG_OK) return st;
+  og::host::ok();
+  if (batch == 0 || m == 0 || n == 0) return 0;
+  return og::ns::plan(batch, m, n, type).total();
+}
+
+og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, int64_t ldg,
+                           int64_t strideg, int type, int steps, float a, float b, float c,
+                           float eps, void *O, int64_t ldo, int64_t strideo, void *workspace,
+                           int64_t workspace_bytes) {
+  using namespace og::host;
+  og_status st = og::ns::check_sizes(batch, m, n, type);
+  if (st != OG_OK) return st;
+  if (steps < 1 || steps > 64) return fail(OG_ERR_INVALID_ARG, "steps %d: 1 to 64", steps);
+  if (!(eps >= 0) || !std::isfinite(eps) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    return fail(OG_ERR_INVALID_ARG, "eps must be finite and not negative, a, b and c finite");
+  if (ldg < std::max<int64_t>(1, n) || ldo < std::max<int64_t>(1, n))
+    return fail(OG_ERR_INVALID_ARG, "ldg %lld or ldo %lld below n %lld", (long long)ldg,
+                (long long)ldo, (long long)n);
+  if (batch > 1 && m > 0 && (strideg < 0 || strideo < (m - 1) * ldo + n))
+    return fail(OG_ERR_INVALID_ARG, "strides %lld and %lld: inputs may repeat, outputs not overlap",
+                (long long)strideg, (long long)strideo);
+  if (batch == 0 || m == 0 || n == 0) return ok();
+  if (!G || !O) return fail(OG_ERR_INVALID_ARG, "null matrix");
+  const og::ns::Plan p = og::ns::plan(batch, m, n, type);
+  if (!workspace || workspace_bytes < p.total())
+    return fail(OG_ERR_INVALID_ARG, "workspace of %lld bytes: %lld needed",
+                (long long)(workspace ? workspace_bytes : 0), (long long)p.total());
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(OG_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if ((st = check_device()) != OG_OK) return st;
+  const og::ns::Input in{G, ldg, strideg, (int)m, (int)n};
+  if (type == OG_F32)
+    og::ns::run<float, 3>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+                          static_cast<char *>(workspace), current_stream());
+  else
+    og::ns::run<__bf16, 2>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+                           static_cast<char *>(workspace), current_stream());
+  return check_launch("newton_schulz");
+}
+
+}  // extern "C"

@@ -1,0 +1,315 @@
+// og_tile.hpp -- the bf16 matrix-core tile product the language-model
+// operators share: acc[m][n] = sum over k of A(m, k) * B(n, k), fp32 sums,
+// with the operator's own epilogue on the finished tile.
+//
+// Operands are bf16 planes.  A bf16 matrix is one plane; an fp32 matrix is
+// held as two or three planes h + m (+ l), each the rounding to bf16 of what
+// the planes before it leave (8 bits each: two planes carry 16 bits, three
+// all 24), and a product of two such matrices is the sum of the plane
+// products named in Args::segs, one after another in the same accumulators.
+// Three planes with the six products hh, hm, mh, mm, hl, lh leave out terms
+// of 2^-24 relative and below: the error of an fp32 product, at a sixth of
+// the bf16 matrix-core rate (417 TFLOP/s of the nominal peak) where the fp32
+// matrix cores have 157.
+//
+// An operand is stored with k contiguous (rows of m, "plain") or with m
+// contiguous (rows of k, "transposed"); both are loaded straight into LDS
+// (buffer_load ... lds, 16 bytes a lane) in 64-deep stages and read back as
+// matrix-core fragments: ds_read_b128 for plain ones, ds_read_b64_tr_b16
+// (which transposes 16 x 4 blocks on the way) for transposed ones.  The LDS
+// image is what the loads write, lane after lane, so the bank swizzle sits
+// in the global address each lane loads: granule g of plain row r is kept
+// in slot g ^ (r % 8); the 32-byte units of a transposed row k are permuted
+// by a hash of k so that the rows one instruction reads lie in different
+// banks.
+//
+// k beyond the operand (the tail of the last stage) is loaded from an
+// offset past the buffer's range, which the hardware returns as +0; rows
+// beyond m repeat the last one and are masked by the epilogue.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace og::tile {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr uint32_t kRange = 0xFFFFFF00u;  // range of a staging buffer, in bytes
+constexpr uint32_t kOutside = kRange;     // an offset at or past the range: the load returns +0
+constexpr int kDepth = 64;                // k of one stage
+
+// One operand: bf16 elements, ld and plane in elements.  ld is a multiple of
+// 8 and p 16-byte aligned; the elements between a row's length and the next
+// multiple of 8 are zero (plain) or readable (transposed).
+struct Operand {
+  const uint16_t *p;
+  int64_t ld;
+  int64_t plane;  // from one plane to the next
+  int64_t batch;  // from one matrix of a batch to the next
+};
+
+struct Args {
+  Operand a, b;
+  int M, N, K;
+  const int *count;  // when not null, *count (on the device, at most M or K) stands for M or K
+  int count_is_k;
+  int nseg;       // plane products
+  uint32_t segs;  // plane of A | plane of B << 2, four bits each, first product lowest
+  int tiles_m, tiles_n;
+};
+
+// Plane products by number of planes (see the top of this file).
+inline int plane_products(int planes) { return planes == 1 ? 1 : planes == 2 ? 3 : 6; }
+constexpr uint32_t kSegs = 0x0 | 0x1 << 4 | 0x4 << 8 | 0x5 << 12 | 0x2 << 16 | 0x8 << 20;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 buffer_of(const uint16_t *base) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, kRange, 0x00020000u};
+}
+// 16 bytes a lane from the buffer into LDS, lane after lane from `lds` on (a
+// uniform LDS address).  Written as asm because the compiler waits for every
+// such load in flight before any LDS read it cannot tell apart; here the
+// stages are told apart by the counted waits of the main loop.  No register
+// is written (the LDS address goes through m0, set in the same block, which
+// needs one wait state; nothing else in these kernels uses m0).
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, u32x4 rs) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(off), "s"(rs)
+               : "memory");
+}
+
+// Loads one operand's stages: BX rows of m by 64 of k.
+template <int BX, int NW, bool T>
+struct Stager {
+  static constexpr int kLoads = BX * kDepth * 2 / (NW * 1024);  // 1 KiB per wave and load
+  static constexpr int kBytes = BX * kDepth * 2;
+  static constexpr int LPR = BX / 8, RPI = 512 / BX;  // transposed: lanes per row, rows per load
+  uint32_t off[kLoads];
+  int kpos, wave;
+
+  // The unit permutation of a transposed row (32-byte units; see the top).
+  static __device__ __forceinline__ int hash(int k) {
+    return BX == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+  }
+  __device__ __forceinline__ void init(const Operand &o, int x0, int X, int w, int lane) {
+    wave = w;
+    if constexpr (!T) {
+      const int g = (lane & 7) ^ (lane >> 3);
+      kpos = g * 8;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int row = (j * NW + w) * 8 + (lane >> 3);
+        off[j] = (uint32_t)(min(row, X - 1 - x0) * (int)o.ld) * 2u + g * 16;
+      }
+    } else {
+      kpos = w * RPI + lane / LPR;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int k = j * NW * RPI + kpos;
+        const int g = (lane % LPR) ^ (hash(k) << 1);
+        off[j] = x0 + g * 8 < X ? (uint32_t)(k * (int)o.ld) * 2u + g * 16 : kOutside;
+      }
+    }
+  }
+  // base: the tile's first row (plain) or column (transposed) at stage start k0
+  __device__ __forceinline__ void issue(uint32_t lds, const uint16_t *base, int k0, int K) const {
+    const u32x4 rs = buffer_of(base);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int k = T ? j * NW * RPI + kpos : kpos;
+      const uint32_t o = k0 + k < K ? off[j] : kOutside;
+      load_to_lds(lds + (j * NW + wave) * 1024, o, rs);
+    }
+  }
+};
+
+// Reads one operand's matrix-core fragments (16 rows of m by 32 of k): lane l
+// holds row l % 16, k = 8 (l / 16) .. + 7.
+template <int BX, bool T>
+struct Reader {
+  int base;
+  // x: the wave's first row within the tile (a multiple of the wave's rows)
+  __device__ __forceinline__ void init(int x, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (!T) {
+      base = (x + i) * 128 + ((g ^ (i & 7)) * 16);
+    } else {
+      const int k = 8 * g + (i >> 2);
+      base = k * BX * 2 + (((x >> 4) ^ Stager<BX, 1, true>::hash(k)) << 5) + (i & 3) * 8;
+    }
+  }
+  // fragment `f` of the wave's rows, k half `kk` of the stage
+  __device__ __forceinline__ bf16x8 read(const char *lds, int f, int kk) const {
+    if constexpr (!T) {
+      return *reinterpret_cast<const bf16x8 *>(lds + (base ^ (kk << 6)) + f * 2048);
+    } else {
+      const int at = (base ^ (f << 5)) + kk * 32 * BX * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 8 * BX));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(bf16x8, v);
+    }
+  }
+};
+
+// Where a wave's accumulators lie: acc[i][j][e] of lane l is row
+// m0 + 16 i + l % 16 and column n0 + 16 j + 4 (l / 16) + e.
+struct Place {
+  int m0, n0;    // the wave's first row and column
+  int M, N;      // rows and columns of the product (M after Args::count)
+  int lane, wm, wn, batch;
+  int tile_m, tile_n;
+  char *lds;     // the block's stages, free once every wave has passed a barrier
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int NST_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+  static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int kStage = (BM + BN) * kDepth * 2;
+};
+
+// The block's tile: blocks go to the eight XCDs in turn, so each XCD gets a
+// run of neighbouring tiles (its L2 holds their rows), walked in bands of 8
+// tile rows; symmetric products run the tiles on and below the diagonal.
+template <bool SYM>
+__device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n) {
+  const int total = SYM ? tm * (tm + 1) / 2 : tm * tn;
+  const int x = id & 7, per = total >> 3, rem = total & 7;
+  const int t = x * per + min(x, rem) + (id >> 3);
+  if constexpr (SYM) {
+    int r = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > t) --r;
+    while ((r + 1) * (r + 2) / 2 <= t) ++r;
+    m = r;
+    n = t - r * (r + 1) / 2;
+  } else {
+    constexpr int kBand = 8;
+    const int band = t / (kBand * tn), in = t - band * kBand * tn;
+    const int rows = min(kBand, tm - band * kBand);
+    m = band * kBand + in % rows;
+    n = in / rows;
+  }
+}
+
+template <class S, bool TA, bool TB, class Epi>
+__global__ __launch_bounds__(S::NW * 64) void tile_kernel(Args g, typename Epi::Args e) {
+  __shared__ __align__(1024) char lds[S::kStage * S::NST];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tm, tn;
+  tile_of<Epi::kSymmetric>(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  int M = g.M, K = g.K;
+  if (g.count) {
+    const int c = *g.count;
+    if (g.count_is_k) K = c; else M = c;
+  }
+  const int x0 = tm * S::BM, y0 = tn * S::BN;
+  if (x0 >= M) return;
+  const int batch = blockIdx.y;
+  const uint16_t *ap = g.a.p + batch * g.a.batch + (TA ? (int64_t)x0 : x0 * g.a.ld);
+  const uint16_t *bp = g.b.p + batch * g.b.batch + (TB ? (int64_t)y0 : y0 * g.b.ld);
+
+  Stager<S::BM, S::NW, TA> sa;
+  Stager<S::BN, S::NW, TB> sb;
+  sa.init(g.a, x0, M, wave, lane);
+  sb.init(g.b, y0, g.N, wave, lane);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  Reader<S::BM, TA> ra;
+  Reader<S::BN, TB> rb;
+  ra.init(wm * S::FM * 16, lane);
+  rb.init(wn * S::FN * 16, lane);
+
+  f32x4 acc[S::FM][S::FN];
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  // stage t holds k from 64 (t / nseg), plane product t % nseg
+  const int total = (K + kDepth - 1) / kDepth * g.nseg;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds;
+  int k_next = 0, seg_next = 0, issued = 0;
+  auto issue = [&]() __attribute__((always_inline)) {
+    const uint32_t s = g.segs >> (4 * seg_next);
+    const uint32_t to = lds0 + (issued % S::NST) * S::kStage;
+    sa.issue(to, ap + (s & 3) * g.a.plane + (TA ? k_next * g.a.ld : (int64_t)k_next), k_next, K);
+    sb.issue(to + Stager<S::BM, S::NW, TA>::kBytes,
+             bp + (s >> 2 & 3) * g.b.plane + (TB ? k_next * g.b.ld : (int64_t)k_next), k_next, K);
+    if (++issued < total) {  // past the last stage its loads are repeated, so that the waits count
+      if (++seg_next == g.nseg) {
+        seg_next = 0;
+        k_next += kDepth;
+      }
+    }
+  };
+  if (total > 0) {
+#pragma unroll
+    for (int p = 0; p < S::NST - 1; ++p) issue();
+    constexpr int kPer = Stager<S::BM, S::NW, TA>::kLoads + Stager<S::BN, S::NW, TB>::kLoads;
+    for (int t = 0; t < total; ++t) {
+      // this wave's loads of stage t have landed; after the barrier every
+      // wave's have, and every wave is done reading stage t - 1
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2))
+                   : "memory");
+      issue();
+      const char *la = lds + (t % S::NST) * S::kStage;
+      const char *lb = la + Stager<S::BM, S::NW, TA>::kBytes;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        bf16x8 fa[S::FM], fb[S::FN];
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) fb[j] = rb.read(lb, j, kk);
+#pragma unroll
+        for (int i = 0; i < S::FM; ++i) fa[i] = ra.read(la, i, kk);
+#pragma unroll
+        for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < S::FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+  // the repeated loads past the last stage still write LDS: none may be in
+  // flight when the epilogue uses it or the block ends
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  Place at{x0 + wm * S::FM * 16, y0 + wn * S::FN * 16, M, g.N, lane, wm, wn, batch, tm, tn, lds};
+  Epi::template store<S>(acc, at, e);
+}
+
+template <class S, bool TA, bool TB, class Epi>
+void launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
+  g.tiles_m = (g.M + S::BM - 1) / S::BM;
+  g.tiles_n = (g.N + S::BN - 1) / S::BN;
+  const int64_t n = Epi::kSymmetric ? (int64_t)g.tiles_m * (g.tiles_m + 1) / 2
+                                    : (int64_t)g.tiles_m * g.tiles_n;
+  hipLaunchKernelGGL((tile_kernel<S, TA, TB, Epi>), dim3((unsigned)n, batches), dim3(S::NW * 64), 0,
+                     s, g, e);
+}
+
+// Planes of four fp32 values: each plane rounds what is left to bf16.  A
+// value that is not finite stays in the first plane alone.
+template <int P>
+__device__ __forceinline__ void split4(const f32x4 v, bf16x4 (&out)[P]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float r = v[e];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const __bf16 h = (__bf16)r;
+      out[p][e] = h;
+      const float d = r - (float)h;
+      r = __builtin_isfinite((float)h) ? d : 0.0f;
+    }
+  }
+}
+
+}  // namespace og::tile

@@ -277,6 +277,49 @@ int og_get_variant(void);
  */
 int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
 
+/* ------------------------------------------------------------------------
+ * Operators of language models around the N x K product (og_gemm_nt_f32's
+ * right operand: each row holds the k weights of one output).  They take
+ * fp32, bf16 or fp16 tensors as stated, sum in fp32 and run on the bf16 and
+ * fp16 matrix cores; the modes above and og_set_variant do not apply to
+ * them.  Results repeat bit for bit from run to run (no atomics).  A
+ * workspace is device memory of the caller's, 256-byte aligned, of at least
+ * the bytes its _workspace function returns; it holds nothing from one call
+ * to the next, and calls that may run at the same time (other streams,
+ * graphs replayed together) need one each.
+ * ---------------------------------------------------------------------- */
+
+#define OG_F32 0
+#define OG_BF16 1
+#define OG_F16 2
+
+/*
+ * The orthogonalised update of `batch` matrices G (m x n, row stride ldg,
+ * matrix stride strideg) by Newton-Schulz products:
+ *
+ *     X = G / (|G| + eps), |G| the Frobenius norm; transposed if m > n
+ *     `steps` times:  A = X X^T;  X <- a X + (b A + c A A) X
+ *     O = X, transposed back
+ *
+ * G and O are of `type` (OG_F32 or OG_BF16); O may be G itself with the same
+ * strides, and must not overlap it otherwise.  |G| is summed in 64 bits.
+ * The products hold X, A and b A + c A A in bf16 planes: three for OG_F32
+ * (24 bits, fp32 accuracy), two for OG_BF16 (16 bits; the result is rounded
+ * to bf16 once).  G = 0 with eps > 0 gives 0; a G that is not finite gives
+ * NaN.  The step's intermediate values must stay within fp32's range, which
+ * they do for coefficients that keep the singular values bounded.
+ * Requirements: 1 <= steps <= 64; a, b, c, eps finite, eps >= 0; ldg, ldo >=
+ * max(1, n); with batch > 1 strideg >= 0 (0: one matrix for all) and strideo
+ * >= (m-1)*ldo + n; m, n <= 2^18, batch <= 65535 (OG_ERR_TOO_LARGE); a
+ * workspace.  batch, m or n 0: nothing is done.
+ */
+og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, int64_t ldg,
+                           int64_t strideg, int type, int steps, float a, float b, float c,
+                           float eps, void *O, int64_t ldo, int64_t strideo, void *workspace,
+                           int64_t workspace_bytes);
+/* Bytes of its workspace, or a negative og_status.  Needs no device. */
+int64_t og_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int type);
+
 /* Description of the calling thread's last error ("" after a success). */
 const char *og_last_error(void);
 
