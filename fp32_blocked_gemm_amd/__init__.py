@@ -82,6 +82,14 @@ def lib() -> ctypes.CDLL:
     L.og_newton_schulz.restype = ctypes.c_int
     L.og_newton_schulz_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int]
     L.og_newton_schulz_workspace.restype = _i64
+    L.og_linear_cross_entropy.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _vp,
+                                          _i64, _vp, _vp, _vp, _i64]
+    L.og_linear_cross_entropy.restype = ctypes.c_int
+    L.og_linear_cross_entropy_grad.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, ctypes.c_int,
+                                               _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64]
+    L.og_linear_cross_entropy_grad.restype = ctypes.c_int
+    L.og_linear_cross_entropy_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int]
+    L.og_linear_cross_entropy_workspace.restype = _i64
     L.og_last_error.argtypes = []
     L.og_last_error.restype = ctypes.c_char_p
     L.og_version.argtypes = []
@@ -365,3 +373,82 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
                                       o3.data_ptr(), rows_o, o3.stride(0) if batch > 1 else 0,
                                       ws.data_ptr(), ws.numel()))
     return out
+
+
+def _vector(t, n, dtype, what):
+    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor of {n} {dtype} values")
+
+
+def _lce_shapes(X, W, target):
+    torch = _torch()
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("expected 2-D X and W")
+    n, d = X.shape
+    v, d2 = W.shape
+    if d != d2:
+        raise ValueError(f"inner sizes differ: {d} vs {d2}")
+    code = _type(X)
+    if W.dtype != X.dtype:
+        raise ValueError("X and W must have the same type")
+    _vector(target, n, torch.int64, "target")
+    return n, v, d, code
+
+
+def linear_cross_entropy_workspace(n, v, d, dtype, grad=False) -> int:
+    """Bytes linear_cross_entropy (grad: its gradient) needs, dtype F32 or BF16."""
+    b = int(lib().og_linear_cross_entropy_workspace(n, v, d, dtype, int(bool(grad))))
+    _check(min(b, 0))
+    return b
+
+
+def linear_cross_entropy(X, W, target, ignore_index=-100, loss=None, lse=None, workspace=None):
+    """(loss, lse) of each row: the softmax cross entropy of X @ W.T against target, the
+    logits never kept (og_linear_cross_entropy).  X [n, d] and W [v, d] float32 or
+    bfloat16, target [n] int64; loss and lse [n] float32."""
+    torch = _torch()
+    n, v, d, code = _lce_shapes(X, W, target)
+    loss = torch.empty(n, dtype=torch.float32, device=X.device) if loss is None else loss
+    lse = torch.empty(n, dtype=torch.float32, device=X.device) if lse is None else lse
+    _vector(loss, n, torch.float32, "loss")
+    _vector(lse, n, torch.float32, "lse")
+    dev = _one_device(X, W, target, loss, lse)
+    with torch.cuda.device(dev):
+        _use_stream_of(X)
+        ws = _workspace(int(lib().og_linear_cross_entropy_workspace(n, v, d, code, 0)), workspace,
+                        dev)
+        _check(lib().og_linear_cross_entropy(n, v, d, X.data_ptr(), _ld(X), W.data_ptr(), _ld(W),
+                                             code, target.data_ptr(), ignore_index,
+                                             loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                             ws.numel()))
+    return loss, lse
+
+
+def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=None, dW=None,
+                              need=(True, True), workspace=None):
+    """(dX, dW) of linear_cross_entropy for dloss [n] float32, from the lse it returned for
+    the same X, W and target (og_linear_cross_entropy_grad).  need: which of the two are
+    wanted; the other is None."""
+    torch = _torch()
+    n, v, d, code = _lce_shapes(X, W, target)
+    _vector(lse, n, torch.float32, "lse")
+    _vector(dloss, n, torch.float32, "dloss")
+    outs = []
+    for t, like, wanted in ((dX, X, need[0]), (dW, W, need[1])):
+        if wanted and t is None:
+            t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError("a gradient must have its tensor's shape and type")
+        outs.append(t if wanted else None)
+    given = [t for t in outs if t is not None]
+    dev = _one_device(X, W, target, lse, dloss, *given)
+    args = [p for t in outs for p in ((None, 0) if t is None else (t.data_ptr(), _ld(t)))]
+    with torch.cuda.device(dev):
+        _use_stream_of(X)
+        ws = _workspace(int(lib().og_linear_cross_entropy_workspace(n, v, d, code, 1)), workspace,
+                        dev)
+        _check(lib().og_linear_cross_entropy_grad(n, v, d, X.data_ptr(), _ld(X), W.data_ptr(),
+                                                  _ld(W), code, target.data_ptr(), ignore_index,
+                                                  lse.data_ptr(), dloss.data_ptr(), *args,
+                                                  ws.data_ptr(), ws.numel()))
+    return tuple(outs)

@@ -1,0 +1,540 @@
+// og_lce.hip -- og_linear_cross_entropy and its gradient: the softmax cross
+// entropy of the logits z = X W^T (X n x d, W v x d, a row per vocabulary
+// entry), the logits never kept.
+//
+//   lse_i = log sum_j exp z_ij,  loss_i = lse_i - z_i,t(i)
+//   g_ij = dloss_i (exp(z_ij - lse_i) - [j = t(i)]),  dX = g W,  dW = g^T X
+//
+// Rows that do not count (the ignored index) are left out before anything is
+// computed: the others are packed to the front, so that ignored rows cost
+// nothing and whatever they hold (NaN in a padded batch) reaches nothing.
+// The number of rows left stays on the device; the products read it there.
+//
+// Forward: one tile product whose epilogue keeps a running maximum and sum of
+// each row over the tile's columns; a second kernel joins the tiles.  The
+// gradient recomputes the logits in pieces of the vocabulary: g of a piece is
+// rounded to bf16 planes (one for bf16 tensors, whose rounding is that of the
+// gradients themselves; three, fp32's 24 bits, for fp32 ones) and both
+// products read it from there.  All of it is bound by the matrix cores:
+// 2 n v d operations forward, 6 n v d backward.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "og.h"
+#include "og_host.hpp"
+#include "og_tile.hpp"
+
+namespace og::lce {
+
+using namespace og::tile;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The compact list of the rows that count.
+struct Rows {
+  int *count;     // how many
+  int *pos;       // original row -> place in the list, -1 if it does not count
+  int *row;       // place -> original row
+  int *target;    // by place, as the next two
+  float *lse;
+  float *dloss;
+  float *zt;      // the target's logit (forward)
+};
+
+// One block: the rows' places by a running count, in order.  Rows that do not
+// count get their loss here (forward): 0 for the ignored index, NaN for a
+// target outside the vocabulary.
+__global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int64_t *target,
+                                                    int64_t ignore, Rows r, const float *lse_in,
+                                                    const float *dloss, float *loss, float *lse) {
+  __shared__ int waves[16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int done = 0;
+  for (int i0 = 0; i0 < n; i0 += 1024) {
+    const int i = i0 + threadIdx.x;
+    const int64_t t = i < n ? target[i] : ignore;
+    const bool counts = i < n && t != ignore && t >= 0 && t < v;
+    const uint64_t vote = __ballot(counts);
+    if (lane == 0) waves[w] = __popcll(vote);
+    __syncthreads();
+    int at = done, all = 0;
+    for (int k = 0; k < 16; ++k) {
+      if (k < w) at += waves[k];
+      all += waves[k];
+    }
+    at += __popcll(vote & ((1ull << lane) - 1));
+    if (counts) {
+      r.pos[i] = at;
+      r.row[at] = i;
+      r.target[at] = (int)t;
+      if (lse_in) {
+        r.lse[at] = lse_in[i];
+        r.dloss[at] = dloss[i];
+      }
+    } else if (i < n) {
+      r.pos[i] = -1;
+      if (loss) {
+        loss[i] = t == ignore ? 0.0f : __builtin_nanf("");
+        lse[i] = 0.0f;
+      }
+    }
+    done += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *r.count = done;
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ f32x4 load4(const T *p, int left) {
+  f32x4 v = {0, 0, 0, 0};
+  if constexpr (VEC) {
+    if (left >= 4) {
+      if constexpr (sizeof(T) == 4) {
+        v = *reinterpret_cast<const f32x4 *>(p);
+      } else {
+        const bf16x4 h = *reinterpret_cast<const bf16x4 *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+      }
+      return v;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) v[e] = (float)p[e];
+  return v;
+}
+
+// Planes of `rows` rows of `cols` values, padded with zeros to ld columns.
+// With pos, row i goes to place pos[i], and a row without a place clears its
+// row of `clear` instead (the gradient of an ignored row).
+template <class T, int P, bool VEC>
+__global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const T *x, int64_t ldx,
+                                                     const int *pos, uint16_t *out, int64_t ld,
+                                                     int64_t plane, T *clear, int64_t ldc) {
+  const int per = (int)(ld / 4);
+  const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * 256;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += step) {
+    const int i = (int)(q / per), c = (int)(q - (int64_t)i * per) * 4;
+    const int to = pos ? pos[i] : i;
+    if (to < 0) {
+      if (clear)
+        for (int e = 0; e < 4; ++e)
+          if (c + e < cols) clear[i * ldc + c + e] = (T)0.0f;
+      continue;
+    }
+    bf16x4 h[P];
+    split4<P>(load4<T, VEC>(x + i * ldx + c, cols - c), h);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      *reinterpret_cast<bf16x4 *>(out + p * plane + to * ld + c) = h[p];
+  }
+}
+
+// Epilogue of the forward product: each row's maximum over the tile's columns
+// and the sum of exp against it, and the target's logit where it lies here.
+struct LseArgs {
+  float2 *part;  // [tile column][n]
+  const int *target;
+  float *zt;
+  int n, v0, part0;  // rows of part, first column, first tile column
+};
+struct Lse {
+  using Args = LseArgs;
+  static constexpr bool kSymmetric = false;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
+                                               const Args &e) {
+    float2 *sh = reinterpret_cast<float2 *>(t.lds);  // [WN][BM]
+    const int nc = t.n0 + 4 * (t.lane >> 4);
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = t.m0 + 16 * i + (t.lane & 15);
+      const int want = m < t.M ? e.target[m] - e.v0 - nc : -1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (want == 16 * j + q) e.zt[m] = acc[i][j][q];
+          if (nc + 16 * j + q >= t.N) acc[i][j][q] = -INFINITY;
+          top = fmaxf(top, acc[i][j][q]);
+        }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float from = top == -INFINITY ? 0.0f : top;
+      float sum = 0;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          sum += __builtin_amdgcn_exp2f((acc[i][j][q] - from) * kLog2e);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (t.lane < 16) sh[t.wn * S::BM + t.wm * S::FM * 16 + 16 * i + t.lane] = {top, sum};
+    }
+    __syncthreads();
+    const int m0 = t.tile_m * S::BM;
+    for (int r = threadIdx.x; r < S::BM; r += S::NW * 64) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < S::WN; ++w) top = fmaxf(top, sh[w * S::BM + r].x);
+      const float from = top == -INFINITY ? 0.0f : top;
+      float sum = 0;
+#pragma unroll
+      for (int w = 0; w < S::WN; ++w)
+        sum += sh[w * S::BM + r].y * __builtin_amdgcn_exp2f((sh[w * S::BM + r].x - from) * kLog2e);
+      if (m0 + r < t.M) e.part[(int64_t)(e.part0 + t.tile_n) * e.n + m0 + r] = {top, sum};
+    }
+  }
+};
+
+// Joins the tiles of 8 rows per block: 32 threads a row.
+__global__ __launch_bounds__(256) void finish_kernel(Rows r, const float2 *part, int n, int tiles,
+                                                     float *loss, float *lse) {
+  __shared__ float2 sh[32][8];
+  const int m = blockIdx.x * 8 + (threadIdx.x & 7), w = threadIdx.x >> 3;
+  const int count = *r.count;
+  float top = -INFINITY, sum = 0;
+  if (m < count)
+    for (int t = w; t < tiles; t += 32) {
+      const float2 p = part[(int64_t)t * n + m];
+      const float to = fmaxf(top, p.x), from = to == -INFINITY ? 0.0f : to;
+      sum = sum * __builtin_amdgcn_exp2f((top - from) * kLog2e) +
+            p.y * __builtin_amdgcn_exp2f((p.x - from) * kLog2e);
+      top = to;
+    }
+  sh[w][threadIdx.x & 7] = {top, sum};
+  __syncthreads();
+  if (threadIdx.x >= 8 || m >= count) return;
+  top = -INFINITY;
+  for (int k = 0; k < 32; ++k) top = fmaxf(top, sh[k][threadIdx.x].x);
+  const float from = top == -INFINITY ? 0.0f : top;
+  sum = 0;
+  for (int k = 0; k < 32; ++k)
+    sum += sh[k][threadIdx.x].y * __builtin_amdgcn_exp2f((sh[k][threadIdx.x].x - from) * kLog2e);
+  const float l = top + logf(sum);
+  const int i = r.row[m];
+  lse[i] = l;
+  loss[i] = l - r.zt[m];
+}
+
+// Epilogue of the recomputed logits: g in planes, zero beyond the vocabulary.
+struct GradArgs {
+  uint16_t *g;
+  int64_t ld, plane;
+  const int *target;
+  const float *lse, *dloss;
+  int v0;
+};
+template <int P>
+struct Grad {
+  using Args = GradArgs;
+  static constexpr bool kSymmetric = false;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
+                                               const Args &e) {
+    const int nc = t.n0 + 4 * (t.lane >> 4);
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = t.m0 + 16 * i + (t.lane & 15);
+      if (m >= t.M) continue;
+      const float l = e.lse[m], d = e.dloss[m];
+      const int want = e.target[m] - e.v0 - nc;
+      uint16_t *to = e.g + m * e.ld + nc;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        if (nc + 16 * j >= e.ld) continue;
+        f32x4 v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float p = __builtin_amdgcn_exp2f((acc[i][j][q] - l) * kLog2e);
+          v[q] = nc + 16 * j + q < t.N ? (want == 16 * j + q ? p - 1.0f : p) * d : 0.0f;
+        }
+        bf16x4 h[P];
+        split4<P>(v, h);
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * e.plane + 16 * j) = h[p];
+      }
+    }
+  }
+};
+
+// Epilogue of dX and dW: the sum so far (dX, over the pieces) is kept in fp32
+// and rounded once, with the last piece.
+struct OutArgs {
+  float *sum;  // null: a single piece
+  int64_t lds;
+  int first, last;
+  void *out;
+  int64_t ldo;
+  const int *row;  // null: row m is row m of out
+};
+template <class T>
+struct Out {
+  using Args = OutArgs;
+  static constexpr bool kSymmetric = false;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
+                                               const Args &e) {
+    const int nc = t.n0 + 4 * (t.lane >> 4);
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = t.m0 + 16 * i + (t.lane & 15);
+      if (m >= t.M) continue;
+      T *to = static_cast<T *>(e.out) + (e.row ? e.row[m] : m) * e.ldo;
+      float *sum = e.sum + m * e.lds;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const int n = nc + 16 * j;
+        if (n >= t.N) continue;
+        f32x4 v = acc[i][j];
+        if (!e.first) {
+          const f32x4 was = *reinterpret_cast<const f32x4 *>(sum + n);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += was[q];
+        }
+        if (!e.last) {
+          *reinterpret_cast<f32x4 *>(sum + n) = v;
+          continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (n + q < t.N) to[n + q] = (T)v[q];
+      }
+    }
+  }
+};
+
+struct Plan {
+  int planes;
+  int64_t dp;           // d padded
+  int64_t piece;        // vocabulary rows of a piece
+  int64_t x_plane, w_plane, g_plane;
+  int64_t rows_at, x_at, w_at, part_at, g_at, sum_at, total;
+};
+
+// A piece keeps g (and the planes of its weights) at up to 2^26 values a
+// plane: large enough to fill the card with tiles (8192 columns of 4096 rows
+// are 512 of them), small enough to stay in the 256 MB last-level cache.
+Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
+  Plan p;
+  p.planes = type == OG_F32 ? 3 : 1;
+  p.dp = round_up(d, 64);
+  const int64_t most = (int64_t(1) << 25) / std::max(n, p.dp) / 256 * 256;
+  p.piece = std::min(round_up(v, 256), std::max<int64_t>(2048, most));
+  p.x_plane = n * p.dp;
+  p.w_plane = p.piece * p.dp;
+  p.g_plane = n * p.piece;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  p.rows_at = take(256 + 6 * round_up(n, 64) * 4);
+  p.x_at = take(p.planes * p.x_plane * 2);
+  p.w_at = take(p.planes * p.w_plane * 2);
+  p.part_at = grad ? at : take((round_up(v, p.piece) / 64) * n * 8);
+  p.g_at = grad ? take(p.planes * p.g_plane * 2) : at;
+  p.sum_at = grad ? take(n * p.dp * 4) : at;
+  p.total = at;
+  return p;
+}
+
+Rows rows_of(char *at, int64_t n) {
+  const int64_t s = round_up(n, 64);
+  int *p = reinterpret_cast<int *>(at + 256);
+  return Rows{reinterpret_cast<int *>(at), p, p + s, p + 2 * s, reinterpret_cast<float *>(p + 3 * s),
+              reinterpret_cast<float *>(p + 4 * s), reinterpret_cast<float *>(p + 5 * s)};
+}
+
+template <class T, int P>
+void planes(int64_t rows, int64_t cols, const T *x, int64_t ldx, const int *pos, uint16_t *out,
+            int64_t ld, int64_t plane, T *clear, int64_t ldc, hipStream_t s) {
+  const int64_t quads = rows * (ld / 4);
+  const dim3 grid((unsigned)std::min<int64_t>((quads + 255) / 256, 8192));
+  const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0;
+  if (vec)
+    hipLaunchKernelGGL((planes_kernel<T, P, true>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
+                       ldx, pos, out, ld, plane, clear, ldc);
+  else
+    hipLaunchKernelGGL((planes_kernel<T, P, false>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
+                       ldx, pos, out, ld, plane, clear, ldc);
+}
+
+struct Call {
+  int64_t n, v, d;
+  const void *x, *w;
+  int64_t ldx, ldw;
+  const int64_t *target;
+  int64_t ignore;
+  char *ws;
+};
+
+// Rows [v0, v0 + c) of W as an operand: in place where the kernels can read
+// it (bf16, whole aligned granules of 8), else its planes in the workspace.
+template <class T, int P>
+Operand weights(const Plan &p, const Call &c, int64_t v0, int64_t rows, bool in_place,
+                hipStream_t s) {
+  const T *w = static_cast<const T *>(c.w) + v0 * c.ldw;
+  if (in_place) return Operand{reinterpret_cast<const uint16_t *>(w), c.ldw, 0, 0};
+  uint16_t *to = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
+  planes<T, P>(rows, c.d, w, c.ldw, nullptr, to, p.dp, p.w_plane, nullptr, 0, s);
+  return Operand{to, p.dp, p.w_plane, 0};
+}
+template <class T>
+bool readable(const Call &c) {
+  return sizeof(T) == 2 && c.d % 8 == 0 && c.ldw % 8 == 0 &&
+         reinterpret_cast<uintptr_t>(c.w) % 16 == 0;
+}
+
+template <class T, int P>
+void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t s) {
+  const Rows r = rows_of(c.ws + p.rows_at, c.n);
+  uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
+  hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, (int)c.n, c.v, c.target, c.ignore, r,
+                     (const float *)nullptr, (const float *)nullptr, loss, lse);
+  planes<T, P>(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, p.x_plane,
+               (T *)nullptr, 0, s);
+  float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
+  const bool in_place = readable<T>(c);
+  const int64_t piece = in_place ? c.v : p.piece;
+  int tiles = 0;
+  for (int64_t v0 = 0; v0 < c.v; v0 += piece) {
+    const int rows = (int)std::min(piece, c.v - v0);
+    const Operand X{x, p.dp, p.x_plane, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
+    tiles += product<false, false, Lse>(
+        Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, plane_products(P), kSegs, 0, 0},
+        LseArgs{part, r.target, r.zt, (int)c.n, (int)v0, tiles}, 1, s);
+  }
+  hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((c.n + 7) / 8)), dim3(256), 0, s, r, part,
+                     (int)c.n, tiles, loss, lse);
+}
+
+template <class T, int P>
+void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss, T *dx,
+              int64_t lddx, T *dw, int64_t lddw, hipStream_t s) {
+  const Rows r = rows_of(c.ws + p.rows_at, c.n);
+  uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
+  uint16_t *g = reinterpret_cast<uint16_t *>(c.ws + p.g_at);
+  const int n = (int)c.n, d = (int)c.d, nseg = plane_products(P);
+  const Operand X{x, p.dp, p.x_plane, 0}, G{g, p.piece, p.g_plane, 0};
+  if (n > 0) {
+    hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, n, c.v, c.target, c.ignore, r, lse,
+                       dloss, (float *)nullptr, (float *)nullptr);
+    planes<T, P>(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, p.x_plane, dx, lddx, s);
+  }
+  const bool in_place = readable<T>(c);
+  for (int64_t v0 = 0; v0 < c.v; v0 += p.piece) {
+    const int rows = (int)std::min(p.piece, c.v - v0);
+    if (n > 0) {
+      const Operand W = weights<T, P>(p, c, v0, rows, in_place, s);
+      product<false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, nseg, kSegs, 0, 0},
+                                     GradArgs{g, p.piece, p.g_plane, r.target, r.lse, r.dloss, (int)v0},
+                                     1, s);
+      if (dx)
+        product<false, true, Out<T>>(
+            Args{G, W, n, d, rows, r.count, 0, nseg, kSegs, 0, 0},
+            OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, v0 == 0,
+                    v0 + p.piece >= c.v, dx, lddx, r.row},
+            1, s);
+    }
+    if (dw)
+      product<true, true, Out<T>>(
+          Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, nseg, kSegs, 0, 0},
+          OutArgs{nullptr, 0, 1, 1, dw + v0 * lddw, lddw, nullptr}, 1, s);
+  }
+}
+
+og_status check_sizes(int64_t n, int64_t v, int64_t d, int type) {
+  using og::host::fail;
+  if (type != OG_F32 && type != OG_BF16)
+    return fail(OG_ERR_INVALID_ARG, "type %d: linear_cross_entropy takes OG_F32 or OG_BF16", type);
+  if (n < 0 || v < 1 || d < 1)
+    return fail(OG_ERR_INVALID_ARG, "n %lld must be >= 0, v %lld and d %lld >= 1", (long long)n,
+                (long long)v, (long long)d);
+  if (n > (1 << 24) || v > (1 << 28) || d > (1 << 18))
+    return fail(OG_ERR_TOO_LARGE, "n %lld, v %lld, d %lld: at most 2^24, 2^28 and 2^18",
+                (long long)n, (long long)v, (long long)d);
+  return OG_OK;
+}
+
+og_status check(const Call &c, int type, int64_t workspace_bytes, bool grad, Plan &p) {
+  using og::host::fail;
+  if (c.ldx < c.d || c.ldw < c.d)
+    return fail(OG_ERR_INVALID_ARG, "ldx %lld or ldw %lld below d %lld", (long long)c.ldx,
+                (long long)c.ldw, (long long)c.d);
+  if (c.ldw > (1 << 22))
+    return fail(OG_ERR_TOO_LARGE, "ldw %lld: at most 2^22", (long long)c.ldw);
+  if (c.n > 0 && (!c.x || !c.w || !c.target))
+    return fail(OG_ERR_INVALID_ARG, "X, W or target is null");
+  p = plan(c.n, c.v, c.d, type, grad);
+  if (!c.ws || workspace_bytes < p.total)
+    return fail(OG_ERR_INVALID_ARG, "workspace of %lld bytes: %lld needed",
+                (long long)(c.ws ? workspace_bytes : 0), (long long)p.total);
+  if (reinterpret_cast<uintptr_t>(c.ws) % 256)
+    return fail(OG_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return OG_OK;
+}
+
+}  // namespace og::lce
+
+extern "C" {
+
+int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int type, int grad) {
+  const og_status st = og::lce::check_sizes(n, v, d, type);
+  if (st != OG_OK) return st;
+  og::host::ok();
+  return og::lce::plan(n, v, d, type, grad != 0).total;
+}
+
+og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X, int64_t ldx,
+                                  const void *W, int64_t ldw, int type, const int64_t *target,
+                                  int64_t ignore_index, float *loss, float *lse, void *workspace,
+                                  int64_t workspace_bytes) {
+  using namespace og::host;
+  og_status st = og::lce::check_sizes(n, v, d, type);
+  if (st != OG_OK) return st;
+  const og::lce::Call c{n, v, d, X, W, ldx, ldw, target, ignore_index, static_cast<char *>(workspace)};
+  og::lce::Plan p;
+  if ((st = og::lce::check(c, type, workspace_bytes, false, p)) != OG_OK) return st;
+  if (n == 0) return ok();
+  if (!loss || !lse) return fail(OG_ERR_INVALID_ARG, "loss or lse is null");
+  if ((st = check_device()) != OG_OK) return st;
+  if (type == OG_F32)
+    og::lce::forward<float, 3>(p, c, loss, lse, current_stream());
+  else
+    og::lce::forward<__bf16, 1>(p, c, loss, lse, current_stream());
+  return check_launch("linear_cross_entropy");
+}
+
+og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const void *X, int64_t ldx,
+                                       const void *W, int64_t ldw, int type, const int64_t *target,
+                                       int64_t ignore_index, const float *lse, const float *dloss,
+                                       void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                       void *workspace, int64_t workspace_bytes) {
+  using namespace og::host;
+  og_status st = og::lce::check_sizes(n, v, d, type);
+  if (st != OG_OK) return st;
+  const og::lce::Call c{n, v, d, X, W, ldx, ldw, target, ignore_index, static_cast<char *>(workspace)};
+  og::lce::Plan p;
+  if ((st = og::lce::check(c, type, workspace_bytes, true, p)) != OG_OK) return st;
+  if ((dX && lddx < d) || (dW && lddw < d))
+    return fail(OG_ERR_INVALID_ARG, "lddx %lld or lddw %lld below d %lld", (long long)lddx,
+                (long long)lddw, (long long)d);
+  if (n > 0 && (!lse || !dloss)) return fail(OG_ERR_INVALID_ARG, "lse or dloss is null");
+  if ((n == 0 && !dW) || (!dX && !dW)) return ok();
+  if ((st = check_device()) != OG_OK) return st;
+  if (type == OG_F32)
+    og::lce::gradient<float, 3>(p, c, lse, dloss, static_cast<float *>(dX), lddx,
+                                static_cast<float *>(dW), lddw, current_stream());
+  else
+    og::lce::gradient<__bf16, 1>(p, c, lse, dloss, static_cast<__bf16 *>(dX), lddx,
+                                 static_cast<__bf16 *>(dW), lddw, current_stream());
+  return check_launch("linear_cross_entropy_grad");
+}
+
+}  // extern "C"

@@ -228,8 +228,6 @@ struct Plan {
   int64_t total() const { return norm_bytes + 2 * x_bytes + 2 * a_bytes; }
 };
 
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
 Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
   Plan p;
   p.r = (int)std::min(m, n);
@@ -243,33 +241,6 @@ Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
   p.a_bytes = round_up(batch * p.planes * p.a_plane * 2, 256);
   p.norm_bytes = round_up(batch * kNormBlocks * 8, 256);
   return p;
-}
-
-using T256 = Shape<256, 256, 2, 4, 2>;
-using T128 = Shape<128, 128, 2, 2, 2>;
-using T64 = Shape<64, 64, 2, 2, 4>;
-
-// The tile of a product: the largest whose blocks give every compute unit
-// work; below that the one with the least rounds x time of a block (a 256 x
-// 256 block takes 4 / 0.8 of a 128 x 128 one's time and 16 / 0.45 of a 64 x
-// 64 one's, two of which share a compute unit).
-int tile_choice(int64_t M, int64_t N, int64_t batch, bool sym) {
-  auto cost = [&](int64_t b, double t) {
-    const int64_t tm = (M + b - 1) / b, tn = (N + b - 1) / b;
-    const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
-    return (double)((n + 255) / 256) * t;
-  };
-  const double c256 = cost(256, 16), c128 = cost(128, 5), c64 = cost(64, 2.2);
-  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
-}
-
-template <bool TA, bool TB, class Epi>
-void product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
-  switch (tile_choice(g.M, g.N, batch, Epi::kSymmetric)) {
-    case 256: return launch<T256, TA, TB, Epi>(g, e, batch, s);
-    case 128: return launch<T128, TA, TB, Epi>(g, e, batch, s);
-    default: return launch<T64, TA, TB, Epi>(g, e, batch, s);
-  }
 }
 
 template <class T, int P>

@@ -286,13 +286,44 @@ __global__ __launch_bounds__(S::NW * 64) void tile_kernel(Args g, typename Epi::
 }
 
 template <class S, bool TA, bool TB, class Epi>
-void launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
+int launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
   g.tiles_m = (g.M + S::BM - 1) / S::BM;
   g.tiles_n = (g.N + S::BN - 1) / S::BN;
   const int64_t n = Epi::kSymmetric ? (int64_t)g.tiles_m * (g.tiles_m + 1) / 2
                                     : (int64_t)g.tiles_m * g.tiles_n;
   hipLaunchKernelGGL((tile_kernel<S, TA, TB, Epi>), dim3((unsigned)n, batches), dim3(S::NW * 64), 0,
                      s, g, e);
+  return g.tiles_n;
+}
+
+inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+using T256 = Shape<256, 256, 2, 4, 2>;
+using T128 = Shape<128, 128, 2, 2, 2>;
+using T64 = Shape<64, 64, 2, 2, 4>;
+
+// The tile of a product: the largest whose blocks give every compute unit
+// work; below that the one with the least rounds x time of a block (a 256 x
+// 256 block takes 4 / 0.8 of a 128 x 128 one's time and 16 / 0.45 of a 64 x
+// 64 one's, two of which share a compute unit).
+inline int tile_choice(int64_t M, int64_t N, int64_t batch, bool sym) {
+  auto cost = [&](int64_t b, double t) {
+    const int64_t tm = (M + b - 1) / b, tn = (N + b - 1) / b;
+    const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
+    return (double)((n + 255) / 256) * t;
+  };
+  const double c256 = cost(256, 16), c128 = cost(128, 5), c64 = cost(64, 2.2);
+  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+}
+
+// Runs a product on the chosen tile; returns the number of tile columns.
+template <bool TA, bool TB, class Epi>
+int product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
+  switch (tile_choice(g.M, g.N, batch, Epi::kSymmetric)) {
+    case 256: return launch<T256, TA, TB, Epi>(g, e, batch, s);
+    case 128: return launch<T128, TA, TB, Epi>(g, e, batch, s);
+    default: return launch<T64, TA, TB, Epi>(g, e, batch, s);
+  }
 }
 
 // Planes of four fp32 values: each plane rounds what is left to bf16.  A

@@ -320,6 +320,56 @@ og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, i
 /* Bytes of its workspace, or a negative og_status.  Needs no device. */
 int64_t og_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int type);
 
+/*
+ * Softmax cross entropy of the logits z = X W^T, without keeping them: X is
+ * n x d (row stride ldx), W v x d (row stride ldw; a row per vocabulary
+ * entry), both of `type` (OG_F32 or OG_BF16), target n indices.  For row i
+ *
+ *     lse[i]  = log sum_j exp z_ij
+ *     loss[i] = lse[i] - z_i,target[i]
+ *
+ * A row whose target is ignore_index (any value, one inside [0, v) too) does
+ * not count: its loss and lse are 0 and its row of X is not used (it may hold
+ * anything).  A row whose target is neither ignore_index nor in [0, v) gets
+ * the loss NaN, the lse 0 and otherwise does not count.  The products run on
+ * the bf16 matrix cores with fp32 sums: bf16 tensors as they are, fp32 ones
+ * in three bf16 planes (24 bits; fp32 accuracy).  X and W of rows that count
+ * must be finite: a value that is not makes the results it enters NaN.
+ * Requirements: n >= 0, v, d >= 1; ldx, ldw >= d; n <= 2^24, v <= 2^28,
+ * d <= 2^18, ldw <= 2^22 (OG_ERR_TOO_LARGE); loss and lse n floats each; a
+ * workspace of og_linear_cross_entropy_workspace(n, v, d, type, 0) bytes.
+ * n == 0: nothing is done.
+ */
+og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X, int64_t ldx,
+                                  const void *W, int64_t ldw, int type, const int64_t *target,
+                                  int64_t ignore_index, float *loss, float *lse, void *workspace,
+                                  int64_t workspace_bytes);
+
+/*
+ * Its gradient for dloss, the derivative with respect to each row's loss
+ * (a mean over c rows that count: 1/c each), from the lse that the forward
+ * call gave for the same X, W and target:
+ *
+ *     g_ij = dloss[i] (exp(z_ij - lse[i]) - [j == target[i]])
+ *     dX = g W  (n x d, row stride lddx),   dW = g^T X  (v x d, lddw)
+ *
+ * both of `type`, overwritten; either may be NULL (not wanted).  The logits
+ * are recomputed in pieces of the vocabulary; g is held in one bf16 plane for
+ * OG_BF16 and in three for OG_F32, the sums over the vocabulary and over the
+ * rows in fp32, rounded once.  Rows that do not count have zero gradient
+ * whatever dloss and lse hold there, and add nothing to dW; n == 0 clears
+ * dW.  Otherwise as above, with a workspace of
+ * og_linear_cross_entropy_workspace(n, v, d, type, 1) bytes.
+ */
+og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const void *X, int64_t ldx,
+                                       const void *W, int64_t ldw, int type, const int64_t *target,
+                                       int64_t ignore_index, const float *lse, const float *dloss,
+                                       void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                       void *workspace, int64_t workspace_bytes);
+/* Bytes of the workspace, or a negative og_status; grad: 0 the forward call's,
+ * 1 the gradient's.  Needs no device. */
+int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int type, int grad);
+
 /* Description of the calling thread's last error ("" after a success). */
 const char *og_last_error(void);
 
