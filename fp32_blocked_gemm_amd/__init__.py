@@ -77,6 +77,9 @@ def lib() -> ctypes.CDLL:
     L.og_get_variant.restype = ctypes.c_int
     L.og_gemm_choice.argtypes = [_i64, _i64, _i64, ctypes.c_int]
     L.og_gemm_choice.restype = ctypes.c_int
+    L.og_gemm_nt_q4.argtypes = [_i64, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _i64, _vp,
+                                ctypes.c_int, _i64, _vp, _i64, _i64, _vp, _i64]
+    L.og_gemm_nt_q4.restype = ctypes.c_int
     L.og_newton_schulz.argtypes = ([_i64, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, ctypes.c_int]
                                    + [ctypes.c_float] * 4 + [_vp, _i64, _i64, _vp, _i64])
     L.og_newton_schulz.restype = ctypes.c_int
@@ -329,6 +332,42 @@ def _workspace(nbytes, workspace, dev):
     if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
     return workspace
+
+
+def gemm_nt_q4(A, Q, scales, zeros=None, group=128, out=None):
+    """C = A @ W.T with 4-bit weights W[j][p] = (q[j][p] - z[j][p // group]) * s[j][p // group]
+    (og_gemm_nt_q4).  A [m, k] float32, bfloat16 or float16; Q [n, ceil(k / 2)] uint8, two
+    codes a byte, the even k low; scales [n, ceil(k / group)] of any of the three types;
+    zeros the same shape, uint8, or None for 8.  C has A's type."""
+    torch = _torch()
+    if A.dim() != 2 or Q.dim() != 2:
+        raise ValueError("expected 2-D A and Q")
+    m, k = A.shape
+    n = Q.shape[0]
+    if group < 32 or group % 32:
+        raise ValueError("group must be a positive multiple of 32")
+    groups = -(-k // group)
+    every = (F32, BF16, F16)
+    code, scode = _type(A, every), _type(scales, every)
+    if Q.dtype != torch.uint8 or Q.shape[1] != (k + 1) // 2:
+        raise ValueError(f"Q must be uint8 of {(k + 1) // 2} columns for k = {k}")
+    if tuple(scales.shape) != (n, groups):
+        raise ValueError(f"scales must be [{n}, {groups}]")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+        raise ValueError("zeros must be uint8 of the scales' shape")
+    if out is None:
+        out = torch.empty((m, n), dtype=A.dtype, device=A.device)
+    if tuple(out.shape) != (m, n) or out.dtype != A.dtype:
+        raise ValueError("out must be [m, n] of A's type")
+    dev = _one_device(A, Q, scales, out, *([] if zeros is None else [zeros]))
+    with torch.cuda.device(dev):
+        _use_stream_of(out)
+        _check(lib().og_gemm_nt_q4(m, n, k, A.data_ptr(), code, _ld(A), Q.data_ptr(), _ld(Q),
+                                   scales.data_ptr(), scode, _ld(scales),
+                                   None if zeros is None else zeros.data_ptr(),
+                                   0 if zeros is None else _ld(zeros), group, out.data_ptr(),
+                                   _ld(out)))
+    return out
 
 
 def newton_schulz_workspace(batch, m, n, dtype) -> int:

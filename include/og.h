@@ -294,6 +294,36 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
 #define OG_F16 2
 
 /*
+ * Matrix product with 4-bit weights, og_gemm_nt_f32's form: for 0 <= i < m,
+ * 0 <= j < n, with t(p) = p / group,
+ *
+ *     C[i*ldc + j] = sum over p of A[i*lda + p] * (q[j][p] - z[j][t(p)]) * S[j*lds + t(p)]
+ *
+ * q[j][p] is the low (p even) or high (p odd) half of the byte
+ * Q[j*ldq + p/2], 0..15; z is the byte Z[j*ldz + t] (0..255), or 8 where Z
+ * is NULL.  The last group of a row may be short; with k odd the last byte's
+ * high half is not used.  A and C are of `type`, S of `scale_type` (OG_F32,
+ * OG_BF16 or OG_F16 each).  C is overwritten, its gaps are not.
+ *
+ * A is multiplied by the whole numbers q - z on the fp16 matrix cores with
+ * fp32 sums, 32 terms at a time; each sum is multiplied by its group's scale
+ * in fp32.  fp16 activations are exact there; bf16 and fp32 ones are taken
+ * relative to a power of two near the largest finite value of their row (of
+ * 1/16 of its k), bf16 exactly down to 2^-39 of it, fp32 to 2^-24 of each
+ * value (and 2^-39 of the largest).  Infinities and NaN act as in the
+ * formula.  The weights are read once for each 16 rows of A: it is the
+ * product of single tokens and small batches.
+ * Requirements: m, n, k >= 0; group a multiple of 32, >= 32; lda >= max(1,k),
+ * ldq >= max(1, ceil(k/2)), lds and ldz >= max(1, ceil(k/group)), ldc >=
+ * max(1,n); pointers non-null as in og_gemm_f32.  m or n 0: nothing is done;
+ * k == 0: every output is +0.  OG_ERR_TOO_LARGE when m exceeds 2^19 or n, k
+ * or group 2^30.  No workspace.
+ */
+og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *A, int type, int64_t lda,
+                        const uint8_t *Q, int64_t ldq, const void *S, int scale_type, int64_t lds,
+                        const uint8_t *Z, int64_t ldz, int64_t group, void *C, int64_t ldc);
+
+/*
  * The orthogonalised update of `batch` matrices G (m x n, row stride ldg,
  * matrix stride strideg) by Newton-Schulz products:
  *
