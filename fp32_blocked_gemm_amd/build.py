@@ -30,9 +30,11 @@ FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall",
 ]
+# not for the language-model operators: their largest tile keeps 256 accumulators a lane in
+# the accumulation registers
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 # the host pass does not know the packed-fp32 target feature; that note is harmless
 NOISE = "is not a recognized feature for this target"
 
@@ -68,11 +70,13 @@ def build(verbose: bool = False) -> str:
     before = _digest()
     os.makedirs(OBJDIR, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
-    jobs = [(src, [], os.path.join(OBJDIR, os.path.basename(src).replace(".hip", ".o")))
-            for src in [API, *OPERATORS]]
+    jobs = [(API, [], os.path.join(OBJDIR, "og_api.o"))]
+    jobs += [(src, [], os.path.join(OBJDIR, os.path.basename(src).replace(".hip", ".o")))
+             for src in OPERATORS]
     jobs += [(UNITS, [f"-DOG_UNIT={u}"], os.path.join(OBJDIR, f"og_unit{u}.o"))
              for u in range(1, N_UNITS + 1)]
-    cmds = [[HIPCC, *FLAGS, *inc, *defs, "-c", src, "-o", obj] for src, defs, obj in jobs]
+    cmds = [[HIPCC, *FLAGS, *([] if src in OPERATORS else VGPR_FORM), *inc, *defs, "-c", src, "-o",
+             obj] for src, defs, obj in jobs]
     pending, running, msgs, failed = list(cmds), [], [], []
     limit = _jobs()
     while pending or running:

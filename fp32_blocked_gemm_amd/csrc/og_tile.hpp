@@ -18,10 +18,19 @@
 // matrix-core fragments: ds_read_b128 for plain ones, ds_read_b64_tr_b16
 // (which transposes 16 x 4 blocks on the way) for transposed ones.  The LDS
 // image is what the loads write, lane after lane, so the bank swizzle sits
-// in the global address each lane loads: granule g of plain row r is kept
-// in slot g ^ (r % 8); the 32-byte units of a transposed row k are permuted
-// by a hash of k so that the rows one instruction reads lie in different
+// in the global address each lane loads: 16-byte granule g of a plain row is
+// kept in slot g ^ f(row), the 32-byte units of a transposed row k are
+// permuted by a hash of k; f and the hash put what one instruction reads in
+// one cycle (16 rows, half of them one granule further on) in different
 // banks.
+//
+// The main loop is a pipeline of three, a row of matrix instructions at a
+// time: while a row runs, the fragments of the row after next are read from
+// LDS and loads of a later stage are issued.  Each 64-deep stage has one
+// barrier, placed where its last fragments have been read: before it every
+// wave waits for those and for its own loads of the next stage (a counted
+// wait: later stages stay in flight), after it the next stage may be read and
+// this one's buffer loaded again.
 //
 // k beyond the operand (the tail of the last stage) is loaded from an
 // offset past the buffer's range, which the hardware returns as +0; rows
@@ -94,14 +103,19 @@ struct Stager {
   uint32_t off[kLoads];
   int kpos, wave;
 
-  // The unit permutation of a transposed row (32-byte units; see the top).
+  // The slot permutation of a plain row and the unit permutation of a
+  // transposed one (see the top).
+  static __device__ __forceinline__ int slots(int row) {
+    return ((row >> 1) & 1) << 2 | ((row >> 3) & 1) << 1;
+  }
   static __device__ __forceinline__ int hash(int k) {
     return BX == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
   }
   __device__ __forceinline__ void init(const Operand &o, int x0, int X, int w, int lane) {
+    static_assert(NW % 2 == 0, "a wave's rows of 8 have one parity");
     wave = w;
     if constexpr (!T) {
-      const int g = (lane & 7) ^ (lane >> 3);
+      const int g = (lane & 7) ^ slots(w * 8 + (lane >> 3));
       kpos = g * 8;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
@@ -118,15 +132,11 @@ struct Stager {
       }
     }
   }
-  // base: the tile's first row (plain) or column (transposed) at stage start k0
-  __device__ __forceinline__ void issue(uint32_t lds, const uint16_t *base, int k0, int K) const {
-    const u32x4 rs = buffer_of(base);
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int k = T ? j * NW * RPI + kpos : kpos;
-      const uint32_t o = k0 + k < K ? off[j] : kOutside;
-      load_to_lds(lds + (j * NW + wave) * 1024, o, rs);
-    }
+  // load j of a stage; rs: the tile's first row (plain) or column (transposed) at its first k,
+  // of which `left` remain
+  __device__ __forceinline__ void issue(int j, uint32_t lds, u32x4 rs, int left) const {
+    const int k = T ? j * NW * RPI + kpos : kpos;
+    load_to_lds(lds + (j * NW + wave) * 1024, k < left ? off[j] : kOutside, rs);
   }
 };
 
@@ -139,10 +149,10 @@ struct Reader {
   __device__ __forceinline__ void init(int x, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (!T) {
-      base = (x + i) * 128 + ((g ^ (i & 7)) * 16);
+      base = (x + i) * 128 + ((g ^ Stager<BX, 2, false>::slots(i)) * 16);
     } else {
       const int k = 8 * g + (i >> 2);
-      base = k * BX * 2 + (((x >> 4) ^ Stager<BX, 1, true>::hash(k)) << 5) + (i & 3) * 8;
+      base = k * BX * 2 + (((x >> 4) ^ Stager<BX, 2, true>::hash(k)) << 5) + (i & 3) * 8;
     }
   }
   // fragment `f` of the wave's rows, k half `kk` of the stage
@@ -170,9 +180,10 @@ struct Place {
   char *lds;     // the block's stages, free once every wave has passed a barrier
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int NST_>
+// BLOCKS: blocks a compute unit is to hold (the register budget).
+template <int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, BLOCKS = BLOCKS_;
   static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int kStage = (BM + BN) * kDepth * 2;
 };
@@ -201,8 +212,10 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n) 
 }
 
 template <class S, bool TA, bool TB, class Epi>
-__global__ __launch_bounds__(S::NW * 64) void tile_kernel(Args g, typename Epi::Args e) {
+__global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typename Epi::Args e) {
   __shared__ __align__(1024) char lds[S::kStage * S::NST];
+  using SA = Stager<S::BM, S::NW, TA>;
+  using SB = Stager<S::BN, S::NW, TB>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tm, tn;
@@ -218,8 +231,8 @@ __global__ __launch_bounds__(S::NW * 64) void tile_kernel(Args g, typename Epi::
   const uint16_t *ap = g.a.p + batch * g.a.batch + (TA ? (int64_t)x0 : x0 * g.a.ld);
   const uint16_t *bp = g.b.p + batch * g.b.batch + (TB ? (int64_t)y0 : y0 * g.b.ld);
 
-  Stager<S::BM, S::NW, TA> sa;
-  Stager<S::BN, S::NW, TB> sb;
+  SA sa;
+  SB sb;
   sa.init(g.a, x0, M, wave, lane);
   sb.init(g.b, y0, g.N, wave, lane);
   const int wm = wave / S::WN, wn = wave % S::WN;
@@ -234,52 +247,92 @@ __global__ __launch_bounds__(S::NW * 64) void tile_kernel(Args g, typename Epi::
 #pragma unroll
     for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // stage t holds k from 64 (t / nseg), plane product t % nseg
+  // stage t: k from 64 (t / nseg), plane product t % nseg; stages past the
+  // last load zeros
   const int total = (K + kDepth - 1) / kDepth * g.nseg;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds;
-  int k_next = 0, seg_next = 0, issued = 0;
-  auto issue = [&]() __attribute__((always_inline)) {
+  int k_next = 0, seg_next = 0, buf_next = 0;
+  u32x4 rsa, rsb;
+  uint32_t to;
+  int left;
+  auto next_stage = [&]() __attribute__((always_inline)) {
     const uint32_t s = g.segs >> (4 * seg_next);
-    const uint32_t to = lds0 + (issued % S::NST) * S::kStage;
-    sa.issue(to, ap + (s & 3) * g.a.plane + (TA ? k_next * g.a.ld : (int64_t)k_next), k_next, K);
-    sb.issue(to + Stager<S::BM, S::NW, TA>::kBytes,
-             bp + (s >> 2 & 3) * g.b.plane + (TB ? k_next * g.b.ld : (int64_t)k_next), k_next, K);
-    if (++issued < total) {  // past the last stage its loads are repeated, so that the waits count
-      if (++seg_next == g.nseg) {
-        seg_next = 0;
-        k_next += kDepth;
-      }
+    to = lds0 + buf_next * S::kStage;
+    rsa = buffer_of(ap + (s & 3) * g.a.plane + (TA ? k_next * g.a.ld : (int64_t)k_next));
+    rsb = buffer_of(bp + (s >> 2 & 3) * g.b.plane + (TB ? k_next * g.b.ld : (int64_t)k_next));
+    left = K - k_next;
+    if (++buf_next == S::NST) buf_next = 0;
+    if (++seg_next == g.nseg) {
+      seg_next = 0;
+      k_next += kDepth;
     }
   };
+  constexpr int kPer = SA::kLoads + SB::kLoads, kEarly = kPer / 2;
+  auto issue = [&](int j) __attribute__((always_inline)) {
+    if (j < SA::kLoads) sa.issue(j, to, rsa, left);
+    else sb.issue(j - SA::kLoads, to + SA::kBytes, rsb, left);
+  };
   if (total > 0) {
+    constexpr int FM = S::FM, FN = S::FN;
+    // loads of the stage NST ahead: the first kEarly right after the barrier,
+    // the others in the next stage's first rows
+    for (int p = 0; p < S::NST; ++p) {
+      next_stage();
+      for (int j = 0; j < (p + 1 < S::NST ? kPer : kEarly); ++j) issue(j);
+    }
+    bf16x8 fa[4], fb[2][FN];  // rows of A: a ring, two rows ahead; columns of B: two halves
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2) + kEarly) : "memory");
+    const char *la = lds, *lb = lds + SA::kBytes;
 #pragma unroll
-    for (int p = 0; p < S::NST - 1; ++p) issue();
-    constexpr int kPer = Stager<S::BM, S::NW, TA>::kLoads + Stager<S::BN, S::NW, TB>::kLoads;
+    for (int j = 0; j < FN; ++j) fb[0][j] = rb.read(lb, j, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) fa[i] = ra.read(la, i, 0);
+    int buf = 0;
     for (int t = 0; t < total; ++t) {
-      // this wave's loads of stage t have landed; after the barrier every
-      // wave's have, and every wave is done reading stage t - 1
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2))
-                   : "memory");
-      issue();
-      const char *la = lds + (t % S::NST) * S::kStage;
-      const char *lb = la + Stager<S::BM, S::NW, TA>::kBytes;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        bf16x8 fa[S::FM], fb[S::FN];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j) fb[j] = rb.read(lb, j, kk);
+        for (int i = 0; i < FM; ++i) {
+          // each row's reads, loads and products keep together (fences)
+          __builtin_amdgcn_sched_barrier(0);
+          const int ahead = i + 2;
+          if (h == 1 && ahead == FM) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2))
+                         : "memory");
+            if (++buf == S::NST) buf = 0;
+            la = lds + buf * S::kStage;
+            lb = la + SA::kBytes;
+            next_stage();
+          }
+          // columns of the next half: over its predecessor's rows, or after the barrier
+          if (h == 0) {
 #pragma unroll
-        for (int i = 0; i < S::FM; ++i) fa[i] = ra.read(la, i, kk);
+            for (int j = i * FN / FM; j < (i + 1) * FN / FM; ++j) fb[1][j] = rb.read(lb, j, 1);
+          } else if (ahead >= FM) {
 #pragma unroll
-        for (int i = 0; i < S::FM; ++i)
+            for (int j = (ahead - FM) * FN / 2; j < (ahead - FM + 1) * FN / 2; ++j)
+              fb[0][j] = rb.read(lb, j, 0);
+          }
+          const int slot = (h * FM + ahead) % 4;
+          if (ahead < FM) fa[slot] = ra.read(la, ahead, h);
+          else fa[slot] = ra.read(la, ahead - FM, h ^ 1);
+          if (h == 0) {
 #pragma unroll
-          for (int j = 0; j < S::FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-      }
+            for (int j = kEarly + i * kEarly * 2 / FM; j < kEarly + (i + 1) * kEarly * 2 / FM; ++j)
+              if (j < kPer) issue(j);
+          } else if (ahead >= FM) {
+#pragma unroll
+            for (int j = (ahead - FM) * kEarly / 2; j < (ahead - FM + 1) * kEarly / 2; ++j) issue(j);
+          }
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[(h * FM + i) % 4], acc[i][j], 0, 0, 0);
+        }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // the repeated loads past the last stage still write LDS: none may be in
-  // flight when the epilogue uses it or the block ends
+  // loads past the last stage still write LDS: none may be in flight when the
+  // epilogue uses it or the block ends
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   Place at{x0 + wm * S::FM * 16, y0 + wn * S::FN * 16, M, g.N, lane, wm, wn, batch, tm, tn, lds};
   Epi::template store<S>(acc, at, e);
@@ -298,9 +351,9 @@ int launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-using T256 = Shape<256, 256, 2, 4, 2>;
-using T128 = Shape<128, 128, 2, 2, 2>;
-using T64 = Shape<64, 64, 2, 2, 4>;
+using T256 = Shape<256, 256, 2, 4, 2, 1>;
+using T128 = Shape<128, 128, 2, 2, 2, 2>;
+using T64 = Shape<64, 64, 2, 2, 4, 2>;
 
 // The tile of a product: the largest whose blocks give every compute unit
 // work; below that the one with the least rounds x time of a block (a 256 x
