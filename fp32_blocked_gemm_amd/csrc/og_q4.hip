@@ -3,23 +3,21 @@
 //   C[i][j] = sum over groups t of s[j][t] * sum over p in t of A[i][p] (q[j][p] - z[j][t])
 //
 // For one to some tens of rows of A the product is bound by the bytes of the
-// codes, so the kernel is built around reading them once, in long rows, with
-// everything else on the side: a wave takes 16 weight rows, each lane 16
-// bytes (32 codes) of one of them, 128 k in all; four lane-swap instructions
-// transpose the dwords among the four lane groups so that each of the next
-// four matrix-core instructions (16 x 16 x 32, fp16) covers 32 consecutive k,
-// that is, one group of scales.  A code becomes fp16 in one operation for two
-// of them: OR-ed into the mantissa of 1024 it is 1024 + q, and subtracting
-// 1024 + z is exact, so the matrix cores multiply A by the whole numbers
-// q - z, and the group's scale multiplies the fp32 sum of its 32 k.  The
-// activations are fp16 fragments: fp16 ones as they are; bf16 ones are whole
-// in fp16 after a power of two that each wave takes from the largest of its
-// row slice (2^15 at most, so 2^-39 of it is the last bit kept); fp32 ones
-// are two such planes (22 bits and the rounding of the second, 2^-24 in all).
+// codes, so both kernels are built around asking for all of them at once, in
+// long rows (no branch lies between the loads of a piece of k: the pieces that
+// reach the end of a row have code of their own), and around few operations
+// per code.  A code becomes fp16 in one operation for two of them: OR-ed into
+// the mantissa of 1024 it is 1024 + q, and subtracting 1024 + z is exact, so A
+// is multiplied by the whole numbers q - z, and the group's scale multiplies
+// the fp32 sum of its terms (at least 32 of them).
 //
-// k is split among the waves of a block (their sums meet in LDS, in wave
-// order) so that even one 4096 x 4096 layer has sixteen waves on every
-// compute unit asking for its bytes at once.
+//  - Up to 4 rows of A: row_kernel, fp32 multiply-adds that take the fp16
+//    code as an operand.  A lane holds 32 consecutive k of A in registers and
+//    runs them against the same 32 of several weight rows.
+//  - More: block_kernel on the matrix cores, 16 weight rows x 16 rows of A.
+//    fp16 activations run against the fp16 codes; bf16 ones against the codes
+//    made bf16 (whole numbers up to 255 are); fp32 ones as three bf16 planes,
+//    24 bits.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -31,12 +29,15 @@ namespace og::q4 {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 struct Problem {
-  int m, n, k, group;   // group: a multiple of 32
+  int m, n, k;
+  int group;            // a multiple of 32
+  int shift;            // log2 of group, or -1
   const void *a;
   int64_t lda;
   const uint8_t *q;
@@ -50,59 +51,49 @@ struct Problem {
   int64_t ldc;
 };
 
-__device__ __forceinline__ float scale_at(const void *s, int type, int64_t i) {
-  if (type == OG_F32) return static_cast<const float *>(s)[i];
-  if (type == OG_BF16) return (float)static_cast<const __bf16 *>(s)[i];
-  return (float)static_cast<const _Float16 *>(s)[i];
+__device__ __forceinline__ int group_of(const Problem &p, int k) {
+  return p.shift >= 0 ? k >> p.shift : k / p.group;
 }
 
-// Eight activations of a row from k on, zero past its end.
-template <class T>
-__device__ __forceinline__ void load8(const T *row, int k, int K, float (&v)[8]) {
-  if (k + 8 <= K) {
-    T t[8];
-    __builtin_memcpy(t, row + k, sizeof t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < K ? (float)row[k + e] : 0.0f;
+// A group's scale and zero point as they lie in memory, so that nothing waits
+// for them where they are loaded, and as values.
+struct Group {
+  uint32_t s, z;
+  __device__ __forceinline__ void load(const Problem &p, int64_t n, int64_t t) {
+    const int64_t i = n * p.lds + t;
+    if (p.s_type == OG_F32) s = static_cast<const uint32_t *>(p.s)[i];
+    else s = static_cast<const uint16_t *>(p.s)[i];
+    z = p.z ? p.z[n * p.ldz + t] : 8;
   }
-}
-
-// The planes of eight activations in the order of the codes' extraction:
-// 0 4 1 5 2 6 3 7 (nibbles j and j + 4 of a dword come out together).
-template <int P>
-__device__ __forceinline__ void fragment(const float (&v)[8], float up, f16x8 (&out)[P]) {
-  constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = v[order[e]] * up;
-    const _Float16 h = (_Float16)x;
-    out[0][e] = h;
-    if constexpr (P == 2) {
-      const float d = x - (float)h;
-      out[1][e] = (_Float16)(__builtin_isfinite(x) ? d : 0.0f);
-    }
+  __device__ __forceinline__ float scale(int type) const {
+    const float h = (float)__builtin_bit_cast(_Float16, (uint16_t)s);
+    const float b = __builtin_bit_cast(float, s << 16);
+    return type == OG_F32 ? __builtin_bit_cast(float, s) : type == OG_BF16 ? b : h;
   }
-}
+  // -(1024 + z) twice
+  __device__ __forceinline__ f16x2 minus_zero() const {
+    const _Float16 h = (_Float16)(float)(-1024 - (int)z);
+    return f16x2{h, h};
+  }
+};
 
-// Two of a dword's codes (nibbles j and j + 4) as fp16, less the zero point:
-// minus_zero is -(1024 + z) twice.
+// Two of a dword's codes (nibbles J and J + 4) as fp16, less the zero point.
 template <int J>
 __device__ __forceinline__ f16x2 codes(uint32_t w, f16x2 minus_zero) {
   const uint32_t b = ((w >> (4 * J)) & 0x000F000Fu) | 0x64006400u;
   return __builtin_bit_cast(f16x2, b) + minus_zero;
 }
 
-// 32 codes of a row from k on (k a multiple of 32): whole 16-byte loads
-// inside the row, single bytes at its end, zero past it.
+// 32 codes of a row from k on (k a multiple of 32): one 16-byte load, or, FULL
+// false, single bytes up to the end of the row and zero past it.
+template <bool FULL>
 __device__ __forceinline__ u32x4 load_codes(const uint8_t *row, int k, int K) {
   u32x4 w = {0, 0, 0, 0};
-  const int at = k >> 1, bytes = (K + 1) >> 1;
-  if (at + 16 <= bytes) {
+  const int at = k >> 1;
+  if constexpr (FULL) {
     __builtin_memcpy(&w, row + at, 16);
-  } else if (at < bytes) {
+  } else {
+    const int bytes = (K + 1) >> 1;
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -112,118 +103,311 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t *row, int k, int K) {
   return w;
 }
 
-// Block: W waves, each a slice of k; NT tiles of 16 weight rows, 16 rows of A.
-template <class T, int W, int NT>
-__global__ __launch_bounds__(W * 64) void q4_kernel(Problem p) {
-  constexpr int P = sizeof(T) == 4 ? 2 : 1;
-  __shared__ float sums[W][NT * 16][17];
+template <class T>
+struct Eight {
+  T v[8];
+};
+// Eight activations of a row from k on; FULL false: zero past its end.
+template <class T, bool FULL>
+__device__ __forceinline__ Eight<T> load8(const T *row, int k, int K) {
+  Eight<T> t;
+  if constexpr (FULL) {
+    __builtin_memcpy(&t, row + k, sizeof t);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t.v[e] = k + e < K ? row[k + e] : (T)0.0f;
+  }
+  return t;
+}
+
+// Sum over the wave, in every lane.  The swaps exchange rows of 16 (then
+// halves) of two registers; given one register twice the compiler takes both
+// results for equal, so the second is a copy it cannot see through.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+  auto value = [](uint32_t x) { return __builtin_bit_cast(float, x); };
+#define OG_ROR(N) v += value(__builtin_amdgcn_mov_dpp(bits(v), 0x120 + N, 0xf, 0xf, true))
+  OG_ROR(8);
+  OG_ROR(4);
+  OG_ROR(2);
+  OG_ROR(1);
+#undef OG_ROR
+  uint32_t u = bits(v), copy = u;
+  asm volatile("" : "+v"(copy));
+  const u32x2 a = __builtin_amdgcn_permlane16_swap(u, copy, false, false);
+  u = copy = bits(value(a[0]) + value(a[1]));
+  asm volatile("" : "+v"(copy));
+  const u32x2 b = __builtin_amdgcn_permlane32_swap(u, copy, false, false);
+  return value(b[0]) + value(b[1]);
+}
+
+// 32 k of R weight rows against M rows of A.
+template <class T, int M, int R, bool FULL>
+__device__ __forceinline__ void row_piece(const Problem &p, const int64_t (&row)[R], int k,
+                                          float (&acc)[M][R]) {
+  u32x4 w[R];
+  Group gr[R];
+  Eight<T> x[M][4];
+  const int t = group_of(p, k);
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = load_codes<FULL>(p.q + row[r] * p.ldq, k, p.k);
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      x[m][d] = load8<T, FULL>(static_cast<const T *>(p.a) + m * p.lda, k + 8 * d, p.k);
+#pragma unroll
+  for (int r = 0; r < R; ++r) gr[r].load(p, row[r], t);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const f16x2 mz = gr[r].minus_zero();
+    float sum[M][2];
+#pragma unroll
+    for (int m = 0; m < M; ++m) sum[m][0] = sum[m][1] = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const f16x2 q[4] = {codes<0>(w[r][d], mz), codes<1>(w[r][d], mz), codes<2>(w[r][d], mz),
+                          codes<3>(w[r][d], mz)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          sum[m][0] = fmaf((float)q[j][0], (float)x[m][d].v[j], sum[m][0]);
+          sum[m][1] = fmaf((float)q[j][1], (float)x[m][d].v[j + 4], sum[m][1]);
+        }
+    }
+    const float s = gr[r].scale(p.s_type);
+#pragma unroll
+    for (int m = 0; m < M; ++m) acc[m][r] = fmaf(s, sum[m][0] + sum[m][1], acc[m][r]);
+  }
+}
+
+// Up to 4 rows of A.  Block: 4 waves; KS of them share R weight rows, each
+// taking every KS-th piece of 2048 k (64 lanes x 32).
+template <class T, int M, int R, int KS>
+__global__ __launch_bounds__(256) void row_kernel(Problem p) {
+  __shared__ float part[4][M * R];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = wave % KS, n0 = (blockIdx.x * (4 / KS) + wave / KS) * R;
+  float acc[M][R];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[m][r] = 0;
+  if (n0 < p.n) {
+    int64_t row[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) row[r] = min(n0 + r, p.n - 1);
+    for (int k0 = ks * 2048; k0 < p.k; k0 += KS * 2048) {
+      const int k = k0 + lane * 32;
+      if (k + 32 <= p.k) row_piece<T, M, R, true>(p, row, k, acc);
+      else if (k < p.k) row_piece<T, M, R, false>(p, row, k, acc);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float v = wave_sum(acc[m][r]);
+      if (lane == 0) part[wave][m * R + r] = v;
+    }
+  __syncthreads();
+  // (wave group, m, r) of the block's sums, the pieces of k in order
+  for (int o = threadIdx.x; o < 4 / KS * M * R; o += 256) {
+    const int group = o / (M * R), m = o % (M * R) / R, r = o % R;
+    float v = 0;
+#pragma unroll
+    for (int q = 0; q < KS; ++q) v += part[group * KS + q][m * R + r];
+    const int n = (blockIdx.x * (4 / KS) + group) * R + r;
+    if (n < p.n) static_cast<T *>(p.c)[m * p.ldc + n] = (T)v;
+  }
+}
+
+// The element type and planes of a block's fragments.
+template <class T>
+struct Planes {
+  using V = bf16x8;
+  static constexpr int P = sizeof(T) == 4 ? 3 : 1;
+  // the planes of eight activations in the order of the codes' extraction:
+  // 0 4 1 5 2 6 3 7 (nibbles j and j + 4 of a dword come out together)
+  static __device__ __forceinline__ void split(const Eight<T> &x, V (&out)[P]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int from = (e >> 1) + 4 * (e & 1);
+      if constexpr (P == 1) {
+        out[0][e] = x.v[from];
+      } else {
+        float r = x.v[from];
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          const __bf16 h = (__bf16)r;
+          out[q][e] = h;
+          r = __builtin_isfinite((float)h) ? r - (float)h : 0.0f;
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ V weights(const f16x2 (&q)[4]) {
+    V w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = (__bf16)(float)q[e >> 1][e & 1];
+    return w;
+  }
+  static __device__ __forceinline__ f32x4 mfma(V x, V w, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
+  }
+};
+template <>
+struct Planes<_Float16> {
+  using V = f16x8;
+  static constexpr int P = 1;
+  static __device__ __forceinline__ void split(const Eight<_Float16> &x, V (&out)[1]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[0][e] = x.v[(e >> 1) + 4 * (e & 1)];
+  }
+  static __device__ __forceinline__ V weights(const f16x2 (&q)[4]) {
+    return V{q[0][0], q[0][1], q[1][0], q[1][1], q[2][0], q[2][1], q[3][0], q[3][1]};
+  }
+  static __device__ __forceinline__ f32x4 mfma(V x, V w, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, c, 0, 0, 0);
+  }
+};
+
+// 128 k of a wave's operands, as loaded.
+template <class T, int MT>
+struct Chunk {
+  u32x4 w;
+  Group gr[4];
+  Eight<T> x[MT][4];
+  template <bool FULL>
+  __device__ __forceinline__ void load(const Problem &p, const T *const (&a)[MT], const bool (&in)[MT],
+                                       int64_t n, int c, int g) {
+    const int k = c * 128;
+    w = load_codes<FULL>(p.q + n * p.ldq, k + 32 * g, p.k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gr[j].load(p, n, group_of(p, min(k + 32 * j, p.k - 1)));
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (in[t]) x[t][j] = load8<T, FULL>(a[t], k + 32 * j + 8 * g, p.k);
+  }
+};
+
+// MT x 16 rows of A and 16 weight rows per block; k split among W waves (their
+// sums meet in LDS, in wave order), so that even a 4096-row layer has sixteen
+// waves on every compute unit asking for its bytes at once.  Each lane takes
+// 16 bytes (32 codes) of one weight row, 128 k in all; four lane-swap
+// instructions transpose the dwords among the four lane groups so that each of
+// the next four matrix-core instructions (16 x 16 x 32) covers 32 consecutive
+// k, that is, one group of scales.  The operands of the next 128 k are read
+// ahead.
+template <class T, int W, int MT>
+__global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
+  using Pl = Planes<T>;
+  constexpr int P = Pl::P;
+  __shared__ float sums[W][16 * MT][17];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * NT * 16, m0 = blockIdx.y * 16;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
   const int chunks = (p.k + 127) / 128;
   const int c0 = (int)((int64_t)chunks * wave / W), c1 = (int)((int64_t)chunks * (wave + 1) / W);
 
-  // lane i's row of A (fragment column) and row of W (fragment row)
-  const int m = m0 + i;
-  const bool in = m < p.m;
-  const T *arow = static_cast<const T *>(p.a) + (int64_t)min(m, p.m - 1) * p.lda;
-  int64_t nrow[NT];
+  // lane i's rows of A (fragment rows) and row of W (fragment column)
+  const T *a[MT];
+  bool in[MT];
+  Chunk<T, MT> next;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) nrow[t] = min(n0 + 16 * t + i, p.n - 1);
-
-  // the slice's power of two for each row of A
-  float up = 1, down = 1;
-  if constexpr (!__is_same(T, _Float16)) {
-    float top = 0;
-    if (in)
-      for (int k = c0 * 128 + g * 8; k < c1 * 128 && k < p.k; k += 32) {
-        float v[8];
-        load8(arow, k, p.k, v);
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + i;
+    in[t] = m < p.m;
+    a[t] = static_cast<const T *>(p.a) + (int64_t)min(m, p.m - 1) * p.lda;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f);
-      }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    // 2^e with top 2^e in [2^14, 2^15), e kept where 2^e and 2^-e are normal
-    const int e = top > 0 ? min(126, max(-126, 14 - (int)__builtin_amdgcn_frexp_expf(top) + 1)) : 0;
-    up = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-    down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) next.x[t][j].v[e] = (T)0.0f;  // what rows past m hold
   }
-
-  // acc[t][r]: weight row 16 t + i, A row m0 + 4 g + r
-  f32x4 acc[NT];
+  const int64_t n = min(n0 + i, p.n - 1);
+  auto load = [&](int c) __attribute__((always_inline)) {
+    if (c * 128 + 128 <= p.k) next.template load<true>(p, a, in, n, c, g);
+    else next.template load<false>(p, a, in, n, c, g);
+  };
+  // acc[t][r]: weight row i, A row m0 + 16 t + 4 g + r
+  f32x4 acc[MT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
 
-  u32x4 next[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-    next[t] = c0 < c1 ? load_codes(p.q + nrow[t] * p.ldq, c0 * 128 + 32 * g, p.k) : u32x4{0, 0, 0, 0};
+  if (c0 < c1) load(c0);
   for (int c = c0; c < c1; ++c) {
-    u32x4 w[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      w[t] = next[t];
-      if (c + 1 < c1) next[t] = load_codes(p.q + nrow[t] * p.ldq, (c + 1) * 128 + 32 * g, p.k);
-    }
-    f16x8 x[4][P];
+    const Chunk<T, MT> now = next;
+    if (c + 1 < c1) load(c + 1);
+    // dword d of lane group g (k 32 g + 8 d) to dword g of lane group d
+    const u32x2 s0 = __builtin_amdgcn_permlane32_swap(now.w[0], now.w[2], false, false);
+    const u32x2 s1 = __builtin_amdgcn_permlane32_swap(now.w[1], now.w[3], false, false);
+    const u32x2 lo = __builtin_amdgcn_permlane16_swap(s0[0], s1[0], false, false);
+    const u32x2 hi = __builtin_amdgcn_permlane16_swap(s0[1], s1[1], false, false);
+    const uint32_t d[4] = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (in) load8(arow, c * 128 + 32 * j + 8 * g, p.k, v);
-      fragment<P>(v, up, x[j]);
-    }
+      const f16x2 mz = now.gr[j].minus_zero();
+      const f16x2 q[4] = {codes<0>(d[j], mz), codes<1>(d[j], mz), codes<2>(d[j], mz), codes<3>(d[j], mz)};
+      const typename Pl::V w = Pl::weights(q);
+      const float s = now.gr[j].scale(p.s_type);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // dword d of lane group g (k 32 g + 8 d) to dword g of lane group d
-      const u32x2 a = __builtin_amdgcn_permlane32_swap(w[t][0], w[t][2], false, false);
-      const u32x2 b = __builtin_amdgcn_permlane32_swap(w[t][1], w[t][3], false, false);
-      const u32x2 lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-      const u32x2 hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-      const uint32_t d[4] = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = c * 128 + 32 * j;
-        const int64_t at = min(k, p.k - 1) / p.group;
-        const float s = scale_at(p.s, p.s_type, nrow[t] * p.lds + at);
-        const int z = p.z ? p.z[nrow[t] * p.ldz + at] : 8;
-        const _Float16 mz = (_Float16)(float)(-1024 - z);
-        const f16x2 zz = {mz, mz};
-        const f16x2 q0 = codes<0>(d[j], zz), q1 = codes<1>(d[j], zz), q2 = codes<2>(d[j], zz),
-                    q3 = codes<3>(d[j], zz);
-        const f16x8 q = {q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
+      for (int t = 0; t < MT; ++t) {
+        typename Pl::V x[P];
+        Pl::split(now.x[t][j], x);
         f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
-        for (int h = P - 1; h >= 0; --h)
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j][h], q, sum, 0, 0, 0);
-        // sum[r]: A row 4 g + r, weight row i
+        for (int h = P - 1; h >= 0; --h) sum = Pl::mfma(x[h], w, sum);
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(s, sum[r], acc[t][r]);
       }
     }
   }
-  // the rows' powers of two are held by lanes 0..15: row 4 g + r's by lane 4 g + r
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float d = __shfl(down, 4 * g + r);
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sums[wave][16 * t + i][4 * g + r] = acc[t][r] * d;
-  }
+    for (int r = 0; r < 4; ++r) sums[wave][16 * t + 4 * g + r][i] = acc[t][r];
   __syncthreads();
-  for (int o = threadIdx.x; o < NT * 256; o += W * 64) {
-    const int row = o / (NT * 16), col = o % (NT * 16);
+  for (int o = threadIdx.x; o < MT * 256; o += W * 64) {
+    const int row = o >> 4, col = o & 15;
     float v = 0;
-    for (int w = 0; w < W; ++w) v += sums[w][col][row];
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += sums[w][row][col];
     if (m0 + row < p.m && n0 + col < p.n)
       static_cast<T *>(p.c)[(int64_t)(m0 + row) * p.ldc + n0 + col] = (T)v;
   }
 }
 
+template <class T, int M, int R>
+void run_rows(const Problem &p, hipStream_t s) {
+  const int groups = (p.n + R - 1) / R;
+  const int pieces = (p.k + 2047) / 2048;
+  const int ks = pieces >= 4 ? 4 : pieces >= 2 ? 2 : 1;
+  const dim3 block(256);
+  if (ks == 4)
+    hipLaunchKernelGGL((row_kernel<T, M, R, 4>), dim3(groups), block, 0, s, p);
+  else if (ks == 2)
+    hipLaunchKernelGGL((row_kernel<T, M, R, 2>), dim3((groups + 1) / 2), block, 0, s, p);
+  else
+    hipLaunchKernelGGL((row_kernel<T, M, R, 1>), dim3((groups + 3) / 4), block, 0, s, p);
+}
+
+template <class T, int W, int MT>
+void run_blocks(const Problem &p, hipStream_t s) {
+  hipLaunchKernelGGL((block_kernel<T, W, MT>), dim3((p.n + 15) / 16, (p.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(W * 64), 0, s, p);
+}
+
 template <class T>
 void run(const Problem &p, hipStream_t s) {
-  const unsigned my = (unsigned)((p.m + 15) / 16);
-  const int tiles = (p.n + 15) / 16;
-  hipLaunchKernelGGL((q4_kernel<T, 16, 1>), dim3(tiles, my), dim3(1024), 0, s, p);
+  if (p.m == 1) return run_rows<T, 1, 4>(p, s);
+  if (p.m == 2) return run_rows<T, 2, 4>(p, s);
+  if (p.m == 3) return run_rows<T, 3, 4>(p, s);
+  if (p.m == 4) return run_rows<T, 4, 4>(p, s);
+  if (p.m <= 16) return run_blocks<T, 16, 1>(p, s);
+  return run_blocks<T, 8, 2>(p, s);
 }
 
 }  // namespace og::q4
@@ -255,7 +439,9 @@ extern "C" og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *
   if (!C || (k > 0 && (!A || !Q || !S))) return fail(OG_ERR_INVALID_ARG, "a null pointer");
   og_status st = check_device();
   if (st != OG_OK) return st;
-  const og::q4::Problem p{(int)m, (int)n, (int)k, (int)group, A, lda, Q, ldq, S, scale_type, lds,
+  const bool whole = (group & (group - 1)) == 0;
+  const og::q4::Problem p{(int)m, (int)n, (int)k, (int)group,
+                          whole ? __builtin_ctzll((unsigned long long)group) : -1, A, lda, Q, ldq, S, scale_type, lds,
                           Z, ldz, C, ldc};
   if (type == OG_F32) og::q4::run<float>(p, current_stream());
   else if (type == OG_BF16) og::q4::run<__bf16>(p, current_stream());

@@ -305,13 +305,10 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
  * high half is not used.  A and C are of `type`, S of `scale_type` (OG_F32,
  * OG_BF16 or OG_F16 each).  C is overwritten, its gaps are not.
  *
- * A is multiplied by the whole numbers q - z on the fp16 matrix cores with
- * fp32 sums, 32 terms at a time; each sum is multiplied by its group's scale
- * in fp32.  fp16 activations are exact there; bf16 and fp32 ones are taken
- * relative to a power of two near the largest finite value of their row (of
- * 1/16 of its k), bf16 exactly down to 2^-39 of it, fp32 to 2^-24 of each
- * value (and 2^-39 of the largest).  Infinities and NaN act as in the
- * formula.  The weights are read once for each 16 rows of A: it is the
+ * A is multiplied by the whole numbers q - z with fp32 sums (of fp16 and bf16
+ * activations exactly, of fp32 ones to 24 bits); each sum of at least 32 terms
+ * is multiplied by its group's scale in fp32.  Infinities and NaN act as in
+ * the formula.  The weights are read once for each 32 rows of A: it is the
  * product of single tokens and small batches.
  * Requirements: m, n, k >= 0; group a multiple of 32, >= 32; lda >= max(1,k),
  * ldq >= max(1, ceil(k/2)), lds and ldz >= max(1, ceil(k/group)), ldc >=

@@ -24,21 +24,17 @@ def q4_weights(q, scales, zeros, k, group):
 
 
 def q4(a, q, scales, zeros, group):
-    """(exact, bound).  A term passes at most 64 additions of two 32-term matrix products,
-    one per 32 k of its wave's slice, the 16 waves' and the products with its scale and power
-    of two; bf16 and fp32 activations lose 2^-39 of their row's largest value (last bit of a
-    subnormal fp16, the row scaled to at least 2^14), fp32 ones also 2^-22 of each (two fp16
-    roundings of 2^-11 each)."""
+    """(exact, bound).  A term passes at most 96 additions of three 32-term matrix products,
+    one per 32 k of its wave's slice, the 16 waves' and the product with its scale; three bf16
+    planes of an fp32 activation leave out 2^-24 of it."""
     k = a.shape[1]
     w = q4_weights(q, scales, zeros, k, group)
     a64 = a.to(F64)
     exact = a64 @ w.t()
     size = a64.abs() @ w.abs().t()
-    e = (64 + k / 32 + 16 + 4) * ADD * size
-    if a.dtype != torch.float16:
-        e = e + 2.0 ** -39 * a64.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    e = (96 + k / 32 + 16 + 2) * ADD * size
     if a.dtype == torch.float32:
-        e = e + 2.0 ** -22 * size
+        e = e + 2.0 ** -24 * size
     return exact, e + half_step(a.dtype) * (exact.abs() + e) + torch.finfo(a.dtype).tiny
 
 
