@@ -107,14 +107,14 @@ __device__ __forceinline__ f32x4 load4(const T *p, int left) {
   return v;
 }
 
-// Planes of `rows` rows of `cols` values, padded with zeros to ld columns.
+// Planes of `rows` rows of `cols` values, padded with zeros to ld / P columns.
 // With pos, row i goes to place pos[i], and a row without a place clears its
 // row of `clear` instead (the gradient of an ignored row).
 template <class T, int P, bool VEC>
 __global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const T *x, int64_t ldx,
                                                      const int *pos, uint16_t *out, int64_t ld,
-                                                     int64_t plane, T *clear, int64_t ldc) {
-  const int per = (int)(ld / 4);
+                                                     T *clear, int64_t ldc) {
+  const int per = (int)(ld / (4 * P));
   const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * 256;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += step) {
     const int i = (int)(q / per), c = (int)(q - (int64_t)i * per) * 4;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const T
     split4<P>(load4<T, VEC>(x + i * ldx + c, cols - c), h);
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      *reinterpret_cast<bf16x4 *>(out + p * plane + to * ld + c) = h[p];
+      *reinterpret_cast<bf16x4 *>(out + to * ld + column<P>(c, p)) = h[p];
   }
 }
 
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void finish_kernel(Rows r, const float2 *part,
 // Epilogue of the recomputed logits: g in planes, zero beyond the vocabulary.
 struct GradArgs {
   uint16_t *g;
-  int64_t ld, plane;
+  int64_t ld;
   const int *target;
   const float *lse, *dloss;
   int v0;
@@ -243,10 +243,10 @@ struct Grad {
       if (m >= t.M) continue;
       const float l = e.lse[m], d = e.dloss[m];
       const int want = e.target[m] - e.v0 - nc;
-      uint16_t *to = e.g + m * e.ld + nc;
+      uint16_t *to = e.g + m * e.ld;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
-        if (nc + 16 * j >= e.ld) continue;
+        if (nc + 16 * j >= e.ld / P) continue;
         f32x4 v;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -256,7 +256,7 @@ struct Grad {
         bf16x4 h[P];
         split4<P>(v, h);
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * e.plane + 16 * j) = h[p];
+        for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(nc + 16 * j, p)) = h[p];
       }
     }
   }
@@ -312,7 +312,6 @@ struct Plan {
   int planes;
   int64_t dp;           // d padded
   int64_t piece;        // vocabulary rows of a piece
-  int64_t x_plane, w_plane, g_plane;
   int64_t rows_at, x_at, w_at, part_at, g_at, sum_at, total;
 };
 
@@ -325,9 +324,6 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   p.dp = round_up(d, 64);
   const int64_t most = (int64_t(1) << 25) / std::max(n, p.dp) / 256 * 256;
   p.piece = std::min(round_up(v, 256), std::max<int64_t>(2048, most));
-  p.x_plane = n * p.dp;
-  p.w_plane = p.piece * p.dp;
-  p.g_plane = n * p.piece;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -335,10 +331,10 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
     return here;
   };
   p.rows_at = take(256 + 6 * round_up(n, 64) * 4);
-  p.x_at = take(p.planes * p.x_plane * 2);
-  p.w_at = take(p.planes * p.w_plane * 2);
+  p.x_at = take(p.planes * n * p.dp * 2);
+  p.w_at = take(p.planes * p.piece * p.dp * 2);
   p.part_at = grad ? at : take((round_up(v, p.piece) / 64) * n * 8);
-  p.g_at = grad ? take(p.planes * p.g_plane * 2) : at;
+  p.g_at = grad ? take(p.planes * n * p.piece * 2) : at;
   p.sum_at = grad ? take(n * p.dp * 4) : at;
   p.total = at;
   return p;
@@ -353,16 +349,16 @@ Rows rows_of(char *at, int64_t n) {
 
 template <class T, int P>
 void planes(int64_t rows, int64_t cols, const T *x, int64_t ldx, const int *pos, uint16_t *out,
-            int64_t ld, int64_t plane, T *clear, int64_t ldc, hipStream_t s) {
-  const int64_t quads = rows * (ld / 4);
+            int64_t ld, T *clear, int64_t ldc, hipStream_t s) {
+  const int64_t quads = rows * (ld / (4 * P));
   const dim3 grid((unsigned)std::min<int64_t>((quads + 255) / 256, 8192));
   const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0;
   if (vec)
     hipLaunchKernelGGL((planes_kernel<T, P, true>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
-                       ldx, pos, out, ld, plane, clear, ldc);
+                       ldx, pos, out, ld, clear, ldc);
   else
     hipLaunchKernelGGL((planes_kernel<T, P, false>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
-                       ldx, pos, out, ld, plane, clear, ldc);
+                       ldx, pos, out, ld, clear, ldc);
 }
 
 struct Call {
@@ -380,10 +376,10 @@ template <class T, int P>
 Operand weights(const Plan &p, const Call &c, int64_t v0, int64_t rows, bool in_place,
                 hipStream_t s) {
   const T *w = static_cast<const T *>(c.w) + v0 * c.ldw;
-  if (in_place) return Operand{reinterpret_cast<const uint16_t *>(w), c.ldw, 0, 0};
+  if (in_place) return Operand{reinterpret_cast<const uint16_t *>(w), c.ldw, 0};
   uint16_t *to = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
-  planes<T, P>(rows, c.d, w, c.ldw, nullptr, to, p.dp, p.w_plane, nullptr, 0, s);
-  return Operand{to, p.dp, p.w_plane, 0};
+  planes<T, P>(rows, c.d, w, c.ldw, nullptr, to, P * p.dp, nullptr, 0, s);
+  return Operand{to, P * p.dp, 0};
 }
 template <class T>
 bool readable(const Call &c) {
@@ -397,7 +393,7 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
   uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, (int)c.n, c.v, c.target, c.ignore, r,
                      (const float *)nullptr, (const float *)nullptr, loss, lse);
-  planes<T, P>(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, p.x_plane,
+  planes<T, P>(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, P * p.dp,
                (T *)nullptr, 0, s);
   float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
   const bool in_place = readable<T>(c);
@@ -405,9 +401,9 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
   int tiles = 0;
   for (int64_t v0 = 0; v0 < c.v; v0 += piece) {
     const int rows = (int)std::min(piece, c.v - v0);
-    const Operand X{x, p.dp, p.x_plane, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
-    tiles += product<false, false, Lse>(
-        Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, plane_products(P), kSegs, 0, 0},
+    const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
+    tiles += product<P, false, false, Lse>(
+        Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, 0, 0},
         LseArgs{part, r.target, r.zt, (int)c.n, (int)v0, tiles}, 1, s);
   }
   hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((c.n + 7) / 8)), dim3(256), 0, s, r, part,
@@ -420,31 +416,31 @@ void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss
   const Rows r = rows_of(c.ws + p.rows_at, c.n);
   uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
   uint16_t *g = reinterpret_cast<uint16_t *>(c.ws + p.g_at);
-  const int n = (int)c.n, d = (int)c.d, nseg = plane_products(P);
-  const Operand X{x, p.dp, p.x_plane, 0}, G{g, p.piece, p.g_plane, 0};
+  const int n = (int)c.n, d = (int)c.d;
+  const Operand X{x, P * p.dp, 0}, G{g, P * p.piece, 0};
   if (n > 0) {
     hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, n, c.v, c.target, c.ignore, r, lse,
                        dloss, (float *)nullptr, (float *)nullptr);
-    planes<T, P>(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, p.x_plane, dx, lddx, s);
+    planes<T, P>(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, P * p.dp, dx, lddx, s);
   }
   const bool in_place = readable<T>(c);
   for (int64_t v0 = 0; v0 < c.v; v0 += p.piece) {
     const int rows = (int)std::min(p.piece, c.v - v0);
     if (n > 0) {
       const Operand W = weights<T, P>(p, c, v0, rows, in_place, s);
-      product<false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, nseg, kSegs, 0, 0},
-                                     GradArgs{g, p.piece, p.g_plane, r.target, r.lse, r.dloss, (int)v0},
-                                     1, s);
+      product<P, false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, 0, 0},
+                                        GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, (int)v0},
+                                        1, s);
       if (dx)
-        product<false, true, Out<T>>(
-            Args{G, W, n, d, rows, r.count, 0, nseg, kSegs, 0, 0},
+        product<P, false, true, Out<T>>(
+            Args{G, W, n, d, rows, r.count, 0, 0, 0},
             OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, v0 == 0,
                     v0 + p.piece >= c.v, dx, lddx, r.row},
             1, s);
     }
     if (dw)
-      product<true, true, Out<T>>(
-          Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, nseg, kSegs, 0, 0},
+      product<P, true, true, Out<T>>(
+          Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, 0, 0},
           OutArgs{nullptr, 0, 1, 1, dw + v0 * lddw, lddw, nullptr}, 1, s);
   }
 }

@@ -67,8 +67,7 @@ __global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
 // whichever way X lies), padded with zeros to ld columns.
 template <class T, int P, bool TALL>
 __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part, int blocks,
-                                                   float eps, uint16_t *x, int64_t ld,
-                                                   int64_t plane) {
+                                                   float eps, uint16_t *x, int64_t ld) {
   __shared__ float tile[64][65];
   __shared__ float factor;
   const int batch = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
@@ -100,18 +99,18 @@ __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part,
     for (int e = 0; e < 4; ++e) v[e] = tile[i][j + e] * f;
     bf16x4 out[P];
     split4<P>(v, out);
-    uint16_t *to = x + batch * P * plane + (int64_t)(r0 + i) * ld + c0 + j;
+    uint16_t *to = x + (batch * (int64_t)R + r0 + i) * ld;
 #pragma unroll
-    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * plane) = out[p];
+    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(c0 + j, p)) = out[p];
   }
 }
 
 template <int P>
-__device__ __forceinline__ f32x4 load_planes(const uint16_t *p, int64_t plane) {
+__device__ __forceinline__ f32x4 load_planes(const uint16_t *row, int c) {
   f32x4 v = {0, 0, 0, 0};
 #pragma unroll
   for (int q = P - 1; q >= 0; --q) {
-    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(p + q * plane);
+    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(row + column<P>(c, q));
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += (float)h[e];
   }
@@ -123,7 +122,7 @@ __device__ __forceinline__ f32x4 load_planes(const uint16_t *p, int64_t plane) {
 struct SymArgs {
   uint16_t *out;
   const uint16_t *a;  // null: store acc itself
-  int64_t ld, plane, batch;
+  int64_t ld, batch;
   float b, c;
 };
 template <int P>
@@ -136,7 +135,7 @@ struct Sym {
     uint16_t *out = e.out + t.batch * e.batch;
     const uint16_t *a = e.a ? e.a + t.batch * e.batch : nullptr;
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
-    const int width = (int)e.ld;
+    const int width = (int)(e.ld / P);
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
@@ -145,7 +144,7 @@ struct Sym {
         const int n = nc + 16 * j;
         f32x4 v = acc[i][j];
         if (a && m < t.M && n < width) {
-          const f32x4 was = load_planes<P>(a + (int64_t)m * e.ld + n, e.plane);
+          const f32x4 was = load_planes<P>(a + (int64_t)m * e.ld, n);
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = fmaf(e.c, v[q], e.b * was[q]);
         }
@@ -157,7 +156,7 @@ struct Sym {
         if (m < t.M && n < width) {
 #pragma unroll
           for (int p = 0; p < P; ++p)
-            *reinterpret_cast<bf16x4 *>(out + p * e.plane + (int64_t)m * e.ld + n) = h[p];
+            *reinterpret_cast<bf16x4 *>(out + (int64_t)m * e.ld + column<P>(n, p)) = h[p];
         }
         if (t.tile_m != t.tile_n && m < width) {
 #pragma unroll
@@ -165,7 +164,7 @@ struct Sym {
             if (n + q < t.N) {
 #pragma unroll
               for (int p = 0; p < P; ++p)
-                reinterpret_cast<__bf16 *>(out)[p * e.plane + (int64_t)(n + q) * e.ld + m] = h[p][q];
+                reinterpret_cast<__bf16 *>(out)[(int64_t)(n + q) * e.ld + column<P>(m, p)] = h[p][q];
             }
         }
       }
@@ -178,7 +177,7 @@ struct Sym {
 struct NextArgs {
   const uint16_t *x;
   uint16_t *out;  // null after the last step
-  int64_t ld, plane, batch;
+  int64_t ld, batch;
   float a;
   void *o;
   int64_t ldo, batch_o;
@@ -193,7 +192,7 @@ struct Next {
                                                const Args &e) {
     const uint16_t *x = e.x + t.batch * e.batch;
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
-    const int width = (int)e.ld;
+    const int width = (int)(e.ld / P);
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
@@ -201,15 +200,15 @@ struct Next {
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
         if (m >= t.M || n >= width) continue;
-        f32x4 v = load_planes<P>(x + (int64_t)m * e.ld + n, e.plane);
+        f32x4 v = load_planes<P>(x + (int64_t)m * e.ld, n);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(e.a, v[q], acc[i][j][q]) : 0.0f;
         if (e.out) {
           bf16x4 h[P];
           split4<P>(v, h);
-          uint16_t *to = e.out + t.batch * e.batch + (int64_t)m * e.ld + n;
+          uint16_t *to = e.out + t.batch * e.batch + (int64_t)m * e.ld;
 #pragma unroll
-          for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + p * e.plane) = h[p];
+          for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(n, p)) = h[p];
         } else {
           T *o = static_cast<T *>(e.o) + t.batch * e.batch_o;
 #pragma unroll
@@ -223,7 +222,7 @@ struct Next {
 
 struct Plan {
   int r, k, planes;
-  int64_t rp, kp, x_plane, a_plane;       // leading dimensions, elements of a plane
+  int64_t rp, kp;                         // r and k padded to blocks of 64
   int64_t x_bytes, a_bytes, norm_bytes;   // of one buffer, over the batch
   int64_t total() const { return norm_bytes + 2 * x_bytes + 2 * a_bytes; }
 };
@@ -235,10 +234,8 @@ Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
   p.planes = type == OG_F32 ? 3 : 2;
   p.rp = round_up(p.r, 64);
   p.kp = round_up(p.k, 64);
-  p.x_plane = p.r * p.kp;
-  p.a_plane = p.r * p.rp;
-  p.x_bytes = round_up(batch * p.planes * p.x_plane * 2, 256);
-  p.a_bytes = round_up(batch * p.planes * p.a_plane * 2, 256);
+  p.x_bytes = round_up(batch * p.planes * p.r * p.kp * 2, 256);
+  p.a_bytes = round_up(batch * p.planes * p.r * p.rp * 2, 256);
   p.norm_bytes = round_up(batch * kNormBlocks * 8, 256);
   return p;
 }
@@ -258,22 +255,21 @@ void run(const Plan &p, const Input &in, int batch, int steps, float a, float b,
   const dim3 grid((unsigned)(p.kp / 64), (unsigned)(p.rp / 64), batch);
   if (tall)
     hipLaunchKernelGGL((pack_kernel<T, P, true>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       x[0], p.kp, p.x_plane);
+                       x[0], P * p.kp);
   else
     hipLaunchKernelGGL((pack_kernel<T, P, false>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       x[0], p.kp, p.x_plane);
-  const int nseg = plane_products(P);
-  const int64_t xb = P * p.x_plane, ab = P * p.a_plane;
+                       x[0], P * p.kp);
+  const int64_t ldx = P * p.kp, lda = P * p.rp, xb = p.r * ldx, ab = p.r * lda;
   for (int i = 0; i < steps; ++i) {
     uint16_t *from = x[i & 1], *to = i + 1 < steps ? x[(i + 1) & 1] : nullptr;
-    const Operand X{from, p.kp, p.x_plane, xb}, OA{A, p.rp, p.a_plane, ab}, OB{B, p.rp, p.a_plane, ab};
-    product<false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, nseg, kSegs, 0, 0},
-                                  SymArgs{A, nullptr, p.rp, p.a_plane, ab, 0, 0}, batch, s);
-    product<false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, nseg, kSegs, 0, 0},
-                                  SymArgs{B, A, p.rp, p.a_plane, ab, b, c}, batch, s);
-    product<false, true, Next<P, T>>(
-        Args{OB, X, p.r, p.k, p.r, nullptr, 0, nseg, kSegs, 0, 0},
-        NextArgs{from, to, p.kp, p.x_plane, xb, a, o, ldo, stride_o, tall}, batch, s);
+    const Operand X{from, ldx, xb}, OA{A, lda, ab}, OB{B, lda, ab};
+    product<P, false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0},
+                                     SymArgs{A, nullptr, lda, ab, 0, 0}, batch, s);
+    product<P, false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0},
+                                     SymArgs{B, A, lda, ab, b, c}, batch, s);
+    product<P, false, true, Next<P, T>>(Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0},
+                                        NextArgs{from, to, ldx, xb, a, o, ldo, stride_o, tall},
+                                        batch, s);
   }
 }
 

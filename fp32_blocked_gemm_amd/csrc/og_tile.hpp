@@ -6,31 +6,33 @@
 // held as two or three planes h + m (+ l), each the rounding to bf16 of what
 // the planes before it leave (8 bits each: two planes carry 16 bits, three
 // all 24), and a product of two such matrices is the sum of the plane
-// products named in Args::segs, one after another in the same accumulators.
-// Three planes with the six products hh, hm, mh, mm, hl, lh leave out terms
-// of 2^-24 relative and below: the error of an fp32 product, at a sixth of
-// the bf16 matrix-core rate (417 TFLOP/s of the nominal peak) where the fp32
-// matrix cores have 157.
+// products hh, hm, mh (two planes) and mm, hl, lh too (three), in the same
+// accumulators.  Three planes leave out terms of 2^-24 relative and below:
+// the error of an fp32 product, at a sixth of the bf16 matrix-core rate (417
+// TFLOP/s of the nominal peak) where the fp32 matrix cores have 157.  Planes
+// are interleaved by blocks of 32 columns: element (r, c) of plane p of P lies
+// at r ld + 32 (P (c / 32) + p) + c % 32, so that a stage's k of one row is
+// one run in memory, whatever P.
 //
 // An operand is stored with k contiguous (rows of m, "plain") or with m
 // contiguous (rows of k, "transposed"); both are loaded straight into LDS
-// (buffer_load ... lds, 16 bytes a lane) in 64-deep stages and read back as
-// matrix-core fragments: ds_read_b128 for plain ones, ds_read_b64_tr_b16
-// (which transposes 16 x 4 blocks on the way) for transposed ones.  The LDS
-// image is what the loads write, lane after lane, so the bank swizzle sits
-// in the global address each lane loads: 16-byte granule g of a plain row is
-// kept in slot g ^ f(row), the 32-byte units of a transposed row k are
-// permuted by a hash of k; f and the hash put what one instruction reads in
-// one cycle (16 rows, half of them one granule further on) in different
-// banks.
+// (buffer_load ... lds, 16 bytes a lane) in stages of 64 k (one plane) or 32 k
+// (all planes) and read back as matrix-core fragments: ds_read_b128 for plain
+// ones, ds_read_b64_tr_b16 (which transposes 16 x 4 blocks on the way) for
+// transposed ones.  The LDS image is what the loads write, lane after lane, so
+// the bank swizzle sits in the global address each lane loads: 16-byte granule
+// g of a plain row is kept in slot g ^ f(row), the 32-byte units of a
+// transposed row k are permuted by a hash of k; f and the hash put what one
+// instruction reads in one cycle (16 rows, half of them one granule further
+// on) in different banks.
 //
 // The main loop is a pipeline of three, a row of matrix instructions at a
-// time: while a row runs, the fragments of the row after next are read from
-// LDS and loads of a later stage are issued.  Each 64-deep stage has one
-// barrier, placed where its last fragments have been read: before it every
-// wave waits for those and for its own loads of the next stage (a counted
-// wait: later stages stay in flight), after it the next stage may be read and
-// this one's buffer loaded again.
+// time: while a row runs, the fragments of a row ahead are read from LDS and
+// loads of a later stage are issued.  Each stage has one barrier, placed where
+// its last fragments have been read: before it every wave waits for those and
+// for its own loads of the next stage (a counted wait: later stages stay in
+// flight), after it the next stage may be read and this one's buffer loaded
+// again.
 //
 // k beyond the operand (the tail of the last stage) is loaded from an
 // offset past the buffer's range, which the hardware returns as +0; rows
@@ -51,15 +53,17 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr uint32_t kRange = 0xFFFFFF00u;  // range of a staging buffer, in bytes
 constexpr uint32_t kOutside = kRange;     // an offset at or past the range: the load returns +0
-constexpr int kDepth = 64;                // k of one stage
 
-// One operand: bf16 elements, ld and plane in elements.  ld is a multiple of
-// 8 and p 16-byte aligned; the elements between a row's length and the next
-// multiple of 8 are zero (plain) or readable (transposed).
+// k of one stage.
+constexpr int depth(int planes) { return planes == 1 ? 64 : 32; }
+
+// One operand: bf16 elements, ld and batch in elements.  ld is a multiple of 8
+// and p 16-byte aligned; the elements between a row's length and the next
+// multiple of 8 are zero (plain) or readable (transposed).  Planes: rows of
+// whole blocks of 32.
 struct Operand {
   const uint16_t *p;
   int64_t ld;
-  int64_t plane;  // from one plane to the next
   int64_t batch;  // from one matrix of a batch to the next
 };
 
@@ -68,14 +72,18 @@ struct Args {
   int M, N, K;
   const int *count;  // when not null, *count (on the device, at most M or K) stands for M or K
   int count_is_k;
-  int nseg;       // plane products
-  uint32_t segs;  // plane of A | plane of B << 2, four bits each, first product lowest
   int tiles_m, tiles_n;
 };
 
-// Plane products by number of planes (see the top of this file).
-inline int plane_products(int planes) { return planes == 1 ? 1 : planes == 2 ? 3 : 6; }
-constexpr uint32_t kSegs = 0x0 | 0x1 << 4 | 0x4 << 8 | 0x5 << 12 | 0x2 << 16 | 0x8 << 20;
+// Where column c of plane p lies in a row of P planes.
+template <int P>
+__device__ __forceinline__ int64_t column(int c, int p) {
+  return P == 1 ? c : (int64_t)(c >> 5) * (32 * P) + p * 32 + (c & 31);
+}
+
+// The plane products: product i is of plane kPlaneA[i] of A and kPlaneB[i] of B.
+constexpr int plane_products(int planes) { return planes == 1 ? 1 : planes == 2 ? 3 : 6; }
+constexpr int kPlaneA[6] = {0, 0, 1, 1, 0, 2}, kPlaneB[6] = {0, 1, 0, 1, 2, 0};
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 buffer_of(const uint16_t *base) {
@@ -94,75 +102,82 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, u32x4 rs
                : "memory");
 }
 
-// Loads one operand's stages: BX rows of m by 64 of k.
-template <int BX, int NW, bool T>
-struct Stager {
-  static constexpr int kLoads = BX * kDepth * 2 / (NW * 1024);  // 1 KiB per wave and load
-  static constexpr int kBytes = BX * kDepth * 2;
-  static constexpr int LPR = BX / 8, RPI = 512 / BX;  // transposed: lanes per row, rows per load
-  uint32_t off[kLoads];
-  int kpos, wave;
+// The swizzles (see the top): the slot permutation of a plain row, and the
+// unit permutation of row k of BX transposed columns.
+template <int P>
+__device__ __forceinline__ int slots(int row) {
+  return P == 3 ? ((row >> 3) & 1) << 1 : ((row >> 1) & 1) << 2 | ((row >> 3) & 1) << 1;
+}
+template <int BX, int P>
+__device__ __forceinline__ int hash(int k) {
+  // rows that are not a multiple of 256 bytes alternate between the bank halves by themselves
+  return BX * P * 2 % 256 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+}
 
-  // The slot permutation of a plain row and the unit permutation of a
-  // transposed one (see the top).
-  static __device__ __forceinline__ int slots(int row) {
-    return ((row >> 1) & 1) << 2 | ((row >> 3) & 1) << 1;
-  }
-  static __device__ __forceinline__ int hash(int k) {
-    return BX == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
-  }
+// Loads one operand's stages: BX rows of m by depth(P) of k, P planes.
+template <int BX, int NW, bool T, int P>
+struct Stager {
+  static constexpr int kBytes = BX * depth(P) * P * 2;
+  static constexpr int kLoads = kBytes / (NW * 1024);  // 1 KiB per wave and load
+  static_assert(kLoads * NW * 1024 == kBytes, "whole loads");
+  // 16-byte granules of a row of LDS
+  static constexpr int kRow = T ? BX * P / 8 : P == 1 ? 8 : 4 * P;
+  uint32_t off[kLoads];
+  int kpos[kLoads];  // the k of the stage that a load's lane brings
+  int wave;
+
   __device__ __forceinline__ void init(const Operand &o, int x0, int X, int w, int lane) {
-    static_assert(NW % 2 == 0, "a wave's rows of 8 have one parity");
     wave = w;
-    if constexpr (!T) {
-      const int g = (lane & 7) ^ slots(w * 8 + (lane >> 3));
-      kpos = g * 8;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int row = (j * NW + w) * 8 + (lane >> 3);
+    for (int j = 0; j < kLoads; ++j) {
+      const int at = (j * NW + w) * 64 + lane, row = at / kRow, s = at % kRow;
+      if constexpr (!T) {
+        const int g = P == 3 ? (s & ~3) | ((s & 3) ^ slots<P>(row)) : s ^ slots<P>(row);
+        kpos[j] = (P == 1 ? g : g & 3) * 8;
         off[j] = (uint32_t)(min(row, X - 1 - x0) * (int)o.ld) * 2u + g * 16;
-      }
-    } else {
-      kpos = w * RPI + lane / LPR;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int k = j * NW * RPI + kpos;
-        const int g = (lane % LPR) ^ (hash(k) << 1);
-        off[j] = x0 + g * 8 < X ? (uint32_t)(k * (int)o.ld) * 2u + g * 16 : kOutside;
+      } else {
+        const int u = (s >> 1) ^ hash<BX, P>(row);  // 16 columns of one plane
+        const int c = P == 1 ? u * 16 + (s & 1) * 8 : u / (2 * P) * 32;
+        kpos[j] = row;
+        off[j] = x0 + c < X ? (uint32_t)(row * (int)o.ld) * 2u + u * 32 + (s & 1) * 16 : kOutside;
       }
     }
   }
   // load j of a stage; rs: the tile's first row (plain) or column (transposed) at its first k,
   // of which `left` remain
   __device__ __forceinline__ void issue(int j, uint32_t lds, u32x4 rs, int left) const {
-    const int k = T ? j * NW * RPI + kpos : kpos;
-    load_to_lds(lds + (j * NW + wave) * 1024, k < left ? off[j] : kOutside, rs);
+    load_to_lds(lds + (j * NW + wave) * 1024, kpos[j] < left ? off[j] : kOutside, rs);
   }
 };
 
 // Reads one operand's matrix-core fragments (16 rows of m by 32 of k): lane l
 // holds row l % 16, k = 8 (l / 16) .. + 7.
-template <int BX, bool T>
+template <int BX, bool T, int P>
 struct Reader {
-  int base;
+  int base, swz, unit;
   // x: the wave's first row within the tile (a multiple of the wave's rows)
   __device__ __forceinline__ void init(int x, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (!T) {
-      base = (x + i) * 128 + ((g ^ Stager<BX, 2, false>::slots(i)) * 16);
+      base = (x + i) * (P == 3 ? 192 : 128) + ((g ^ slots<P>(i)) * 16);
     } else {
       const int k = 8 * g + (i >> 2);
-      base = k * BX * 2 + (((x >> 4) ^ Stager<BX, 2, true>::hash(k)) << 5) + (i & 3) * 8;
+      base = k * BX * P * 2 + (i & 3) * 8;
+      swz = hash<BX, P>(k) << 5;
+      unit = (x >> 4) * P;  // x / 32 blocks of 2 P units
     }
   }
-  // fragment `f` of the wave's rows, k half `kk` of the stage
-  __device__ __forceinline__ bf16x8 read(const char *lds, int f, int kk) const {
+  // fragment `f` (even + odd pairs make blocks of 32) of the wave's rows; b: the k half of the
+  // stage (one plane) or the plane
+  __device__ __forceinline__ bf16x8 read(const char *lds, int f, int b) const {
     if constexpr (!T) {
-      return *reinterpret_cast<const bf16x8 *>(lds + (base ^ (kk << 6)) + f * 2048);
+      const int at = P == 3 ? base + b * 64 : base ^ (b << 6);
+      return *reinterpret_cast<const bf16x8 *>(lds + at + f * (P == 3 ? 3072 : 2048));
     } else {
-      const int at = (base ^ (f << 5)) + kk * 32 * BX * 2;
+      const int u = unit + (P == 1 ? f : (f >> 1) * 2 * P + b * 2 + (f & 1));
+      const int at = base + ((u << 5) ^ swz) + (P == 1 ? b * 32 * BX * 2 : 0);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 8 * BX));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 8 * BX * P));
       typedef short s16x8 __attribute__((ext_vector_type(8)));
       const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(bf16x8, v);
@@ -180,12 +195,13 @@ struct Place {
   char *lds;     // the block's stages, free once every wave has passed a barrier
 };
 
-// BLOCKS: blocks a compute unit is to hold (the register budget).
-template <int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
+// A tile of BM x BN by WM x WN waves, NST stages of P planes in LDS; BLOCKS: blocks a compute
+// unit is to hold (the register budget).
+template <int P_, int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, BLOCKS = BLOCKS_;
+  static constexpr int P = P_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, BLOCKS = BLOCKS_;
   static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
-  static constexpr int kStage = (BM + BN) * kDepth * 2;
+  static constexpr int kStage = (BM + BN) * depth(P) * P * 2;
 };
 
 // The block's tile: blocks go to the eight XCDs in turn, so each XCD gets a
@@ -213,9 +229,10 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n) 
 
 template <class S, bool TA, bool TB, class Epi>
 __global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typename Epi::Args e) {
+  constexpr int P = S::P, FM = S::FM, FN = S::FN, kDepth = depth(P);
   __shared__ __align__(1024) char lds[S::kStage * S::NST];
-  using SA = Stager<S::BM, S::NW, TA>;
-  using SB = Stager<S::BN, S::NW, TB>;
+  using SA = Stager<S::BM, S::NW, TA, P>;
+  using SB = Stager<S::BN, S::NW, TB, P>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tm, tn;
@@ -228,113 +245,149 @@ __global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typ
   const int x0 = tm * S::BM, y0 = tn * S::BN;
   if (x0 >= M) return;
   const int batch = blockIdx.y;
-  const uint16_t *ap = g.a.p + batch * g.a.batch + (TA ? (int64_t)x0 : x0 * g.a.ld);
-  const uint16_t *bp = g.b.p + batch * g.b.batch + (TB ? (int64_t)y0 : y0 * g.b.ld);
+  const uint16_t *ap = g.a.p + batch * g.a.batch + (TA ? (int64_t)x0 * P : x0 * g.a.ld);
+  const uint16_t *bp = g.b.p + batch * g.b.batch + (TB ? (int64_t)y0 * P : y0 * g.b.ld);
 
   SA sa;
   SB sb;
   sa.init(g.a, x0, M, wave, lane);
   sb.init(g.b, y0, g.N, wave, lane);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  Reader<S::BM, TA> ra;
-  Reader<S::BN, TB> rb;
-  ra.init(wm * S::FM * 16, lane);
-  rb.init(wn * S::FN * 16, lane);
+  Reader<S::BM, TA, P> ra;
+  Reader<S::BN, TB, P> rb;
+  ra.init(wm * FM * 16, lane);
+  rb.init(wn * FN * 16, lane);
 
-  f32x4 acc[S::FM][S::FN];
+  f32x4 acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < S::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // stage t: k from 64 (t / nseg), plane product t % nseg; stages past the
-  // last load zeros
-  const int total = (K + kDepth - 1) / kDepth * g.nseg;
+  // stages past the last load zeros
+  const int total = (K + kDepth - 1) / kDepth;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds;
-  int k_next = 0, seg_next = 0, buf_next = 0;
+  int k_next = 0, buf_next = 0;
   u32x4 rsa, rsb;
   uint32_t to;
   int left;
   auto next_stage = [&]() __attribute__((always_inline)) {
-    const uint32_t s = g.segs >> (4 * seg_next);
     to = lds0 + buf_next * S::kStage;
-    rsa = buffer_of(ap + (s & 3) * g.a.plane + (TA ? k_next * g.a.ld : (int64_t)k_next));
-    rsb = buffer_of(bp + (s >> 2 & 3) * g.b.plane + (TB ? k_next * g.b.ld : (int64_t)k_next));
+    rsa = buffer_of(ap + (TA ? k_next * g.a.ld : (int64_t)k_next * P));
+    rsb = buffer_of(bp + (TB ? k_next * g.b.ld : (int64_t)k_next * P));
     left = K - k_next;
     if (++buf_next == S::NST) buf_next = 0;
-    if (++seg_next == g.nseg) {
-      seg_next = 0;
-      k_next += kDepth;
-    }
+    k_next += kDepth;
   };
-  constexpr int kPer = SA::kLoads + SB::kLoads, kEarly = kPer / 2;
+  // A row's reads run kAhead rows before its products.  The loads of the stage
+  // NST ahead: kRate a row, from right after the barrier on.
+  constexpr int kAhead = P == 1 ? 2 : 1;
+  constexpr int kPer = SA::kLoads + SB::kLoads;
+  constexpr int kRate = P == 1 ? kPer / 4 : (kPer + FM / 2 - 1) / (FM / 2);
+  constexpr int kEarly = kPer < kRate * kAhead ? kPer : kRate * kAhead;
   auto issue = [&](int j) __attribute__((always_inline)) {
     if (j < SA::kLoads) sa.issue(j, to, rsa, left);
     else sb.issue(j - SA::kLoads, to + SA::kBytes, rsb, left);
   };
   if (total > 0) {
-    constexpr int FM = S::FM, FN = S::FN;
-    // loads of the stage NST ahead: the first kEarly right after the barrier,
-    // the others in the next stage's first rows
     for (int p = 0; p < S::NST; ++p) {
       next_stage();
-      for (int j = 0; j < (p + 1 < S::NST ? kPer : kEarly); ++j) issue(j);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (p + 1 < S::NST || j < kEarly) issue(j);
     }
-    bf16x8 fa[4], fb[2][FN];  // rows of A: a ring, two rows ahead; columns of B: two halves
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2) + kEarly) : "memory");
     const char *la = lds, *lb = lds + SA::kBytes;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fb[0][j] = rb.read(lb, j, 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) fa[i] = ra.read(la, i, 0);
     int buf = 0;
-    for (int t = 0; t < total; ++t) {
+    auto meet = [&]() __attribute__((always_inline)) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2)) : "memory");
+      if (++buf == S::NST) buf = 0;
+      la = lds + buf * S::kStage;
+      lb = la + SA::kBytes;
+      next_stage();
+    };
+    if constexpr (P == 1) {
+      bf16x8 fa[4], fb[2][FN];  // rows of A: a ring; columns of B: two halves
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < FN; ++j) fb[0][j] = rb.read(lb, j, 0);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          // each row's reads, loads and products keep together (fences)
-          __builtin_amdgcn_sched_barrier(0);
-          const int ahead = i + 2;
-          if (h == 1 && ahead == FM) {
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(kPer * (S::NST - 2))
-                         : "memory");
-            if (++buf == S::NST) buf = 0;
-            la = lds + buf * S::kStage;
-            lb = la + SA::kBytes;
-            next_stage();
+      for (int i = 0; i < 2; ++i) fa[i] = ra.read(la, i, 0);
+      for (int t = 0; t < total; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            // each row's reads, loads and products keep together (fences)
+            __builtin_amdgcn_sched_barrier(0);
+            const int ahead = i + kAhead, slot = (h * FM + ahead) % 4;
+            if (h == 1 && ahead == FM) meet();
+            // columns of the next half: over its predecessor's rows, or after the barrier
+            if (h == 0) {
+#pragma unroll
+              for (int j = i * FN / FM; j < (i + 1) * FN / FM; ++j) fb[1][j] = rb.read(lb, j, 1);
+            } else if (ahead >= FM) {
+#pragma unroll
+              for (int j = (ahead - FM) * FN / 2; j < (ahead - FM + 1) * FN / 2; ++j)
+                fb[0][j] = rb.read(lb, j, 0);
+            }
+            if (ahead < FM) fa[slot] = ra.read(la, ahead, h);
+            else fa[slot] = ra.read(la, ahead - FM, h ^ 1);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              if (h == 0 && j >= kEarly + i * kRate && j < kEarly + (i + 1) * kRate) issue(j);
+              if (h == 1 && ahead >= FM && j >= (ahead - FM) * kRate && j < (ahead - FM + 1) * kRate) issue(j);
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[(h * FM + i) % 4], acc[i][j], 0, 0, 0);
           }
-          // columns of the next half: over its predecessor's rows, or after the barrier
-          if (h == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      bf16x8 fa[2][P], fb[2][FN][P];  // rows of A in turn; columns of B by stage
 #pragma unroll
-            for (int j = i * FN / FM; j < (i + 1) * FN / FM; ++j) fb[1][j] = rb.read(lb, j, 1);
-          } else if (ahead >= FM) {
+      for (int p = 0; p < P; ++p) {
 #pragma unroll
-            for (int j = (ahead - FM) * FN / 2; j < (ahead - FM + 1) * FN / 2; ++j)
-              fb[0][j] = rb.read(lb, j, 0);
+        for (int j = 0; j < FN; ++j) fb[0][j][p] = rb.read(lb, j, p);
+        fa[0][p] = ra.read(la, 0, p);
+      }
+      for (int t = 0; t < total; t += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + 1 == FM) meet();
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              if (i + 1 < FM) fa[(i + 1) & 1][p] = ra.read(la, i + 1, p);
+              else fa[(i + 1) & 1][p] = ra.read(la, 0, p);
+            }
+            if (i + 1 == FM) {
+#pragma unroll
+              for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int p = 0; p < P; ++p) fb[h ^ 1][j][p] = rb.read(lb, j, p);
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              if (i + 1 < FM && j >= kEarly + i * kRate && j < kEarly + (i + 1) * kRate) issue(j);
+              if (i + 1 == FM && j < kEarly) issue(j);
+            }
+#pragma unroll
+            for (int q = 0; q < plane_products(P); ++q)
+#pragma unroll
+              for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j][kPlaneB[q]], fa[i & 1][kPlaneA[q]], acc[i][j], 0, 0, 0);
           }
-          const int slot = (h * FM + ahead) % 4;
-          if (ahead < FM) fa[slot] = ra.read(la, ahead, h);
-          else fa[slot] = ra.read(la, ahead - FM, h ^ 1);
-          if (h == 0) {
-#pragma unroll
-            for (int j = kEarly + i * kEarly * 2 / FM; j < kEarly + (i + 1) * kEarly * 2 / FM; ++j)
-              if (j < kPer) issue(j);
-          } else if (ahead >= FM) {
-#pragma unroll
-            for (int j = (ahead - FM) * kEarly / 2; j < (ahead - FM + 1) * kEarly / 2; ++j) issue(j);
-          }
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[(h * FM + i) % 4], acc[i][j], 0, 0, 0);
-        }
-      __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
   // loads past the last stage still write LDS: none may be in flight when the
   // epilogue uses it or the block ends
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  Place at{x0 + wm * S::FM * 16, y0 + wn * S::FN * 16, M, g.N, lane, wm, wn, batch, tm, tn, lds};
+  Place at{x0 + wm * FM * 16, y0 + wn * FN * 16, M, g.N, lane, wm, wn, batch, tm, tn, lds};
   Epi::template store<S>(acc, at, e);
 }
 
@@ -351,32 +404,47 @@ int launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-using T256 = Shape<256, 256, 2, 4, 2, 1>;
-using T128 = Shape<128, 128, 2, 2, 2, 2>;
-using T64 = Shape<64, 64, 2, 2, 4, 2>;
+// The tiles, by planes: large, middle, small.
+template <int P, bool SYM>
+struct Tiles {
+  using L = Shape<P, 256, 256, 2, 4, 2, 1>;
+  using M = Shape<P, 128, 128, 2, 2, 2, 2>;
+  using S = Shape<P, 64, 64, 2, 2, 4, 2>;
+};
+template <bool SYM>
+struct Tiles<2, SYM> {
+  using L = Shape<2, 256, 256, 2, 4, 2, 1>;
+  using M = Shape<2, 128, 128, 2, 4, 2, 2>;
+  using S = Shape<2, 64, 64, 2, 2, 4, 2>;
+};
+template <bool SYM>
+struct Tiles<3, SYM> {
+  using L = Shape<3, 128, SYM ? 128 : 256, 2, 4, SYM ? 3 : 2, 1>;  // symmetric: square tiles
+  using M = Shape<3, 128, 128, 2, 4, 3, 1>;
+  using S = Shape<3, 64, 64, 2, 2, 3, 2>;
+};
 
 // The tile of a product: the largest whose blocks give every compute unit
 // work; below that the one with the least rounds x time of a block (a 256 x
 // 256 block takes 4 / 0.8 of a 128 x 128 one's time and 16 / 0.45 of a 64 x
 // 64 one's, two of which share a compute unit).
-inline int tile_choice(int64_t M, int64_t N, int64_t batch, bool sym) {
-  auto cost = [&](int64_t b, double t) {
-    const int64_t tm = (M + b - 1) / b, tn = (N + b - 1) / b;
-    const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
-    return (double)((n + 255) / 256) * t;
-  };
-  const double c256 = cost(256, 16), c128 = cost(128, 5), c64 = cost(64, 2.2);
-  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+template <class S, bool SYM>
+double rounds(int64_t M, int64_t N, int64_t batch, double per_value) {
+  const int64_t tm = (M + S::BM - 1) / S::BM, tn = (N + S::BN - 1) / S::BN;
+  const int64_t n = (SYM ? tm * (tm + 1) / 2 : tm * tn) * batch;
+  return (double)((n + 255) / 256) * (S::BM * S::BN) * per_value;
 }
 
 // Runs a product on the chosen tile; returns the number of tile columns.
-template <bool TA, bool TB, class Epi>
+template <int P, bool TA, bool TB, class Epi>
 int product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
-  switch (tile_choice(g.M, g.N, batch, Epi::kSymmetric)) {
-    case 256: return launch<T256, TA, TB, Epi>(g, e, batch, s);
-    case 128: return launch<T128, TA, TB, Epi>(g, e, batch, s);
-    default: return launch<T64, TA, TB, Epi>(g, e, batch, s);
-  }
+  using T = Tiles<P, Epi::kSymmetric>;
+  const double l = rounds<typename T::L, Epi::kSymmetric>(g.M, g.N, batch, 1.0);
+  const double m = rounds<typename T::M, Epi::kSymmetric>(g.M, g.N, batch, 1.25);
+  const double c = rounds<typename T::S, Epi::kSymmetric>(g.M, g.N, batch, 2.2);
+  if (l <= m && l <= c) return launch<typename T::L, TA, TB, Epi>(g, e, batch, s);
+  if (m <= c) return launch<typename T::M, TA, TB, Epi>(g, e, batch, s);
+  return launch<typename T::S, TA, TB, Epi>(g, e, batch, s);
 }
 
 // Planes of four fp32 values: each plane rounds what is left to bf16.  A
