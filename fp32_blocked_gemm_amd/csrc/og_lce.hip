@@ -262,11 +262,13 @@ struct Grad {
   }
 };
 
-// Epilogue of dX and dW: the sum so far (dX, over the pieces) is kept in fp32
-// and rounded once, with the last piece.
+// Epilogue of dX and dW.  The sum so far (dX, over the pieces) is kept in fp32
+// and rounded once, with the last piece; a product whose k is split stores its
+// parts for join_kernel.
 struct OutArgs {
-  float *sum;  // null: a single piece
+  float *sum;    // the sum over pieces, or the parts; not used by a single piece
   int64_t lds;
+  int64_t part;  // from one part to the next; 0: not split
   int first, last;
   void *out;
   int64_t ldo;
@@ -285,7 +287,7 @@ struct Out {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
       T *to = static_cast<T *>(e.out) + (e.row ? e.row[m] : m) * e.ldo;
-      float *sum = e.sum + m * e.lds;
+      float *sum = e.sum + t.batch * e.part + m * e.lds;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
@@ -308,12 +310,52 @@ struct Out {
   }
 };
 
+// Adds the parts of a split product in order, the sum of the pieces before it
+// first; the result goes where Out would store it.
+template <class T>
+__global__ __launch_bounds__(256) void join_kernel(int rows, int cols, const int *count, int parts,
+                                                   const float *from, int64_t part, float *sum,
+                                                   int64_t lds, int first, int last, T *out,
+                                                   int64_t ldo, const int *row) {
+  const int per = (cols + 3) / 4;
+  if (count) rows = *count;
+  const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * 256;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += step) {
+    const int m = (int)(at / per), n = (int)(at - (int64_t)m * per) * 4;
+    f32x4 v = {0, 0, 0, 0};
+    if (!first) v = *reinterpret_cast<const f32x4 *>(sum + m * lds + n);
+    for (int p = 0; p < parts; ++p) {
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(from + p * part + m * lds + n);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += w[q];
+    }
+    if (!last) {
+      *reinterpret_cast<f32x4 *>(sum + m * lds + n) = v;
+      continue;
+    }
+    T *to = out + (row ? row[m] : m) * ldo;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < cols) to[n + q] = (T)v[q];
+  }
+}
+
 struct Plan {
   int planes;
   int64_t dp;           // d padded
   int64_t piece;        // vocabulary rows of a piece
-  int64_t rows_at, x_at, w_at, part_at, g_at, sum_at, total;
+  int dx_parts, dw_parts;  // parts of k of a piece's gradient products
+  int64_t rows_at, x_at, w_at, part_at, g_at, sum_at, parts_at, total;
 };
+
+// Parts of k of an m x n product: as many as make up two tiles of 64 x 64 for
+// each compute unit, of at least 512 k each (one part costs its own fp32 copy
+// of the result and a pass that adds the copies: 1000 x 384 over 8191 took 107
+// us whole, 48 in eight parts).
+int parts_of(int64_t m, int64_t n, int64_t k) {
+  const int64_t tiles = std::max<int64_t>(1, (m + 63) / 64 * ((n + 63) / 64));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, k / 512, 16}));
+}
 
 // A piece keeps g (and the planes of its weights) at up to 2^26 values a
 // plane: large enough to fill the card with tiles (8192 columns of 4096 rows
@@ -333,9 +375,15 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   p.rows_at = take(256 + 6 * round_up(n, 64) * 4);
   p.x_at = take(p.planes * n * p.dp * 2);
   p.w_at = take(p.planes * p.piece * p.dp * 2);
-  p.part_at = grad ? at : take((round_up(v, p.piece) / 64) * n * 8);
+  p.part_at = grad ? at : take((round_up(v, p.piece) / 32) * n * 8);
   p.g_at = grad ? take(p.planes * n * p.piece * 2) : at;
   p.sum_at = grad ? take(n * p.dp * 4) : at;
+  const int64_t piece = std::min(p.piece, v);
+  p.dx_parts = parts_of(n, d, piece);
+  p.dw_parts = parts_of(piece, d, n);
+  p.parts_at = grad ? take(std::max(p.dx_parts > 1 ? p.dx_parts * n : 0,
+                                    p.dw_parts > 1 ? p.dw_parts * piece : 0) * p.dp * 4)
+                    : at;
   p.total = at;
   return p;
 }
@@ -403,11 +451,29 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
     const int rows = (int)std::min(piece, c.v - v0);
     const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
     tiles += product<P, false, false, Lse>(
-        Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, 0, 0},
+        Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, 0, 0, 0},
         LseArgs{part, r.target, r.zt, (int)c.n, (int)v0, tiles}, 1, s);
   }
   hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((c.n + 7) / 8)), dim3(256), 0, s, r, part,
                      (int)c.n, tiles, loss, lse);
+}
+
+// A product with Out's epilogue, its k in `parts` parts (each a multiple of
+// the stages' depth; `room` rows of a part have their place in the workspace).
+template <class T, int P, bool TA>
+void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s) {
+  if (parts < 2) {
+    product<P, TA, true, Out<T>>(g, o, 1, s);
+    return;
+  }
+  float *from = reinterpret_cast<float *>(ws);
+  g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
+  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, nullptr};
+  product<P, TA, true, Out<T>>(g, part, parts, s);
+  const int64_t quads = (int64_t)g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
+                     dim3(256), 0, s, g.M, g.N, g.count_is_k ? nullptr : g.count, parts, from,
+                     part.part, o.sum, o.lds, o.first, o.last, static_cast<T *>(o.out), o.ldo, o.row);
 }
 
 template <class T, int P>
@@ -428,20 +494,19 @@ void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss
     const int rows = (int)std::min(p.piece, c.v - v0);
     if (n > 0) {
       const Operand W = weights<T, P>(p, c, v0, rows, in_place, s);
-      product<P, false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, 0, 0},
+      product<P, false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, 0, 0, 0},
                                         GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, (int)v0},
                                         1, s);
       if (dx)
-        product<P, false, true, Out<T>>(
-            Args{G, W, n, d, rows, r.count, 0, 0, 0},
-            OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, v0 == 0,
-                    v0 + p.piece >= c.v, dx, lddx, r.row},
-            1, s);
+        summed<T, P, false>(Args{G, W, n, d, rows, r.count, 0, 0, 0, 0}, p.dx_parts,
+                            OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, 0, v0 == 0,
+                                    v0 + p.piece >= c.v, dx, lddx, r.row},
+                            n, c.ws + p.parts_at, s);
     }
     if (dw)
-      product<P, true, true, Out<T>>(
-          Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, 0, 0},
-          OutArgs{nullptr, 0, 1, 1, dw + v0 * lddw, lddw, nullptr}, 1, s);
+      summed<T, P, true>(Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, 0, 0, 0}, p.dw_parts,
+                         OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, nullptr},
+                         std::min(p.piece, c.v), c.ws + p.parts_at, s);
   }
 }
 

@@ -26,7 +26,7 @@ namespace og::ns {
 
 using namespace og::tile;
 
-constexpr int kNormBlocks = 256;  // partial sums of squares per matrix
+constexpr int kNormBlocks = 1024;  // partial sums of squares per matrix
 
 struct Input {
   const void *g;
@@ -34,27 +34,31 @@ struct Input {
   int m, n;  // of G
 };
 
-template <class T>
-__device__ __forceinline__ float load(const void *p, int64_t i) {
-  return (float)static_cast<const T *>(p)[i];
-}
-
 // Partial sums of squares of G, in 64 bits (no square of an fp32 value
-// overflows there).  One pass over G: bound by its bytes.
+// overflows there): a block takes every gridDim.x-th row, eight sums a lane in
+// flight.  One pass over G: bound by its bytes.
 template <class T>
 __global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
   const int batch = blockIdx.y;
-  double s = 0;
-  const int64_t base = batch * in.batch;
-  const int64_t count = (int64_t)in.m * in.n;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += step) {
-    const int64_t row = i / in.n;
-    const double v = load<T>(in.g, base + row * in.ld + (i - row * in.n));
-    s += v * v;
+  double s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const T *g = static_cast<const T *>(in.g) + batch * in.batch;
+  for (int row = blockIdx.x; row < in.m; row += gridDim.x) {
+    const T *r = g + row * in.ld;
+    int c = threadIdx.x;
+    for (; c + 7 * 256 < in.n; c += 8 * 256) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = (float)r[c + q * 256];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += (double)v[q] * v[q];
+    }
+    for (; c < in.n; c += 256) {
+      const double v = (float)r[c];
+      s[0] += v * v;
+    }
   }
   __shared__ double sum[256];
-  sum[threadIdx.x] = s;
+  sum[threadIdx.x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
   for (int h = 128; h > 0; h >>= 1) {
     if (threadIdx.x < h) sum[threadIdx.x] += sum[threadIdx.x + h];
@@ -64,41 +68,45 @@ __global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
 }
 
 // X's planes from G: 64 x 64 tiles through LDS (G is read along its rows
-// whichever way X lies), padded with zeros to ld columns.
+// whichever way X lies), padded with zeros to a multiple of 64 columns.
 template <class T, int P, bool TALL>
 __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part, int blocks,
                                                    float eps, uint16_t *x, int64_t ld) {
   __shared__ float tile[64][65];
   __shared__ float factor;
   const int batch = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const int R = TALL ? in.n : in.m, C = TALL ? in.m : in.n;
+  const int R = TALL ? in.n : in.m;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const T *g = static_cast<const T *>(in.g) + batch * in.batch;
+  float v[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    // row i of G's part of the tile
+    const int i = w + 4 * q, row = (TALL ? c0 : r0) + i, col = (TALL ? r0 : c0) + lane;
+    v[q] = row < in.m && col < in.n ? (float)g[row * in.ld + col] : 0.0f;
+  }
   if (threadIdx.x < 64) {
     double s = 0;
     for (int i = threadIdx.x; i < blocks; i += 64) s += part[batch * kNormBlocks + i];
     for (int h = 32; h > 0; h >>= 1) s += __shfl_xor(s, h);
     if (threadIdx.x == 0) factor = (float)(1.0 / ((double)(float)sqrt(s) + (double)eps));
   }
-  const int64_t base = batch * in.batch;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int i = w; i < 64; i += 4) {
-    if (TALL) {
-      const int c = c0 + i, r = r0 + lane;
-      tile[lane][i] = c < C && r < R ? load<T>(in.g, base + (int64_t)c * in.ld + r) : 0.0f;
-    } else {
-      const int r = r0 + i, c = c0 + lane;
-      tile[i][lane] = r < R && c < C ? load<T>(in.g, base + (int64_t)r * in.ld + c) : 0.0f;
-    }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    if (TALL) tile[lane][w + 4 * q] = v[q];
+    else tile[w + 4 * q][lane] = v[q];
   }
   __syncthreads();
   const float f = factor;
-  for (int q = threadIdx.x; q < 64 * 16; q += 256) {
-    const int i = q >> 4, j = (q & 15) * 4;
-    if (r0 + i >= R) continue;
-    f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = tile[i][j + e] * f;
+  for (int q = 0; q < 4; ++q) {
+    const int at = threadIdx.x + 256 * q, i = at >> 4, j = (at & 15) * 4;
+    if (r0 + i >= R) continue;
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = tile[i][j + e] * f;
     bf16x4 out[P];
-    split4<P>(v, out);
+    split4<P>(y, out);
     uint16_t *to = x + (batch * (int64_t)R + r0 + i) * ld;
 #pragma unroll
     for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(c0 + j, p)) = out[p];
@@ -249,8 +257,7 @@ void run(const Plan &p, const Input &in, int batch, int steps, float a, float b,
   uint16_t *A = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes);
   uint16_t *B = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes + p.a_bytes);
   const bool tall = in.m > in.n;
-  const int64_t count = (int64_t)in.m * in.n;
-  const int blocks = (int)std::min<int64_t>(kNormBlocks, (count + 2047) / 2048);
+  const int blocks = std::min(kNormBlocks, in.m);
   hipLaunchKernelGGL(norm_kernel<T>, dim3(blocks, batch), dim3(256), 0, s, in, norm);
   const dim3 grid((unsigned)(p.kp / 64), (unsigned)(p.rp / 64), batch);
   if (tall)
@@ -263,11 +270,11 @@ void run(const Plan &p, const Input &in, int batch, int steps, float a, float b,
   for (int i = 0; i < steps; ++i) {
     uint16_t *from = x[i & 1], *to = i + 1 < steps ? x[(i + 1) & 1] : nullptr;
     const Operand X{from, ldx, xb}, OA{A, lda, ab}, OB{B, lda, ab};
-    product<P, false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0},
+    product<P, false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0, 0},
                                      SymArgs{A, nullptr, lda, ab, 0, 0}, batch, s);
-    product<P, false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0},
+    product<P, false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0, 0},
                                      SymArgs{B, A, lda, ab, b, c}, batch, s);
-    product<P, false, true, Next<P, T>>(Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0},
+    product<P, false, true, Next<P, T>>(Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0, 0},
                                         NextArgs{from, to, ldx, xb, a, o, ldo, stride_o, tall},
                                         batch, s);
   }

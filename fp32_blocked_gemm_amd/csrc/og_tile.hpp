@@ -40,6 +40,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 namespace og::tile {
@@ -73,6 +74,7 @@ struct Args {
   const int *count;  // when not null, *count (on the device, at most M or K) stands for M or K
   int count_is_k;
   int tiles_m, tiles_n;
+  int k_split;  // when not 0, batch y takes k from y k_split to the next split
 };
 
 // Where column c of plane p lies in a row of P planes.
@@ -111,7 +113,8 @@ __device__ __forceinline__ int slots(int row) {
 template <int BX, int P>
 __device__ __forceinline__ int hash(int k) {
   // rows that are not a multiple of 256 bytes alternate between the bank halves by themselves
-  return BX * P * 2 % 256 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+  // (those of 64 and 192 bytes hold whole pairs of units only)
+  return BX * P * 2 % 128 ? (k >> 3) & 1 : BX * P * 2 % 256 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
 }
 
 // Loads one operand's stages: BX rows of m by depth(P) of k, P planes.
@@ -164,17 +167,16 @@ struct Reader {
       const int k = 8 * g + (i >> 2);
       base = k * BX * P * 2 + (i & 3) * 8;
       swz = hash<BX, P>(k) << 5;
-      unit = (x >> 4) * P;  // x / 32 blocks of 2 P units
+      unit = x >> 4;
     }
   }
-  // fragment `f` (even + odd pairs make blocks of 32) of the wave's rows; b: the k half of the
-  // stage (one plane) or the plane
+  // fragment `f` of the wave's rows; b: the k half of the stage (one plane) or the plane
   __device__ __forceinline__ bf16x8 read(const char *lds, int f, int b) const {
     if constexpr (!T) {
       const int at = P == 3 ? base + b * 64 : base ^ (b << 6);
       return *reinterpret_cast<const bf16x8 *>(lds + at + f * (P == 3 ? 3072 : 2048));
     } else {
-      const int u = unit + (P == 1 ? f : (f >> 1) * 2 * P + b * 2 + (f & 1));
+      const int c = unit + f, u = P == 1 ? c : (c >> 1) * 2 * P + b * 2 + (c & 1);
       const int at = base + ((u << 5) ^ swz) + (P == 1 ? b * 32 * BX * 2 : 0);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 8 * BX * P));
@@ -201,6 +203,7 @@ template <int P_, int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
 struct Shape {
   static constexpr int P = P_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, BLOCKS = BLOCKS_;
   static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int kWavesPerSimd = BLOCKS * NW > 4 ? BLOCKS * NW / 4 : 1;
   static constexpr int kStage = (BM + BN) * depth(P) * P * 2;
 };
 
@@ -228,7 +231,7 @@ __device__ __forceinline__ void tile_of(int id, int tm, int tn, int &m, int &n) 
 }
 
 template <class S, bool TA, bool TB, class Epi>
-__global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typename Epi::Args e) {
+__global__ __launch_bounds__(S::NW * 64, S::kWavesPerSimd) void tile_kernel(Args g, typename Epi::Args e) {
   constexpr int P = S::P, FM = S::FM, FN = S::FN, kDepth = depth(P);
   __shared__ __align__(1024) char lds[S::kStage * S::NST];
   using SA = Stager<S::BM, S::NW, TA, P>;
@@ -245,6 +248,11 @@ __global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typ
   const int x0 = tm * S::BM, y0 = tn * S::BN;
   if (x0 >= M) return;
   const int batch = blockIdx.y;
+  int k_next = 0;
+  if (g.k_split) {
+    k_next = batch * g.k_split;
+    K = min(K, k_next + g.k_split);
+  }
   const uint16_t *ap = g.a.p + batch * g.a.batch + (TA ? (int64_t)x0 * P : x0 * g.a.ld);
   const uint16_t *bp = g.b.p + batch * g.b.batch + (TB ? (int64_t)y0 * P : y0 * g.b.ld);
 
@@ -265,9 +273,9 @@ __global__ __launch_bounds__(S::NW * 64, S::BLOCKS) void tile_kernel(Args g, typ
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
   // stages past the last load zeros
-  const int total = (K + kDepth - 1) / kDepth;
+  const int total = (K - k_next + kDepth - 1) / kDepth;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds;
-  int k_next = 0, buf_next = 0;
+  int buf_next = 0;
   u32x4 rsa, rsb;
   uint32_t to;
   int left;
@@ -404,47 +412,76 @@ int launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// The tiles, by planes: large, middle, small.
+// A tile and what it costs: microseconds a block spends on a stage, alone on
+// its compute unit on an idle card and as its share of a full one (measured on
+// products of 128 to 14336 columns, within a fifth).
+template <class S_, int ALONE, int SHARE>  // nanoseconds
+struct Choice {
+  using S = S_;
+  static double time(bool sym, int64_t M, int64_t N, int64_t K, int64_t batch) {
+    const int64_t tm = (M + S::BM - 1) / S::BM, tn = (N + S::BN - 1) / S::BN;
+    const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
+    const double per = n <= 256 ? ALONE + (SHARE - ALONE) * (n / 256.0) : (n + 255) / 256 * SHARE;
+    return (double)((K + depth(S::P) - 1) / depth(S::P)) * per;
+  }
+};
+template <class... C>
+struct Choices {};
+
+// The tiles by number of planes.  Large ones reuse each loaded value more
+// often (a compute unit loads about 30 bytes a cycle at most), small ones
+// spread a small product over more compute units; symmetric products need
+// square tiles.
 template <int P, bool SYM>
 struct Tiles {
-  using L = Shape<P, 256, 256, 2, 4, 2, 1>;
-  using M = Shape<P, 128, 128, 2, 2, 2, 2>;
-  using S = Shape<P, 64, 64, 2, 2, 4, 2>;
+  using type = Choices<Choice<Shape<1, 256, 256, 2, 4, 2, 1>, 1400, 1700>,
+                       Choice<Shape<1, 128, 128, 2, 2, 2, 2>, 500, 510>,
+                       Choice<Shape<1, 64, 64, 2, 2, 4, 2>, 210, 220>>;
 };
 template <bool SYM>
 struct Tiles<2, SYM> {
-  using L = Shape<2, 256, 256, 2, 4, 2, 1>;
-  using M = Shape<2, 128, 128, 2, 4, 2, 2>;
-  using S = Shape<2, 64, 64, 2, 2, 4, 2>;
+  using type = Choices<Choice<Shape<2, 256, 256, 2, 4, 2, 1>, 1300, 2250>,
+                       Choice<Shape<2, 192, 192, 2, 4, 3, 1>, 1150, 1250>,
+                       Choice<Shape<2, 128, 128, 2, 4, 2, 2>, 660, 630>,
+                       Choice<Shape<2, 64, 64, 2, 2, 4, 2>, 226, 230>,
+                       Choice<Shape<2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
 };
-template <bool SYM>
-struct Tiles<3, SYM> {
-  using L = Shape<3, 128, SYM ? 128 : 256, 2, 4, SYM ? 3 : 2, 1>;  // symmetric: square tiles
-  using M = Shape<3, 128, 128, 2, 4, 3, 1>;
-  using S = Shape<3, 64, 64, 2, 2, 3, 2>;
+template <>
+struct Tiles<3, false> {
+  using type = Choices<Choice<Shape<3, 128, 256, 2, 4, 2, 1>, 2400, 2500>,
+                       Choice<Shape<3, 128, 128, 2, 4, 3, 1>, 1400, 1280>,
+                       Choice<Shape<3, 64, 64, 2, 2, 3, 2>, 340, 430>,
+                       Choice<Shape<3, 32, 32, 1, 2, 3, 4>, 225, 195>>;
+};
+template <>
+struct Tiles<3, true> {
+  using type = Choices<Choice<Shape<3, 128, 128, 2, 4, 3, 1>, 1400, 1280>,
+                       Choice<Shape<3, 64, 64, 2, 2, 3, 2>, 340, 430>,
+                       Choice<Shape<3, 32, 32, 1, 2, 3, 4>, 225, 195>>;
 };
 
-// The tile of a product: the largest whose blocks give every compute unit
-// work; below that the one with the least rounds x time of a block (a 256 x
-// 256 block takes 4 / 0.8 of a 128 x 128 one's time and 16 / 0.45 of a 64 x
-// 64 one's, two of which share a compute unit).
-template <class S, bool SYM>
-double rounds(int64_t M, int64_t N, int64_t batch, double per_value) {
-  const int64_t tm = (M + S::BM - 1) / S::BM, tn = (N + S::BN - 1) / S::BN;
-  const int64_t n = (SYM ? tm * (tm + 1) / 2 : tm * tn) * batch;
-  return (double)((n + 255) / 256) * (S::BM * S::BN) * per_value;
+// Runs a product on the tile with the least time; returns the number of tile
+// columns.
+template <bool TA, bool TB, class Epi, class First, class... Rest>
+int product_of(Choices<First, Rest...>, double best, const Args &g, const typename Epi::Args &e,
+               int batch, hipStream_t s) {
+  constexpr bool sym = Epi::kSymmetric;
+  const int64_t k = g.k_split ? g.k_split : g.K;
+  if constexpr (sizeof...(Rest) > 0) {
+    if (First::time(sym, g.M, g.N, k, batch) > best)
+      return product_of<TA, TB, Epi>(Choices<Rest...>(), best, g, e, batch, s);
+  }
+  return launch<typename First::S, TA, TB, Epi>(g, e, batch, s);
 }
-
-// Runs a product on the chosen tile; returns the number of tile columns.
+template <class... C>
+double least(Choices<C...>, bool sym, const Args &g, int batch) {
+  const int64_t k = g.k_split ? g.k_split : g.K;
+  return std::min({C::time(sym, g.M, g.N, k, batch)...});
+}
 template <int P, bool TA, bool TB, class Epi>
 int product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
-  using T = Tiles<P, Epi::kSymmetric>;
-  const double l = rounds<typename T::L, Epi::kSymmetric>(g.M, g.N, batch, 1.0);
-  const double m = rounds<typename T::M, Epi::kSymmetric>(g.M, g.N, batch, 1.25);
-  const double c = rounds<typename T::S, Epi::kSymmetric>(g.M, g.N, batch, 2.2);
-  if (l <= m && l <= c) return launch<typename T::L, TA, TB, Epi>(g, e, batch, s);
-  if (m <= c) return launch<typename T::M, TA, TB, Epi>(g, e, batch, s);
-  return launch<typename T::S, TA, TB, Epi>(g, e, batch, s);
+  using T = typename Tiles<P, Epi::kSymmetric>::type;
+  return product_of<TA, TB, Epi>(T(), least(T(), Epi::kSymmetric, g, batch), g, e, batch, s);
 }
 
 // Planes of four fp32 values: each plane rounds what is left to bf16.  A
