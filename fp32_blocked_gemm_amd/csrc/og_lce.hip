@@ -12,15 +12,23 @@
 //
 // Forward: one tile product whose epilogue keeps a running maximum and sum of
 // each row over the tile's columns; a second kernel joins the tiles.  The
-// gradient recomputes the logits in pieces of the vocabulary: g of a piece is
-// rounded to bf16 planes (one for bf16 tensors, whose rounding is that of the
-// gradients themselves; three, fp32's 24 bits, for fp32 ones) and both
-// products read it from there.  All of it is bound by the matrix cores:
+// gradient recomputes the logits in pieces of the vocabulary, stores g of a
+// piece and runs both products on it.  All of it is bound by the matrix cores:
 // 2 n v d operations forward, 6 n v d backward.
+//
+// bf16 tensors run as they are, g in bf16 (whose rounding is that of the
+// gradients themselves).  fp32 ones run as two fp16 planes (og_tile.hpp), each
+// row of X and W times a power of two of its own that brings its largest value
+// to [2^13, 2^14).  The logits undo both powers.  For the gradients, whose sums
+// run over rows of W and of X, g is stored divided by both (and times one power
+// of two for all, c, that brings the largest possible value to 2^14): then each
+// product's own rows of W or X cancel inside the sum, and what is left is one
+// power of two for each row of the result.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "og.h"
 #include "og_host.hpp"
@@ -31,6 +39,7 @@ namespace og::lce {
 using namespace og::tile;
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBias = 4096;
 
 // The compact list of the rows that count.
 struct Rows {
@@ -41,6 +50,10 @@ struct Rows {
   float *lse;
   float *dloss;
   float *zt;      // the target's logit (forward)
+  int *xexp;      // fp32: the exponent of a row of X, by place
+  // fp32: the largest exponent of |dloss| x row maximum of X, and of a row
+  // maximum of W, each + kBias (0: none)
+  int *most;
 };
 
 // One block: the rows' places by a running count, in order.  Rows that do not
@@ -83,7 +96,10 @@ __global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int6
     done += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) *r.count = done;
+  if (threadIdx.x == 0) {
+    *r.count = done;
+    r.most[0] = r.most[1] = 0;
+  }
 }
 
 template <class T, bool VEC>
@@ -107,14 +123,14 @@ __device__ __forceinline__ f32x4 load4(const T *p, int left) {
   return v;
 }
 
-// Planes of `rows` rows of `cols` values, padded with zeros to ld / P columns.
-// With pos, row i goes to place pos[i], and a row without a place clears its
-// row of `clear` instead (the gradient of an ignored row).
-template <class T, int P, bool VEC>
-__global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const T *x, int64_t ldx,
-                                                     const int *pos, uint16_t *out, int64_t ld,
-                                                     T *clear, int64_t ldc) {
-  const int per = (int)(ld / (4 * P));
+// `rows` rows of `cols` bf16 values, padded with zeros to ld columns.  With
+// pos, row i goes to place pos[i], and a row without a place clears its row of
+// `clear` instead (the gradient of an ignored row).
+template <bool VEC>
+__global__ __launch_bounds__(256) void copy_kernel(int rows, int cols, const __bf16 *x, int64_t ldx,
+                                                   const int *pos, uint16_t *out, int64_t ld,
+                                                   __bf16 *clear, int64_t ldc) {
+  const int per = (int)(ld / 4);
   const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * 256;
   for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += step) {
     const int i = (int)(q / per), c = (int)(q - (int64_t)i * per) * 4;
@@ -122,15 +138,82 @@ __global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const T
     if (to < 0) {
       if (clear)
         for (int e = 0; e < 4; ++e)
-          if (c + e < cols) clear[i * ldc + c + e] = (T)0.0f;
+          if (c + e < cols) clear[i * ldc + c + e] = (__bf16)0.0f;
       continue;
     }
-    bf16x4 h[P];
-    split4<P>(load4<T, VEC>(x + i * ldx + c, cols - c), h);
+    const f32x4 v = load4<__bf16, VEC>(x + i * ldx + c, cols - c);
+    bf16x4 h;
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-      *reinterpret_cast<bf16x4 *>(out + to * ld + column<P>(c, p)) = h[p];
+    for (int e = 0; e < 4; ++e) h[e] = (__bf16)v[e];
+    *reinterpret_cast<bf16x4 *>(out + to * ld + c) = h;
   }
+}
+
+// The same for fp32: two planes of each row times its power of two, whose
+// exponent goes to exp (by place).  A wave takes a row: once for its maximum,
+// once more, from the caches, for its planes.  `most`: the largest exponent of
+// a maximum (and |weight| by place, where given) of all, by an atomic maximum
+// of each block's (which does not depend on their order).
+template <bool VEC>
+__global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const float *x, int64_t ldx,
+                                                     const int *pos, uint16_t *out, int64_t ld,
+                                                     float *clear, int64_t ldc, int *exp,
+                                                     const float *weight, int *most) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, width = (int)(ld / 2);
+  int seen = 0;
+  for (int i = blockIdx.x * 4 + w; i < rows; i += gridDim.x * 4) {
+    const float *row = x + i * ldx;
+    const int to = pos ? pos[i] : i;
+    if (to < 0) {
+      if (clear)
+        for (int c = lane; c < cols; c += 64) clear[i * ldc + c] = 0.0f;
+      continue;
+    }
+    float top = 0;
+    for (int c = 4 * lane; c < cols; c += 256) {
+      const f32x4 v = load4<float, VEC>(row + c, cols - c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f);
+    }
+    for (int h = 32; h > 0; h >>= 1) top = fmaxf(top, __shfl_xor(top, h));
+    const int e2 = top > 0 ? 14 - (int)__builtin_amdgcn_frexp_expf(top) : 0;
+    const float by = weight ? weight[to] : 0.5f;  // 0.5: exponent 0
+    if (top > 0 && by != 0 && __builtin_isfinite(by))
+      seen = max(seen, kBias + (int)__builtin_amdgcn_frexp_expf(top) + (int)__builtin_amdgcn_frexp_expf(by));
+    if (lane == 0) exp[to] = e2;
+    for (int c = 4 * lane; c < width; c += 256) {
+      f32x4 v = load4<float, VEC>(row + c, cols - c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], e2);
+      f16x4 h, l;
+      split4(v, h, l);
+      *reinterpret_cast<f16x4 *>(out + to * ld + column<2>(c, 0)) = h;
+      *reinterpret_cast<f16x4 *>(out + to * ld + column<2>(c, 1)) = l;
+    }
+  }
+  if (most) {
+    __shared__ int block[4];
+    if (lane == 0) block[w] = seen;
+    __syncthreads();
+    if (threadIdx.x == 0) atomicMax(most, max(max(block[0], block[1]), max(block[2], block[3])));
+  }
+}
+
+// c of a call (see the top): |g| max |x| max |w| < 2^(both exponents), and the
+// row maxima are 2^13 of the planes' units at least, so that |g 2^c / (both
+// powers)| stays below 2^14.
+__device__ __forceinline__ int common_exponent(const int *most) {
+  return 40 - (most[0] ? most[0] - kBias : 0) - (most[1] ? most[1] - kBias : 0);
+}
+
+// Four logits: fp32 sums as they are, or less their rows' powers of two.
+template <int P>
+__device__ __forceinline__ f32x4 logits(f32x4 v, int xexp, const int *wexp, int n, int N) {
+  if constexpr (P == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = __builtin_ldexpf(v[q], -(xexp + wexp[min(n + q, N - 1)]));
+  }
+  return v;
 }
 
 // Epilogue of the forward product: each row's maximum over the tile's columns
@@ -139,8 +222,10 @@ struct LseArgs {
   float2 *part;  // [tile column][n]
   const int *target;
   float *zt;
+  const int *xexp, *wexp;  // exponents of the planes' rows
   int n, v0, part0;  // rows of part, first column, first tile column
 };
+template <int P>
 struct Lse {
   using Args = LseArgs;
   static constexpr bool kSymmetric = false;
@@ -153,15 +238,18 @@ struct Lse {
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       const int want = m < t.M ? e.target[m] - e.v0 - nc : -1;
+      const int xexp = P == 2 && m < t.M ? e.xexp[m] : 0;
       float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < S::FN; ++j)
+      for (int j = 0; j < S::FN; ++j) {
+        acc[i][j] = logits<P>(acc[i][j], xexp, e.wexp, nc + 16 * j, t.N);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (want == 16 * j + q) e.zt[m] = acc[i][j][q];
           if (nc + 16 * j + q >= t.N) acc[i][j][q] = -INFINITY;
           top = fmaxf(top, acc[i][j][q]);
         }
+      }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float from = top == -INFINITY ? 0.0f : top;
@@ -227,6 +315,8 @@ struct GradArgs {
   int64_t ld;
   const int *target;
   const float *lse, *dloss;
+  const int *xexp, *wexp;
+  const int *most;
   int v0;
 };
 template <int P>
@@ -237,26 +327,39 @@ struct Grad {
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
+    const int common = P == 2 ? common_exponent(e.most) : 0;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
       const float l = e.lse[m], d = e.dloss[m];
       const int want = e.target[m] - e.v0 - nc;
+      const int xexp = P == 2 ? e.xexp[m] : 0;
       uint16_t *to = e.g + m * e.ld;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
-        if (nc + 16 * j >= e.ld / P) continue;
-        f32x4 v;
+        const int n = nc + 16 * j;
+        if (n >= e.ld / P) continue;
+        f32x4 v = logits<P>(acc[i][j], xexp, e.wexp, n, t.N);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float p = __builtin_amdgcn_exp2f((acc[i][j][q] - l) * kLog2e);
-          v[q] = nc + 16 * j + q < t.N ? (want == 16 * j + q ? p - 1.0f : p) * d : 0.0f;
+          const float p = __builtin_amdgcn_exp2f((v[q] - l) * kLog2e);
+          v[q] = n + q < t.N ? (want == 16 * j + q ? p - 1.0f : p) * d : 0.0f;
         }
-        bf16x4 h[P];
-        split4<P>(v, h);
+        if constexpr (P == 1) {
+          bf16x4 h;
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(nc + 16 * j, p)) = h[p];
+          for (int q = 0; q < 4; ++q) h[q] = (__bf16)v[q];
+          *reinterpret_cast<bf16x4 *>(to + n) = h;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = __builtin_ldexpf(v[q], common - xexp - e.wexp[min(n + q, t.N - 1)]);
+          f16x4 h, l2;
+          split4(v, h, l2);
+          *reinterpret_cast<f16x4 *>(to + column<2>(n, 0)) = h;
+          *reinterpret_cast<f16x4 *>(to + column<2>(n, 1)) = l2;
+        }
       }
     }
   }
@@ -273,6 +376,8 @@ struct OutArgs {
   void *out;
   int64_t ldo;
   const int *row;  // null: row m is row m of out
+  const int *exp;  // fp32: the exponents of the rows, less the common one
+  const int *most;
 };
 template <class T>
 struct Out {
@@ -282,10 +387,12 @@ struct Out {
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
+    const int common = S::P == 2 ? common_exponent(e.most) : 0;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
+      const int up = S::P == 2 ? e.exp[m] - common : 0;
       T *to = static_cast<T *>(e.out) + (e.row ? e.row[m] : m) * e.ldo;
       float *sum = e.sum + t.batch * e.part + m * e.lds;
 #pragma unroll
@@ -293,6 +400,10 @@ struct Out {
         const int n = nc + 16 * j;
         if (n >= t.N) continue;
         f32x4 v = acc[i][j];
+        if constexpr (S::P == 2) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = __builtin_ldexpf(v[q], up);
+        }
         if (!e.first) {
           const f32x4 was = *reinterpret_cast<const f32x4 *>(sum + n);
 #pragma unroll
@@ -345,7 +456,7 @@ struct Plan {
   int64_t dp;           // d padded
   int64_t piece;        // vocabulary rows of a piece
   int dx_parts, dw_parts;  // parts of k of a piece's gradient products
-  int64_t rows_at, x_at, w_at, part_at, g_at, sum_at, parts_at, total;
+  int64_t rows_at, wexp_at, x_at, w_at, part_at, g_at, sum_at, parts_at, total;
 };
 
 // Parts of k of an m x n product: as many as make up two tiles of 64 x 64 for
@@ -362,7 +473,7 @@ int parts_of(int64_t m, int64_t n, int64_t k) {
 // are 512 of them), small enough to stay in the 256 MB last-level cache.
 Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   Plan p;
-  p.planes = type == OG_F32 ? 3 : 1;
+  p.planes = type == OG_F32 ? 2 : 1;
   p.dp = round_up(d, 64);
   const int64_t most = (int64_t(1) << 25) / std::max(n, p.dp) / 256 * 256;
   p.piece = std::min(round_up(v, 256), std::max<int64_t>(2048, most));
@@ -372,7 +483,8 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
     at += round_up(bytes, 256);
     return here;
   };
-  p.rows_at = take(256 + 6 * round_up(n, 64) * 4);
+  p.rows_at = take(256 + 7 * round_up(n, 64) * 4);
+  p.wexp_at = take(p.planes == 2 ? p.piece * 4 : 0);
   p.x_at = take(p.planes * n * p.dp * 2);
   p.w_at = take(p.planes * p.piece * p.dp * 2);
   p.part_at = grad ? at : take((round_up(v, p.piece) / 32) * n * 8);
@@ -392,21 +504,27 @@ Rows rows_of(char *at, int64_t n) {
   const int64_t s = round_up(n, 64);
   int *p = reinterpret_cast<int *>(at + 256);
   return Rows{reinterpret_cast<int *>(at), p, p + s, p + 2 * s, reinterpret_cast<float *>(p + 3 * s),
-              reinterpret_cast<float *>(p + 4 * s), reinterpret_cast<float *>(p + 5 * s)};
+              reinterpret_cast<float *>(p + 4 * s), reinterpret_cast<float *>(p + 5 * s), p + 6 * s,
+              reinterpret_cast<int *>(at) + 1};
 }
 
-template <class T, int P>
-void planes(int64_t rows, int64_t cols, const T *x, int64_t ldx, const int *pos, uint16_t *out,
-            int64_t ld, T *clear, int64_t ldc, hipStream_t s) {
-  const int64_t quads = rows * (ld / (4 * P));
-  const dim3 grid((unsigned)std::min<int64_t>((quads + 255) / 256, 8192));
-  const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0;
-  if (vec)
-    hipLaunchKernelGGL((planes_kernel<T, P, true>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
-                       ldx, pos, out, ld, clear, ldc);
-  else
-    hipLaunchKernelGGL((planes_kernel<T, P, false>), grid, dim3(256), 0, s, (int)rows, (int)cols, x,
-                       ldx, pos, out, ld, clear, ldc);
+void operand_rows(int64_t rows, int64_t cols, const __bf16 *x, int64_t ldx, const int *pos,
+                  uint16_t *out, int64_t dp, __bf16 *clear, int64_t ldc, int *, const float *,
+                  int *, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>((rows * (dp / 4) + 255) / 256, 8192));
+  const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 8 == 0;
+  const auto kernel = vec ? copy_kernel<true> : copy_kernel<false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (int)rows, (int)cols, x, ldx, pos, out, dp,
+                     clear, ldc);
+}
+void operand_rows(int64_t rows, int64_t cols, const float *x, int64_t ldx, const int *pos,
+                  uint16_t *out, int64_t dp, float *clear, int64_t ldc, int *exp,
+                  const float *weight, int *most, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>((rows + 3) / 4, most ? 1024 : 4096));
+  const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  const auto kernel = vec ? planes_kernel<true> : planes_kernel<false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (int)rows, (int)cols, x, ldx, pos, out, 2 * dp,
+                     clear, ldc, exp, weight, most);
 }
 
 struct Call {
@@ -422,11 +540,12 @@ struct Call {
 // it (bf16, whole aligned granules of 8), else its planes in the workspace.
 template <class T, int P>
 Operand weights(const Plan &p, const Call &c, int64_t v0, int64_t rows, bool in_place,
-                hipStream_t s) {
+                int *most, hipStream_t s) {
   const T *w = static_cast<const T *>(c.w) + v0 * c.ldw;
   if (in_place) return Operand{reinterpret_cast<const uint16_t *>(w), c.ldw, 0};
   uint16_t *to = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
-  planes<T, P>(rows, c.d, w, c.ldw, nullptr, to, P * p.dp, nullptr, 0, s);
+  operand_rows(rows, c.d, w, c.ldw, nullptr, to, p.dp, (T *)nullptr, 0,
+               reinterpret_cast<int *>(c.ws + p.wexp_at), nullptr, most, s);
   return Operand{to, P * p.dp, 0};
 }
 template <class T>
@@ -435,24 +554,29 @@ bool readable(const Call &c) {
          reinterpret_cast<uintptr_t>(c.w) % 16 == 0;
 }
 
+// The matrix cores' elements: bf16 as given, fp32 as fp16 planes.
+template <class T>
+using Element = std::conditional_t<std::is_same_v<T, float>, _Float16, __bf16>;
+
 template <class T, int P>
 void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t s) {
   const Rows r = rows_of(c.ws + p.rows_at, c.n);
   uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
+  const int *wexp = reinterpret_cast<const int *>(c.ws + p.wexp_at);
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, (int)c.n, c.v, c.target, c.ignore, r,
                      (const float *)nullptr, (const float *)nullptr, loss, lse);
-  planes<T, P>(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, P * p.dp,
-               (T *)nullptr, 0, s);
+  operand_rows(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, (T *)nullptr, 0,
+               r.xexp, nullptr, nullptr, s);
   float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
   const bool in_place = readable<T>(c);
   const int64_t piece = in_place ? c.v : p.piece;
   int tiles = 0;
   for (int64_t v0 = 0; v0 < c.v; v0 += piece) {
     const int rows = (int)std::min(piece, c.v - v0);
-    const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
-    tiles += product<P, false, false, Lse>(
+    const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, nullptr, s);
+    tiles += product<Element<T>, P, false, false, Lse<P>>(
         Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, 0, 0, 0},
-        LseArgs{part, r.target, r.zt, (int)c.n, (int)v0, tiles}, 1, s);
+        LseArgs{part, r.target, r.zt, r.xexp, wexp, (int)c.n, (int)v0, tiles}, 1, s);
   }
   hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((c.n + 7) / 8)), dim3(256), 0, s, r, part,
                      (int)c.n, tiles, loss, lse);
@@ -463,13 +587,13 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
 template <class T, int P, bool TA>
 void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s) {
   if (parts < 2) {
-    product<P, TA, true, Out<T>>(g, o, 1, s);
+    product<Element<T>, P, TA, true, Out<T>>(g, o, 1, s);
     return;
   }
   float *from = reinterpret_cast<float *>(ws);
   g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, nullptr};
-  product<P, TA, true, Out<T>>(g, part, parts, s);
+  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, nullptr, o.exp, o.most};
+  product<Element<T>, P, TA, true, Out<T>>(g, part, parts, s);
   const int64_t quads = (int64_t)g.M * ((g.N + 3) / 4);
   hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
                      dim3(256), 0, s, g.M, g.N, g.count_is_k ? nullptr : g.count, parts, from,
@@ -482,30 +606,32 @@ void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss
   const Rows r = rows_of(c.ws + p.rows_at, c.n);
   uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
   uint16_t *g = reinterpret_cast<uint16_t *>(c.ws + p.g_at);
+  const int *wexp = reinterpret_cast<const int *>(c.ws + p.wexp_at);
   const int n = (int)c.n, d = (int)c.d;
   const Operand X{x, P * p.dp, 0}, G{g, P * p.piece, 0};
-  if (n > 0) {
-    hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, n, c.v, c.target, c.ignore, r, lse,
-                       dloss, (float *)nullptr, (float *)nullptr);
-    planes<T, P>(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, P * p.dp, dx, lddx, s);
-  }
+  // (n = 0 runs this too: it clears what the epilogues read)
+  hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, n, c.v, c.target, c.ignore, r, lse,
+                     dloss, (float *)nullptr, (float *)nullptr);
+  if (n > 0)
+    operand_rows(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, dx, lddx, r.xexp,
+                 r.dloss, r.most, s);
   const bool in_place = readable<T>(c);
   for (int64_t v0 = 0; v0 < c.v; v0 += p.piece) {
     const int rows = (int)std::min(p.piece, c.v - v0);
     if (n > 0) {
-      const Operand W = weights<T, P>(p, c, v0, rows, in_place, s);
-      product<P, false, false, Grad<P>>(Args{X, W, n, rows, d, r.count, 0, 0, 0, 0},
-                                        GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, (int)v0},
-                                        1, s);
+      const Operand W = weights<T, P>(p, c, v0, rows, in_place, r.most + 1, s);
+      product<Element<T>, P, false, false, Grad<P>>(
+          Args{X, W, n, rows, d, r.count, 0, 0, 0, 0},
+          GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, r.xexp, wexp, r.most, (int)v0}, 1, s);
       if (dx)
         summed<T, P, false>(Args{G, W, n, d, rows, r.count, 0, 0, 0, 0}, p.dx_parts,
                             OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, 0, v0 == 0,
-                                    v0 + p.piece >= c.v, dx, lddx, r.row},
+                                    v0 + p.piece >= c.v, dx, lddx, r.row, r.xexp, r.most},
                             n, c.ws + p.parts_at, s);
     }
     if (dw)
-      summed<T, P, true>(Args{G, X, rows, d, n, n > 0 ? r.count : nullptr, 1, 0, 0, 0}, p.dw_parts,
-                         OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, nullptr},
+      summed<T, P, true>(Args{G, X, rows, d, n, r.count, 1, 0, 0, 0}, p.dw_parts,
+                         OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, nullptr, wexp, r.most},
                          std::min(p.piece, c.v), c.ws + p.parts_at, s);
   }
 }
@@ -566,7 +692,7 @@ og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X
   if (!loss || !lse) return fail(OG_ERR_INVALID_ARG, "loss or lse is null");
   if ((st = check_device()) != OG_OK) return st;
   if (type == OG_F32)
-    og::lce::forward<float, 3>(p, c, loss, lse, current_stream());
+    og::lce::forward<float, 2>(p, c, loss, lse, current_stream());
   else
     og::lce::forward<__bf16, 1>(p, c, loss, lse, current_stream());
   return check_launch("linear_cross_entropy");
@@ -590,7 +716,7 @@ og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const vo
   if ((n == 0 && !dW) || (!dX && !dW)) return ok();
   if ((st = check_device()) != OG_OK) return st;
   if (type == OG_F32)
-    og::lce::gradient<float, 3>(p, c, lse, dloss, static_cast<float *>(dX), lddx,
+    og::lce::gradient<float, 2>(p, c, lse, dloss, static_cast<float *>(dX), lddx,
                                 static_cast<float *>(dW), lddw, current_stream());
   else
     og::lce::gradient<__bf16, 1>(p, c, lse, dloss, static_cast<__bf16 *>(dX), lddx,

@@ -4,15 +4,24 @@
 //   X = G / (|G| + eps)   (the Frobenius norm; the shorter side as rows, r <= k)
 //   each step:  A = X X^T,  B = b A + c A A,  X <- a X + B X
 //
-// Every product runs on the bf16 matrix cores with its operands in planes
-// (og_tile.hpp): three planes for fp32 input (fp32 accuracy), two for bf16
-// input (16 bits: the polynomial's slope of up to a per step lifts a rounding
-// of X by a^steps, 484 at the usual coefficients, in the directions it
-// stretches most, so that X held in 8 bits, as one plane, would lose the
-// result's last bits; 16 bits keep the error two hundred times below the
-// rounding of the output).  A and A A are symmetric: only the tiles on and
-// below the diagonal are computed and each is stored to both places, a
-// quarter of the step's work at r = k.
+// Every product runs on the fp16 matrix cores (og_tile.hpp).  X is kept as two
+// fp16 planes (22 bits).  For fp32 input all products take both planes, and A
+// and B have two.  For bf16 input (of more than kNarrow rows) they take the
+// first plane, and A and B have one (11 bits): an error of A or B enters X through B X, whose entries the
+// polynomial's own slope lifts little, and stays a third of the result's own
+// rounding to bf16, while X itself in 11 bits would not do: the slope of up to
+// a per step lifts its rounding by a^steps, 484 at the usual coefficients, in
+// the directions it stretches most (hence X's second plane, which enters
+// through a X).
+//
+// Each matrix is stored times a power of two that its largest possible value
+// sets: the singular values of X stay below s (1 at first, then the largest
+// |p| over [0, s]), those of A below s^2 and those of B below the largest
+// |b x^2 + c x^4|, all found on the host from the coefficients alone.
+//
+// A and A A are symmetric: only the tiles on and below the diagonal are
+// computed and each is stored to both places, a quarter of the step's work at
+// r = k.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -26,7 +35,37 @@ namespace og::ns {
 
 using namespace og::tile;
 
+// Up to this many rows bf16 input runs like fp32: the error of one plane shows
+// against a result whose norm is sqrt(r) (measured over the plain chain's:
+// 1.5 times at 33 rows, 1.2 at 777, 1.02 at 4096), and costs no time there.
+constexpr int kNarrow = 256;
 constexpr int kNormBlocks = 1024;  // partial sums of squares per matrix
+
+// X: two planes, interleaved where the products take both (P = 2), one after
+// the other where they take the first (P = 1).
+template <int P>
+struct Wide {
+  uint16_t *p;
+  int64_t ld, batch, plane;
+  int width;  // columns of a row, padding included
+  __device__ __forceinline__ uint16_t *at(int m, int r, int c, int q) const {
+    return p + m * batch + r * ld + (P == 2 ? column<2>(c, q) : c + q * plane);
+  }
+  __device__ __forceinline__ f32x4 load(int m, int r, int c) const {
+    const f16x4 h = *reinterpret_cast<const f16x4 *>(at(m, r, c, 0));
+    const f16x4 l = *reinterpret_cast<const f16x4 *>(at(m, r, c, 1));
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
+    return v;
+  }
+  __device__ __forceinline__ void store(int m, int r, int c, const f32x4 v) const {
+    f16x4 h, l;
+    split4(v, h, l);
+    *reinterpret_cast<f16x4 *>(at(m, r, c, 0)) = h;
+    *reinterpret_cast<f16x4 *>(at(m, r, c, 1)) = l;
+  }
+};
 
 struct Input {
   const void *g;
@@ -71,9 +110,9 @@ __global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
 // whichever way X lies), padded with zeros to a multiple of 64 columns.
 template <class T, int P, bool TALL>
 __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part, int blocks,
-                                                   float eps, uint16_t *x, int64_t ld) {
+                                                   float eps, float scale, Wide<P> x) {
   __shared__ float tile[64][65];
-  __shared__ float factor;
+  __shared__ double factor;
   const int batch = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const int R = TALL ? in.n : in.m;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -89,7 +128,7 @@ __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part,
     double s = 0;
     for (int i = threadIdx.x; i < blocks; i += 64) s += part[batch * kNormBlocks + i];
     for (int h = 32; h > 0; h >>= 1) s += __shfl_xor(s, h);
-    if (threadIdx.x == 0) factor = (float)(1.0 / ((double)(float)sqrt(s) + (double)eps));
+    if (threadIdx.x == 0) factor = scale / (sqrt(s) + (double)eps);
   }
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
@@ -97,126 +136,115 @@ __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part,
     else tile[w + 4 * q][lane] = v[q];
   }
   __syncthreads();
-  const float f = factor;
+  const double f = factor;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int at = threadIdx.x + 256 * q, i = at >> 4, j = (at & 15) * 4;
     if (r0 + i >= R) continue;
     f32x4 y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = tile[i][j + e] * f;
-    bf16x4 out[P];
-    split4<P>(y, out);
-    uint16_t *to = x + (batch * (int64_t)R + r0 + i) * ld;
-#pragma unroll
-    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(c0 + j, p)) = out[p];
+    for (int e = 0; e < 4; ++e) y[e] = (float)(tile[i][j + e] * f);
+    x.store(batch, r0 + i, c0 + j, y);
   }
 }
 
+// A or B: P planes of an r x r matrix.
 template <int P>
-__device__ __forceinline__ f32x4 load_planes(const uint16_t *row, int c) {
-  f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int q = P - 1; q >= 0; --q) {
-    const bf16x4 h = *reinterpret_cast<const bf16x4 *>(row + column<P>(c, q));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += (float)h[e];
-  }
-  return v;
-}
-
-// Epilogue of the symmetric products: A = acc, or B = b A + c acc; each
-// tile below the diagonal is stored to its mirror too.
-struct SymArgs {
-  uint16_t *out;
-  const uint16_t *a;  // null: store acc itself
+struct Square {
+  uint16_t *p;
   int64_t ld, batch;
-  float b, c;
+  __device__ __forceinline__ f32x4 load(int m, int r, int c) const {
+    const uint16_t *row = p + m * batch + r * ld;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = P - 1; q >= 0; --q) {
+      const f16x4 h = *reinterpret_cast<const f16x4 *>(row + column<P>(c, q));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += (float)h[e];
+    }
+    return v;
+  }
+  // four columns of a row; their mirror, four rows of a column (each where flagged)
+  __device__ __forceinline__ void store(int m, int r, int c, const f32x4 v, bool row, bool mirror,
+                                        int n) const {
+    f16x4 h[2];
+    split4(v, h[0], h[1]);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      if (row) *reinterpret_cast<f16x4 *>(p + m * batch + r * ld + column<P>(c, q)) = h[q];
+      if (mirror)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < n)
+            reinterpret_cast<_Float16 *>(p)[m * batch + (c + e) * ld + column<P>(r, q)] = h[q][e];
+    }
+  }
+};
+
+// Epilogue of the symmetric products: out = was a + acc c; each tile below
+// the diagonal is stored to its mirror too.
+template <int P>
+struct SymArgs {
+  Square<P> out, was;  // was.p null: acc c alone
+  float a, c;
 };
 template <int P>
 struct Sym {
-  using Args = SymArgs;
+  using Args = SymArgs<P>;
   static constexpr bool kSymmetric = true;
   template <class S>
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
-    uint16_t *out = e.out + t.batch * e.batch;
-    const uint16_t *a = e.a ? e.a + t.batch * e.batch : nullptr;
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
-    const int width = (int)(e.ld / P);
+    const int width = (int)(e.out.ld / P);
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
-        f32x4 v = acc[i][j];
-        if (a && m < t.M && n < width) {
-          const f32x4 was = load_planes<P>(a + (int64_t)m * e.ld, n);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = fmaf(e.c, v[q], e.b * was[q]);
-        }
+        const bool in = m < t.M && n < width;
+        f32x4 v = {0, 0, 0, 0};
+        if (e.was.p && in) v = e.was.load(t.batch, m, n);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (m >= t.M || n + q >= t.N) v[q] = 0;
-        bf16x4 h[P];
-        split4<P>(v, h);
-        if (m < t.M && n < width) {
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            *reinterpret_cast<bf16x4 *>(out + (int64_t)m * e.ld + column<P>(n, p)) = h[p];
-        }
-        if (t.tile_m != t.tile_n && m < width) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < t.N) {
-#pragma unroll
-              for (int p = 0; p < P; ++p)
-                reinterpret_cast<__bf16 *>(out)[(int64_t)(n + q) * e.ld + column<P>(m, p)] = h[p][q];
-            }
-        }
+          v[q] = m < t.M && n + q < t.N ? fmaf(e.c, acc[i][j][q], e.a * v[q]) : 0.0f;
+        e.out.store(t.batch, m, n, v, in, t.tile_m != t.tile_n && m < width, t.N);
       }
     }
   }
 };
 
-// Epilogue of X <- a X + B X: planes of the next step's X, or the result in
-// its own type and orientation.
+// Epilogue of X <- a X + B X: out = x a + acc c, the next step's X, or the
+// result in its own type and orientation.
+template <int P>
 struct NextArgs {
-  const uint16_t *x;
-  uint16_t *out;  // null after the last step
-  int64_t ld, batch;
-  float a;
-  void *o;
+  Wide<P> x, out;
+  float a, c;
+  void *o;  // the result, after the last step; else null
   int64_t ldo, batch_o;
   int tall;
 };
 template <int P, class T>
 struct Next {
-  using Args = NextArgs;
+  using Args = NextArgs<P>;
   static constexpr bool kSymmetric = false;
   template <class S>
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
-    const uint16_t *x = e.x + t.batch * e.batch;
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
-    const int width = (int)(e.ld / P);
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
-        if (m >= t.M || n >= width) continue;
-        f32x4 v = load_planes<P>(x + (int64_t)m * e.ld, n);
+        if (m >= t.M || n >= e.x.width) continue;
+        f32x4 v = e.x.load(t.batch, m, n);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(e.a, v[q], acc[i][j][q]) : 0.0f;
-        if (e.out) {
-          bf16x4 h[P];
-          split4<P>(v, h);
-          uint16_t *to = e.out + t.batch * e.batch + (int64_t)m * e.ld;
-#pragma unroll
-          for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4 *>(to + column<P>(n, p)) = h[p];
+        for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(e.c, acc[i][j][q], e.a * v[q]) : 0.0f;
+        if (!e.o) {
+          e.out.store(t.batch, m, n, v);
         } else {
           T *o = static_cast<T *>(e.o) + t.batch * e.batch_o;
 #pragma unroll
@@ -229,9 +257,9 @@ struct Next {
 };
 
 struct Plan {
-  int r, k, planes;
-  int64_t rp, kp;                         // r and k padded to blocks of 64
-  int64_t x_bytes, a_bytes, norm_bytes;   // of one buffer, over the batch
+  int r, k, planes;                      // planes of A, B and of the products' operands
+  int64_t rp, kp;                        // r and k padded to blocks of 64
+  int64_t x_bytes, a_bytes, norm_bytes;  // of one buffer, over the batch
   int64_t total() const { return norm_bytes + 2 * x_bytes + 2 * a_bytes; }
 };
 
@@ -239,44 +267,97 @@ Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
   Plan p;
   p.r = (int)std::min(m, n);
   p.k = (int)std::max(m, n);
-  p.planes = type == OG_F32 ? 3 : 2;
+  p.planes = type == OG_F32 || p.r <= kNarrow ? 2 : 1;
   p.rp = round_up(p.r, 64);
   p.kp = round_up(p.k, 64);
-  p.x_bytes = round_up(batch * p.planes * p.r * p.kp * 2, 256);
+  p.x_bytes = round_up(batch * 2 * p.r * p.kp * 2, 256);
   p.a_bytes = round_up(batch * p.planes * p.r * p.rp * 2, 256);
   p.norm_bytes = round_up(batch * kNormBlocks * 8, 256);
   return p;
+}
+
+// The largest |a x + b x^3 + c x^5| over [0, s]: at s or where the derivative
+// is zero (a quadratic in x^2); and |b x^2 + c x^4|, the same for its own.  A
+// hundredth more is for the roundings.
+double largest_next(double a, double b, double c, double s) {
+  auto p = [&](double x) { return std::fabs((a + (b + c * x * x) * x * x) * x); };
+  double top = p(s);
+  auto at = [&](double square) {
+    if (square > 0 && square < s * s) top = std::max(top, p(std::sqrt(square)));
+  };
+  const double d = 9 * b * b - 20 * a * c;
+  if (c == 0) {
+    if (b != 0) at(-a / (3 * b));
+  } else if (d >= 0) {
+    at((-3 * b + std::sqrt(d)) / (10 * c));
+    at((-3 * b - std::sqrt(d)) / (10 * c));
+  }
+  return top * 1.01;
+}
+double largest_factor(double b, double c, double s) {
+  auto f = [&](double square) { return std::fabs((b + c * square) * square); };
+  double top = f(s * s);
+  if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < s * s) top = std::max(top, f(-b / (2 * c)));
+  return top * 1.01;
+}
+
+// The exponent that brings values up to `bound` to 2^14 (a quarter of fp16's
+// range: the bound is exact arithmetic's).
+int exponent(double bound) {
+  int e = 0;
+  if (bound > 0 && std::isfinite(bound)) std::frexp(bound, &e);
+  return std::min(60, std::max(-60, 14 - e));
 }
 
 template <class T, int P>
 void run(const Plan &p, const Input &in, int batch, int steps, float a, float b, float c, float eps,
          void *o, int64_t ldo, int64_t stride_o, char *ws, hipStream_t s) {
   double *norm = reinterpret_cast<double *>(ws);
-  uint16_t *x[2] = {reinterpret_cast<uint16_t *>(ws + p.norm_bytes),
-                    reinterpret_cast<uint16_t *>(ws + p.norm_bytes + p.x_bytes)};
-  uint16_t *A = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes);
-  uint16_t *B = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes + p.a_bytes);
   const bool tall = in.m > in.n;
+  const int64_t lda = P * p.rp, ab = p.r * lda;
+  Wide<P> x[2];
+  for (int i = 0; i < 2; ++i) {
+    x[i].p = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + i * p.x_bytes);
+    x[i].ld = P * p.kp;
+    x[i].batch = p.r * x[i].ld;
+    x[i].plane = batch * x[i].batch;
+    x[i].width = (int)p.kp;
+  }
+  Square<P> A{reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes), lda, ab};
+  Square<P> B{reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes + p.a_bytes), lda, ab};
+  double top = 1;  // of X's singular values
+  int ex = exponent(top);
   const int blocks = std::min(kNormBlocks, in.m);
   hipLaunchKernelGGL(norm_kernel<T>, dim3(blocks, batch), dim3(256), 0, s, in, norm);
   const dim3 grid((unsigned)(p.kp / 64), (unsigned)(p.rp / 64), batch);
+  const float first = std::ldexp(1.0f, ex);
   if (tall)
     hipLaunchKernelGGL((pack_kernel<T, P, true>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       x[0], P * p.kp);
+                       first, x[0]);
   else
     hipLaunchKernelGGL((pack_kernel<T, P, false>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       x[0], P * p.kp);
-  const int64_t ldx = P * p.kp, lda = P * p.rp, xb = p.r * ldx, ab = p.r * lda;
+                       first, x[0]);
   for (int i = 0; i < steps; ++i) {
-    uint16_t *from = x[i & 1], *to = i + 1 < steps ? x[(i + 1) & 1] : nullptr;
-    const Operand X{from, ldx, xb}, OA{A, lda, ab}, OB{B, lda, ab};
-    product<P, false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0, 0},
-                                     SymArgs{A, nullptr, lda, ab, 0, 0}, batch, s);
-    product<P, false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0, 0},
-                                     SymArgs{B, A, lda, ab, b, c}, batch, s);
-    product<P, false, true, Next<P, T>>(Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0, 0},
-                                        NextArgs{from, to, ldx, xb, a, o, ldo, stride_o, tall},
-                                        batch, s);
+    const Wide<P> &from = x[i & 1], &to = x[(i + 1) & 1];
+    const bool last = i + 1 == steps;
+    const int ea = exponent(top * top);
+    const int eb = exponent(largest_factor(b, c, top));
+    const double next = largest_next(a, b, c, top);
+    const int en = last ? 0 : exponent(next);
+    const Operand X{from.p, from.ld, from.batch}, OA{A.p, lda, ab}, OB{B.p, lda, ab};
+    product<_Float16, P, false, false, Sym<P>>(
+        Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0, 0},
+        SymArgs<P>{A, Square<P>{nullptr, 0, 0}, 0, std::ldexp(1.0f, ea - 2 * ex)}, batch, s);
+    product<_Float16, P, false, false, Sym<P>>(
+        Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0, 0},
+        SymArgs<P>{B, A, std::ldexp(b, eb - ea), std::ldexp(c, eb - 2 * ea)}, batch, s);
+    product<_Float16, P, false, true, Next<P, T>>(
+        Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0, 0},
+        NextArgs<P>{from, to, std::ldexp(a, en - ex), std::ldexp(1.0f, en - eb - ex),
+                    last ? o : nullptr, ldo, stride_o, tall},
+        batch, s);
+    top = next;
+    ex = en;
   }
 }
 
@@ -332,10 +413,13 @@ og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, i
   if ((st = check_device()) != OG_OK) return st;
   const og::ns::Input in{G, ldg, strideg, (int)m, (int)n};
   if (type == OG_F32)
-    og::ns::run<float, 3>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+    og::ns::run<float, 2>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
                           static_cast<char *>(workspace), current_stream());
-  else
+  else if (p.planes == 2)
     og::ns::run<__bf16, 2>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+                           static_cast<char *>(workspace), current_stream());
+  else
+    og::ns::run<__bf16, 1>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
                            static_cast<char *>(workspace), current_stream());
   return check_launch("newton_schulz");
 }

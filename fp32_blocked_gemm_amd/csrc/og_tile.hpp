@@ -1,18 +1,20 @@
-// og_tile.hpp -- the bf16 matrix-core tile product the language-model
+// og_tile.hpp -- the 16-bit matrix-core tile product the language-model
 // operators share: acc[m][n] = sum over k of A(m, k) * B(n, k), fp32 sums,
 // with the operator's own epilogue on the finished tile.
 //
-// Operands are bf16 planes.  A bf16 matrix is one plane; an fp32 matrix is
-// held as two or three planes h + m (+ l), each the rounding to bf16 of what
-// the planes before it leave (8 bits each: two planes carry 16 bits, three
-// all 24), and a product of two such matrices is the sum of the plane
-// products hh, hm, mh (two planes) and mm, hl, lh too (three), in the same
-// accumulators.  Three planes leave out terms of 2^-24 relative and below:
-// the error of an fp32 product, at a sixth of the bf16 matrix-core rate (417
-// TFLOP/s of the nominal peak) where the fp32 matrix cores have 157.  Planes
-// are interleaved by blocks of 32 columns: element (r, c) of plane p of P lies
-// at r ld + 32 (P (c / 32) + p) + c % 32, so that a stage's k of one row is
-// one run in memory, whatever P.
+// Operands are bf16, or fp16 times a power of two.  An fp32 matrix is held as
+// two fp16 planes h + l, l the rounding of what h leaves (22 bits in all, the
+// last of them 2^-38 of the matrix's or row's largest at the least), and a
+// product of two such matrices is the sum of the plane products hh, hl and lh
+// in the same accumulators: it leaves out terms of 2^-22 and below, each a
+// rounding of its own, which is less than what the fp32 additions lose from a
+// few dozen terms on (errors measured: those of fp32 products or below), at a
+// third of the 16-bit matrix-core rate (830 TFLOP/s of the nominal peak) where
+// the fp32 matrix cores have 157.  bf16 planes would need no scale but three
+// planes and six products for the same bits (measured 1.5 to 2 times the
+// time).  Planes are interleaved by blocks of 32 columns: element (r, c) of
+// plane p of two lies at r ld + 32 (2 (c / 32) + p) + c % 32, so that a stage's
+// k of one row is one run in memory.
 //
 // An operand is stored with k contiguous (rows of m, "plain") or with m
 // contiguous (rows of k, "transposed"); both are loaded straight into LDS
@@ -47,6 +49,9 @@ namespace og::tile {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -58,7 +63,7 @@ constexpr uint32_t kOutside = kRange;     // an offset at or past the range: the
 // k of one stage.
 constexpr int depth(int planes) { return planes == 1 ? 64 : 32; }
 
-// One operand: bf16 elements, ld and batch in elements.  ld is a multiple of 8
+// One operand: 16-bit elements, ld and batch in elements.  ld is a multiple of 8
 // and p 16-byte aligned; the elements between a row's length and the next
 // multiple of 8 are zero (plain) or readable (transposed).  Planes: rows of
 // whole blocks of 32.
@@ -84,8 +89,18 @@ __device__ __forceinline__ int64_t column(int c, int p) {
 }
 
 // The plane products: product i is of plane kPlaneA[i] of A and kPlaneB[i] of B.
-constexpr int plane_products(int planes) { return planes == 1 ? 1 : planes == 2 ? 3 : 6; }
-constexpr int kPlaneA[6] = {0, 0, 1, 1, 0, 2}, kPlaneB[6] = {0, 1, 0, 1, 2, 0};
+constexpr int plane_products(int planes) { return planes == 1 ? 1 : 3; }
+constexpr int kPlaneA[3] = {0, 0, 1}, kPlaneB[3] = {0, 1, 0};
+
+template <class E>
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
+  if constexpr (__is_same(E, __bf16))
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 buffer_of(const uint16_t *base) {
@@ -106,15 +121,14 @@ __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t off, u32x4 rs
 
 // The swizzles (see the top): the slot permutation of a plain row, and the
 // unit permutation of row k of BX transposed columns.
-template <int P>
 __device__ __forceinline__ int slots(int row) {
-  return P == 3 ? ((row >> 3) & 1) << 1 : ((row >> 1) & 1) << 2 | ((row >> 3) & 1) << 1;
+  return ((row >> 1) & 1) << 2 | ((row >> 3) & 1) << 1;
 }
 template <int BX, int P>
 __device__ __forceinline__ int hash(int k) {
+  static_assert(BX * P * 2 % 128 == 0, "whole groups of four units");
   // rows that are not a multiple of 256 bytes alternate between the bank halves by themselves
-  // (those of 64 and 192 bytes hold whole pairs of units only)
-  return BX * P * 2 % 128 ? (k >> 3) & 1 : BX * P * 2 % 256 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+  return BX * P * 2 % 256 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
 }
 
 // Loads one operand's stages: BX rows of m by depth(P) of k, P planes.
@@ -124,32 +138,49 @@ struct Stager {
   static constexpr int kLoads = kBytes / (NW * 1024);  // 1 KiB per wave and load
   static_assert(kLoads * NW * 1024 == kBytes, "whole loads");
   // 16-byte granules of a row of LDS
-  static constexpr int kRow = T ? BX * P / 8 : P == 1 ? 8 : 4 * P;
-  uint32_t off[kLoads];
-  int kpos[kLoads];  // the k of the stage that a load's lane brings
+  static constexpr int kRow = T ? BX * P / 8 : 8;
+  // The k of the stage that a load's lane brings: for plain rows that of the
+  // first load (the swizzle repeats), for transposed ones kStep further a load
+  // where the waves' loads are whole rows.
+  static constexpr bool kVary = T && NW * 64 % kRow != 0;
+  static constexpr int kStep = T ? NW * 64 / kRow : 0;
+  static_assert(NW % 2 == 0, "a plain load's rows of 8 have one parity");
+  // Offsets kept: each load's; of whole rows one, or two where bit 3 of the row
+  // (in the hash) alternates from load to load.
+  static constexpr bool kEach = !T || kVary;
+  static constexpr int kOffs = kEach ? kLoads : kStep % 16 == 0 ? 1 : 2;
+  static_assert(kEach || kStep % 8 == 0, "the hash repeats every second load at the latest");
+  uint32_t off[kOffs];
+  int kpos[kVary ? kLoads : 1];
   int wave;
+  uint32_t step;  // bytes from one load's rows to the next's
 
   __device__ __forceinline__ void init(const Operand &o, int x0, int X, int w, int lane) {
     wave = w;
+    step = (uint32_t)(kStep * (int)o.ld) * 2u;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
+    for (int j = 0; j < kOffs; ++j) {
       const int at = (j * NW + w) * 64 + lane, row = at / kRow, s = at % kRow;
       if constexpr (!T) {
-        const int g = P == 3 ? (s & ~3) | ((s & 3) ^ slots<P>(row)) : s ^ slots<P>(row);
-        kpos[j] = (P == 1 ? g : g & 3) * 8;
+        const int g = s ^ slots(row);
+        if (j == 0) kpos[0] = (P == 1 ? g : g & 3) * 8;
         off[j] = (uint32_t)(min(row, X - 1 - x0) * (int)o.ld) * 2u + g * 16;
       } else {
         const int u = (s >> 1) ^ hash<BX, P>(row);  // 16 columns of one plane
         const int c = P == 1 ? u * 16 + (s & 1) * 8 : u / (2 * P) * 32;
-        kpos[j] = row;
-        off[j] = x0 + c < X ? (uint32_t)(row * (int)o.ld) * 2u + u * 32 + (s & 1) * 16 : kOutside;
+        if (kVary || j == 0) kpos[kVary ? j : 0] = row;
+        off[j] = (uint32_t)(row * (int)o.ld) * 2u + u * 32 + (s & 1) * 16;
+        if (x0 + c >= X) off[j] = kOutside;
       }
     }
   }
   // load j of a stage; rs: the tile's first row (plain) or column (transposed) at its first k,
   // of which `left` remain
   __device__ __forceinline__ void issue(int j, uint32_t lds, u32x4 rs, int left) const {
-    load_to_lds(lds + (j * NW + wave) * 1024, kpos[j] < left ? off[j] : kOutside, rs);
+    uint32_t o;
+    if constexpr (kEach) o = kpos[kVary ? j : 0] < left ? off[j] : kOutside;
+    else o = off[j % kOffs] != kOutside && kpos[0] < left - j * kStep ? off[j % kOffs] + (j / kOffs * kOffs) * step : kOutside;
+    load_to_lds(lds + (j * NW + wave) * 1024, o, rs);
   }
 };
 
@@ -162,7 +193,7 @@ struct Reader {
   __device__ __forceinline__ void init(int x, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (!T) {
-      base = (x + i) * (P == 3 ? 192 : 128) + ((g ^ slots<P>(i)) * 16);
+      base = (x + i) * 128 + ((g ^ slots(i)) * 16);
     } else {
       const int k = 8 * g + (i >> 2);
       base = k * BX * P * 2 + (i & 3) * 8;
@@ -171,18 +202,15 @@ struct Reader {
     }
   }
   // fragment `f` of the wave's rows; b: the k half of the stage (one plane) or the plane
-  __device__ __forceinline__ bf16x8 read(const char *lds, int f, int b) const {
+  __device__ __forceinline__ s16x8 read(const char *lds, int f, int b) const {
     if constexpr (!T) {
-      const int at = P == 3 ? base + b * 64 : base ^ (b << 6);
-      return *reinterpret_cast<const bf16x8 *>(lds + at + f * (P == 3 ? 3072 : 2048));
+      return *reinterpret_cast<const s16x8 *>(lds + (base ^ (b << 6)) + f * 2048);
     } else {
       const int c = unit + f, u = P == 1 ? c : (c >> 1) * 2 * P + b * 2 + (c & 1);
       const int at = base + ((u << 5) ^ swz) + (P == 1 ? b * 32 * BX * 2 : 0);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at + 8 * BX * P));
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      return __builtin_bit_cast(bf16x8, v);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
 };
@@ -197,10 +225,11 @@ struct Place {
   char *lds;     // the block's stages, free once every wave has passed a barrier
 };
 
-// A tile of BM x BN by WM x WN waves, NST stages of P planes in LDS; BLOCKS: blocks a compute
-// unit is to hold (the register budget).
-template <int P_, int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
+// A tile of BM x BN by WM x WN waves, elements E, NST stages of P planes in LDS; BLOCKS: blocks a
+// compute unit is to hold (the register budget).
+template <class E_, int P_, int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
 struct Shape {
+  using E = E_;
   static constexpr int P = P_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, BLOCKS = BLOCKS_;
   static constexpr int NW = WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int kWavesPerSimd = BLOCKS * NW > 4 ? BLOCKS * NW / 4 : 1;
@@ -315,7 +344,7 @@ __global__ __launch_bounds__(S::NW * 64, S::kWavesPerSimd) void tile_kernel(Args
       next_stage();
     };
     if constexpr (P == 1) {
-      bf16x8 fa[4], fb[2][FN];  // rows of A: a ring; columns of B: two halves
+      s16x8 fa[4], fb[2][FN];  // rows of A: a ring; columns of B: two halves
 #pragma unroll
       for (int j = 0; j < FN; ++j) fb[0][j] = rb.read(lb, j, 0);
 #pragma unroll
@@ -347,12 +376,12 @@ __global__ __launch_bounds__(S::NW * 64, S::kWavesPerSimd) void tile_kernel(Args
             }
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[(h * FM + i) % 4], acc[i][j], 0, 0, 0);
+              acc[i][j] = mfma<typename S::E>(fb[h][j], fa[(h * FM + i) % 4], acc[i][j]);
           }
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      bf16x8 fa[2][P], fb[2][FN][P];  // rows of A in turn; columns of B by stage
+      s16x8 fa[2][P], fb[2][FN][P];  // rows of A in turn; columns of B by stage
 #pragma unroll
       for (int p = 0; p < P; ++p) {
 #pragma unroll
@@ -386,7 +415,7 @@ __global__ __launch_bounds__(S::NW * 64, S::kWavesPerSimd) void tile_kernel(Args
             for (int q = 0; q < plane_products(P); ++q)
 #pragma unroll
               for (int j = 0; j < FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j][kPlaneB[q]], fa[i & 1][kPlaneA[q]], acc[i][j], 0, 0, 0);
+                acc[i][j] = mfma<typename S::E>(fb[h][j][kPlaneB[q]], fa[i & 1][kPlaneA[q]], acc[i][j]);
           }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -430,34 +459,30 @@ struct Choices {};
 
 // The tiles by number of planes.  Large ones reuse each loaded value more
 // often (a compute unit loads about 30 bytes a cycle at most), small ones
-// spread a small product over more compute units; symmetric products need
-// square tiles.
-template <int P, bool SYM>
+// spread a small product over more compute units.  Symmetric products need
+// square tiles; with both operands transposed two planes of 256 x 256 need
+// more registers than there are.
+template <class E, int P, bool TT>
 struct Tiles {
-  using type = Choices<Choice<Shape<1, 256, 256, 2, 4, 2, 1>, 1400, 1700>,
-                       Choice<Shape<1, 128, 128, 2, 2, 2, 2>, 500, 510>,
-                       Choice<Shape<1, 64, 64, 2, 2, 4, 2>, 210, 220>>;
+  using type = Choices<Choice<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 1400, 1700>,
+                       Choice<Shape<E, 1, 192, 192, 2, 4, 3, 1>, 900, 1100>,
+                       Choice<Shape<E, 1, 128, 128, 2, 2, 2, 2>, 500, 510>,
+                       Choice<Shape<E, 1, 64, 64, 2, 2, 4, 2>, 210, 220>>;
 };
-template <bool SYM>
-struct Tiles<2, SYM> {
-  using type = Choices<Choice<Shape<2, 256, 256, 2, 4, 2, 1>, 1300, 2250>,
-                       Choice<Shape<2, 192, 192, 2, 4, 3, 1>, 1150, 1250>,
-                       Choice<Shape<2, 128, 128, 2, 4, 2, 2>, 660, 630>,
-                       Choice<Shape<2, 64, 64, 2, 2, 4, 2>, 226, 230>,
-                       Choice<Shape<2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
+template <class E>
+struct Tiles<E, 2, true> {
+  using type = Choices<Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 1150, 1420>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 660, 630>,
+                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 226, 230>,
+                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
 };
-template <>
-struct Tiles<3, false> {
-  using type = Choices<Choice<Shape<3, 128, 256, 2, 4, 2, 1>, 2400, 2500>,
-                       Choice<Shape<3, 128, 128, 2, 4, 3, 1>, 1400, 1280>,
-                       Choice<Shape<3, 64, 64, 2, 2, 3, 2>, 340, 430>,
-                       Choice<Shape<3, 32, 32, 1, 2, 3, 4>, 225, 195>>;
-};
-template <>
-struct Tiles<3, true> {
-  using type = Choices<Choice<Shape<3, 128, 128, 2, 4, 3, 1>, 1400, 1280>,
-                       Choice<Shape<3, 64, 64, 2, 2, 3, 2>, 340, 430>,
-                       Choice<Shape<3, 32, 32, 1, 2, 3, 4>, 225, 195>>;
+template <class E>
+struct Tiles<E, 2, false> {
+  using type = Choices<Choice<Shape<E, 2, 256, 256, 2, 4, 2, 1>, 1300, 2250>,
+                       Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 1150, 1420>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 660, 630>,
+                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 226, 230>,
+                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
 };
 
 // Runs a product on the tile with the least time; returns the number of tile
@@ -478,26 +503,20 @@ double least(Choices<C...>, bool sym, const Args &g, int batch) {
   const int64_t k = g.k_split ? g.k_split : g.K;
   return std::min({C::time(sym, g.M, g.N, k, batch)...});
 }
-template <int P, bool TA, bool TB, class Epi>
+template <class E, int P, bool TA, bool TB, class Epi>
 int product(const Args &g, const typename Epi::Args &e, int batch, hipStream_t s) {
-  using T = typename Tiles<P, Epi::kSymmetric>::type;
+  using T = typename Tiles<E, P, TA && TB>::type;
   return product_of<TA, TB, Epi>(T(), least(T(), Epi::kSymmetric, g, batch), g, e, batch, s);
 }
 
-// Planes of four fp32 values: each plane rounds what is left to bf16.  A
-// value that is not finite stays in the first plane alone.
-template <int P>
-__device__ __forceinline__ void split4(const f32x4 v, bf16x4 (&out)[P]) {
+// The fp16 planes of four values (scaled by the caller): the second rounds
+// what the first leaves; a value that is not finite stays in the first.
+__device__ __forceinline__ void split4(const f32x4 v, f16x4 &h, f16x4 &l) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float r = v[e];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const __bf16 h = (__bf16)r;
-      out[p][e] = h;
-      const float d = r - (float)h;
-      r = __builtin_isfinite((float)h) ? d : 0.0f;
-    }
+    h[e] = (_Float16)v[e];
+    const float d = v[e] - (float)h[e];
+    l[e] = (_Float16)(__builtin_isfinite((float)h[e]) ? d : 0.0f);
   }
 }
 

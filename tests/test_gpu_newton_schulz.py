@@ -111,8 +111,8 @@ def test_orthogonal_in_the_limit():
     # the last step's own errors, and half of the error before it is kept (p'(1) = 0 for the
     # stretch, 1 for a rotation, which leaves X X^T as it is)
     a = x.abs()
-    local = ref.sum_error(200, 3) * (a @ a.t()).norm() * 0.5 + ref.sum_error(48, 3) * a.norm() * 48 ** 0.5 + \
-        4 * 2.0 ** -24 * a.norm()
+    local = ref.sum_error(200, 2) * (a @ a.t()).norm() * 0.5 + ref.sum_error(48, 2) * a.norm() * 48 ** 0.5 + \
+        (2.0 ** -22 + 4 * 2.0 ** -24) * a.norm() + (2.0 ** -22 + ref.LAST * 48) * 48 ** 0.5
     assert off <= 2 * 2 * local
 
 
