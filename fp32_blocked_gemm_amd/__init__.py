@@ -303,9 +303,14 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0, 0, 0), dil=(1, 1), groups=1, mode="ex
 # Operators of language models around the N x K product.
 # ---------------------------------------------------------------------------
 
+_TYPES = {}
+
+
 def _type(t, allowed=(F32, BF16)) -> int:
-    torch = _torch()
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if not _TYPES:
+        torch = _torch()
+        _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    code = _TYPES.get(t.dtype)
     if code not in allowed:
         names = ", ".join(("float32", "bfloat16", "float16")[a] for a in allowed)
         raise ValueError(f"a tensor of {t.dtype}: {names} expected")
@@ -320,6 +325,20 @@ def _one_device(*ts):
         if t.device != dev:
             raise ValueError("tensors must be on one device")
     return dev
+
+
+def _run(dev, call, *args):
+    """Calls the library on the current stream of `dev` (which it makes the current device
+    where it is not)."""
+    torch = _torch()
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(dev, call, *args)
+    L = lib()
+    L.og_set_stream(torch._C._cuda_getCurrentRawStream(dev.index))
+    status = call(*args)
+    if status != OG_OK:
+        _check(status)
 
 
 def _workspace(nbytes, workspace, dev):
@@ -360,13 +379,9 @@ def gemm_nt_q4(A, Q, scales, zeros=None, group=128, out=None):
     if tuple(out.shape) != (m, n) or out.dtype != A.dtype:
         raise ValueError("out must be [m, n] of A's type")
     dev = _one_device(A, Q, scales, out, *([] if zeros is None else [zeros]))
-    with torch.cuda.device(dev):
-        _use_stream_of(out)
-        _check(lib().og_gemm_nt_q4(m, n, k, A.data_ptr(), code, _ld(A), Q.data_ptr(), _ld(Q),
-                                   scales.data_ptr(), scode, _ld(scales),
-                                   None if zeros is None else zeros.data_ptr(),
-                                   0 if zeros is None else _ld(zeros), group, out.data_ptr(),
-                                   _ld(out)))
+    _run(dev, lib().og_gemm_nt_q4, m, n, k, A.data_ptr(), code, _ld(A), Q.data_ptr(), _ld(Q),
+         scales.data_ptr(), scode, _ld(scales), None if zeros is None else zeros.data_ptr(),
+         0 if zeros is None else _ld(zeros), group, out.data_ptr(), _ld(out))
     return out
 
 
@@ -402,15 +417,12 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
             g3, o3 = G.view(batch, m, n), out.view(batch, m, n)
         except RuntimeError:
             raise ValueError("the leading dimensions must reduce to one batch stride") from None
-    with torch.cuda.device(dev):
-        _use_stream_of(out)
-        ws = _workspace(int(lib().og_newton_schulz_workspace(batch, m, n, code)), workspace, dev)
-        a, b, c = coeffs
-        rows_g, rows_o = _ld(g3[0]) if batch else max(1, n), _ld(o3[0]) if batch else max(1, n)
-        _check(lib().og_newton_schulz(batch, m, n, g3.data_ptr(), rows_g,
-                                      g3.stride(0) if batch > 1 else 0, code, steps, a, b, c, eps,
-                                      o3.data_ptr(), rows_o, o3.stride(0) if batch > 1 else 0,
-                                      ws.data_ptr(), ws.numel()))
+    ws = _workspace(lib().og_newton_schulz_workspace(batch, m, n, code), workspace, dev)
+    a, b, c = coeffs
+    rows_g, rows_o = _ld(g3[0]) if batch else max(1, n), _ld(o3[0]) if batch else max(1, n)
+    _run(dev, lib().og_newton_schulz, batch, m, n, g3.data_ptr(), rows_g,
+         g3.stride(0) if batch > 1 else 0, code, steps, a, b, c, eps, o3.data_ptr(), rows_o,
+         o3.stride(0) if batch > 1 else 0, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -452,14 +464,10 @@ def linear_cross_entropy(X, W, target, ignore_index=-100, loss=None, lse=None, w
     _vector(loss, n, torch.float32, "loss")
     _vector(lse, n, torch.float32, "lse")
     dev = _one_device(X, W, target, loss, lse)
-    with torch.cuda.device(dev):
-        _use_stream_of(X)
-        ws = _workspace(int(lib().og_linear_cross_entropy_workspace(n, v, d, code, 0)), workspace,
-                        dev)
-        _check(lib().og_linear_cross_entropy(n, v, d, X.data_ptr(), _ld(X), W.data_ptr(), _ld(W),
-                                             code, target.data_ptr(), ignore_index,
-                                             loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                             ws.numel()))
+    ws = _workspace(lib().og_linear_cross_entropy_workspace(n, v, d, code, 0), workspace, dev)
+    _run(dev, lib().og_linear_cross_entropy, n, v, d, X.data_ptr(), _ld(X), W.data_ptr(), _ld(W),
+         code, target.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+         ws.numel())
     return loss, lse
 
 
@@ -482,12 +490,8 @@ def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=No
     given = [t for t in outs if t is not None]
     dev = _one_device(X, W, target, lse, dloss, *given)
     args = [p for t in outs for p in ((None, 0) if t is None else (t.data_ptr(), _ld(t)))]
-    with torch.cuda.device(dev):
-        _use_stream_of(X)
-        ws = _workspace(int(lib().og_linear_cross_entropy_workspace(n, v, d, code, 1)), workspace,
-                        dev)
-        _check(lib().og_linear_cross_entropy_grad(n, v, d, X.data_ptr(), _ld(X), W.data_ptr(),
-                                                  _ld(W), code, target.data_ptr(), ignore_index,
-                                                  lse.data_ptr(), dloss.data_ptr(), *args,
-                                                  ws.data_ptr(), ws.numel()))
+    ws = _workspace(lib().og_linear_cross_entropy_workspace(n, v, d, code, 1), workspace, dev)
+    _run(dev, lib().og_linear_cross_entropy_grad, n, v, d, X.data_ptr(), _ld(X), W.data_ptr(),
+         _ld(W), code, target.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(), *args,
+         ws.data_ptr(), ws.numel())
     return tuple(outs)

@@ -84,39 +84,44 @@ __device__ __forceinline__ f16x2 codes(uint32_t w, f16x2 minus_zero) {
   return __builtin_bit_cast(f16x2, b) + minus_zero;
 }
 
-// 32 codes of a row from k on (k a multiple of 32): one 16-byte load, or, FULL
-// false, single bytes up to the end of the row and zero past it.
+// 16 bytes of a row of `size` (at least 16) from byte `at` on; FULL false: zero
+// past its end, by loading its last 16 bytes and shifting.  (No branch holds
+// the loads of a piece apart.)
 template <bool FULL>
-__device__ __forceinline__ u32x4 load_codes(const uint8_t *row, int k, int K) {
-  u32x4 w = {0, 0, 0, 0};
-  const int at = k >> 1;
+__device__ __forceinline__ u32x4 load16(const uint8_t *row, int at, int size) {
+  u32x4 w;
   if constexpr (FULL) {
     __builtin_memcpy(&w, row + at, 16);
   } else {
-    const int bytes = (K + 1) >> 1;
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (at + 4 * d + b < bytes) w[d] |= (uint32_t)row[at + 4 * d + b] << (8 * b);
+    const int from = min(at, size - 16), past = 8 * (at - from);
+    unsigned __int128 v;
+    __builtin_memcpy(&v, row + from, 16);
+    v = past < 128 ? v >> past : 0;
+    __builtin_memcpy(&w, &v, 16);
   }
   return w;
+}
+
+// 32 codes of a row from k on (k a multiple of 32).
+template <bool FULL>
+__device__ __forceinline__ u32x4 load_codes(const uint8_t *row, int k, int K) {
+  return load16<FULL>(row, k >> 1, (K + 1) >> 1);
 }
 
 template <class T>
 struct Eight {
   T v[8];
 };
-// Eight activations of a row from k on; FULL false: zero past its end.
+// Eight activations of a row from k on.
 template <class T, bool FULL>
 __device__ __forceinline__ Eight<T> load8(const T *row, int k, int K) {
   Eight<T> t;
-  if constexpr (FULL) {
-    __builtin_memcpy(&t, row + k, sizeof t);
-  } else {
+  u32x4 w[sizeof t / 16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t.v[e] = k + e < K ? row[k + e] : (T)0.0f;
-  }
+  for (int i = 0; i < (int)sizeof t / 16; ++i)
+    w[i] = load16<FULL>(reinterpret_cast<const uint8_t *>(row), k * (int)sizeof(T) + 16 * i,
+                        K * (int)sizeof(T));
+  __builtin_memcpy(&t, w, sizeof t);
   return t;
 }
 
@@ -380,6 +385,25 @@ __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
   }
 }
 
+// Rows of fewer than 31 codes (16 bytes): a thread an output.
+template <class T>
+__global__ __launch_bounds__(256) void short_kernel(Problem p) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(at / p.n), n = (int)(at - (int64_t)m * p.n);
+  if (m >= p.m) return;
+  const T *a = static_cast<const T *>(p.a) + m * p.lda;
+  const uint8_t *q = p.q + n * p.ldq;
+  float sum = 0, s = 0;  // (a single group: p.group >= 32 > k)
+  if (p.k > 0) {
+    Group g;
+    g.load(p, n, 0);
+    s = g.scale(p.s_type);
+    for (int k = 0; k < p.k; ++k)
+      sum = fmaf((float)((int)(q[k >> 1] >> (4 * (k & 1)) & 15) - (int)g.z), (float)a[k], sum);
+  }
+  static_cast<T *>(p.c)[m * p.ldc + n] = (T)(s * sum);
+}
+
 template <class T, int M, int R>
 void run_rows(const Problem &p, hipStream_t s) {
   const int groups = (p.n + R - 1) / R;
@@ -402,11 +426,16 @@ void run_blocks(const Problem &p, hipStream_t s) {
 
 template <class T>
 void run(const Problem &p, hipStream_t s) {
+  if (p.k < 31) {
+    const int64_t blocks = ((int64_t)p.m * p.n + 255) / 256;
+    hipLaunchKernelGGL(short_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+    return;
+  }
   if (p.m == 1) return run_rows<T, 1, 4>(p, s);
   if (p.m == 2) return run_rows<T, 2, 4>(p, s);
   if (p.m == 3) return run_rows<T, 3, 4>(p, s);
   if (p.m == 4) return run_rows<T, 4, 4>(p, s);
-  if (p.m <= 16) return run_blocks<T, 16, 1>(p, s);
+  if (p.m <= 16) return run_blocks<T, sizeof(T) == 4 ? 8 : 16, 1>(p, s);
   return run_blocks<T, 8, 2>(p, s);
 }
 
@@ -432,9 +461,11 @@ extern "C" og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *
     return fail(OG_ERR_INVALID_ARG, "a row stride is below its row: lda %lld, ldq %lld, lds %lld, "
                 "ldz %lld, ldc %lld", (long long)lda, (long long)ldq, (long long)lds, (long long)ldz,
                 (long long)ldc);
-  if (m > (1 << 19) || n > (1 << 30) || k > (1 << 30) || group > (1 << 30))
-    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld, k %lld or group %lld: at most 2^19, 2^30, 2^30, 2^30",
+  if (m > (1 << 19) || n > (1 << 30) || k > (1 << 28) || group > (1 << 30))
+    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld, k %lld or group %lld: at most 2^19, 2^30, 2^28, 2^30",
                 (long long)m, (long long)n, (long long)k, (long long)group);
+  if (m * n > (int64_t(1) << 38))
+    return fail(OG_ERR_TOO_LARGE, "%lld x %lld outputs: at most 2^38", (long long)m, (long long)n);
   if (m == 0 || n == 0) return ok();
   if (!C || (k > 0 && (!A || !Q || !S))) return fail(OG_ERR_INVALID_ARG, "a null pointer");
   og_status st = check_device();

@@ -313,8 +313,8 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
  * Requirements: m, n, k >= 0; group a multiple of 32, >= 32; lda >= max(1,k),
  * ldq >= max(1, ceil(k/2)), lds and ldz >= max(1, ceil(k/group)), ldc >=
  * max(1,n); pointers non-null as in og_gemm_f32.  m or n 0: nothing is done;
- * k == 0: every output is +0.  OG_ERR_TOO_LARGE when m exceeds 2^19 or n, k
- * or group 2^30.  No workspace.
+ * k == 0: every output is +0.  OG_ERR_TOO_LARGE when m exceeds 2^19, n or
+ * group 2^30, k 2^28 or m*n 2^38.  No workspace.
  */
 og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *A, int type, int64_t lda,
                         const uint8_t *Q, int64_t ldq, const void *S, int scale_type, int64_t lds,

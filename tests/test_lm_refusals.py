@@ -44,7 +44,8 @@ def test_q4_rejects_before_launch(L, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(m=(1 << 19) + 1), dict(n=(1 << 30) + 1, ldc=1 << 31),
-                                dict(k=(1 << 30) + 1, lda=1 << 31, ldq=1 << 30, lds=1 << 30)])
+                                dict(k=(1 << 28) + 1, lda=1 << 31, ldq=1 << 30, lds=1 << 30),
+                                dict(m=1 << 19, n=1 << 30, ldc=1 << 30)])
 def test_q4_too_large(L, kw):
     assert _q4(L, **kw) == og.OG_ERR_TOO_LARGE
 
