@@ -365,6 +365,22 @@ struct Grad {
   }
 };
 
+// Up to four values of a row.
+template <class T>
+__device__ __forceinline__ void store4(T *to, const f32x4 v, int left, bool whole) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  T4 h;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) h[q] = (T)v[q];
+  if (whole && left >= 4) {
+    *reinterpret_cast<T4 *>(to) = h;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < left) to[q] = h[q];
+  }
+}
+
 // Epilogue of dX and dW.  The sum so far (dX, over the pieces) is kept in fp32
 // and rounded once, with the last piece; a product whose k is split stores its
 // parts for join_kernel.
@@ -375,6 +391,7 @@ struct OutArgs {
   int first, last;
   void *out;
   int64_t ldo;
+  int whole;       // four values of a row of out are one aligned store
   const int *row;  // null: row m is row m of out
   const int *exp;  // fp32: the exponents of the rows, less the common one
   const int *most;
@@ -409,13 +426,8 @@ struct Out {
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] += was[q];
         }
-        if (!e.last) {
-          *reinterpret_cast<f32x4 *>(sum + n) = v;
-          continue;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < t.N) to[n + q] = (T)v[q];
+        if (!e.last) *reinterpret_cast<f32x4 *>(sum + n) = v;
+        else store4(to + n, v, t.N - n, e.whole);
       }
     }
   }
@@ -427,7 +439,7 @@ template <class T>
 __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, const int *count, int parts,
                                                    const float *from, int64_t part, float *sum,
                                                    int64_t lds, int first, int last, T *out,
-                                                   int64_t ldo, const int *row) {
+                                                   int64_t ldo, int whole, const int *row) {
   const int per = (cols + 3) / 4;
   if (count) rows = *count;
   const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * 256;
@@ -440,14 +452,8 @@ __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, const int
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += w[q];
     }
-    if (!last) {
-      *reinterpret_cast<f32x4 *>(sum + m * lds + n) = v;
-      continue;
-    }
-    T *to = out + (row ? row[m] : m) * ldo;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (n + q < cols) to[n + q] = (T)v[q];
+    if (!last) *reinterpret_cast<f32x4 *>(sum + m * lds + n) = v;
+    else store4(out + (row ? row[m] : m) * ldo + n, v, cols - n, whole);
   }
 }
 
@@ -475,7 +481,7 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   Plan p;
   p.planes = type == OG_F32 ? 2 : 1;
   p.dp = round_up(d, 64);
-  const int64_t most = (int64_t(1) << 25) / std::max(n, p.dp) / 256 * 256;
+  const int64_t most = (int64_t(1) << 26) / std::max(n, p.dp) / 256 * 256;
   p.piece = std::min(round_up(v, 256), std::max<int64_t>(2048, most));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -592,12 +598,18 @@ void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s)
   }
   float *from = reinterpret_cast<float *>(ws);
   g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, nullptr, o.exp, o.most};
+  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, 0, nullptr, o.exp, o.most};
   product<Element<T>, P, TA, true, Out<T>>(g, part, parts, s);
   const int64_t quads = (int64_t)g.M * ((g.N + 3) / 4);
   hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
                      dim3(256), 0, s, g.M, g.N, g.count_is_k ? nullptr : g.count, parts, from,
-                     part.part, o.sum, o.lds, o.first, o.last, static_cast<T *>(o.out), o.ldo, o.row);
+                     part.part, o.sum, o.lds, o.first, o.last, static_cast<T *>(o.out), o.ldo, o.whole,
+                     o.row);
+}
+
+template <class T>
+int whole(const T *p, int64_t ld) {
+  return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
 }
 
 template <class T, int P>
@@ -626,12 +638,13 @@ void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss
       if (dx)
         summed<T, P, false>(Args{G, W, n, d, rows, r.count, 0, 0, 0, 0}, p.dx_parts,
                             OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, 0, v0 == 0,
-                                    v0 + p.piece >= c.v, dx, lddx, r.row, r.xexp, r.most},
+                                    v0 + p.piece >= c.v, dx, lddx, whole(dx, lddx), r.row, r.xexp, r.most},
                             n, c.ws + p.parts_at, s);
     }
     if (dw)
       summed<T, P, true>(Args{G, X, rows, d, n, r.count, 1, 0, 0, 0}, p.dw_parts,
-                         OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, nullptr, wexp, r.most},
+                         OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, whole(dw, lddw), nullptr,
+                                 wexp, r.most},
                          std::min(p.piece, c.v), c.ws + p.parts_at, s);
   }
 }

@@ -223,7 +223,8 @@ struct NextArgs {
   float a, c;
   void *o;  // the result, after the last step; else null
   int64_t ldo, batch_o;
-  int tall;
+  int tall;   // the result is X's transpose
+  int whole;  // it is not, and four of its values are one aligned store
 };
 template <int P, class T>
 struct Next {
@@ -246,10 +247,18 @@ struct Next {
         if (!e.o) {
           e.out.store(t.batch, m, n, v);
         } else {
+          typedef T T4 __attribute__((ext_vector_type(4)));
           T *o = static_cast<T *>(e.o) + t.batch * e.batch_o;
+          T4 y;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < t.N) o[e.tall ? (int64_t)(n + q) * e.ldo + m : (int64_t)m * e.ldo + n + q] = (T)v[q];
+          for (int q = 0; q < 4; ++q) y[q] = (T)v[q];
+          if (e.whole && n + 3 < t.N) {
+            *reinterpret_cast<T4 *>(o + (int64_t)m * e.ldo + n) = y;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (n + q < t.N) o[e.tall ? (int64_t)(n + q) * e.ldo + m : (int64_t)m * e.ldo + n + q] = y[q];
+          }
         }
       }
     }
@@ -314,6 +323,8 @@ void run(const Plan &p, const Input &in, int batch, int steps, float a, float b,
          void *o, int64_t ldo, int64_t stride_o, char *ws, hipStream_t s) {
   double *norm = reinterpret_cast<double *>(ws);
   const bool tall = in.m > in.n;
+  const bool whole = !tall && ldo % 4 == 0 && stride_o % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(o) % (4 * sizeof(T)) == 0;
   const int64_t lda = P * p.rp, ab = p.r * lda;
   Wide<P> x[2];
   for (int i = 0; i < 2; ++i) {
@@ -354,7 +365,7 @@ void run(const Plan &p, const Input &in, int batch, int steps, float a, float b,
     product<_Float16, P, false, true, Next<P, T>>(
         Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0, 0},
         NextArgs<P>{from, to, std::ldexp(a, en - ex), std::ldexp(1.0f, en - eb - ex),
-                    last ? o : nullptr, ldo, stride_o, tall},
+                    last ? o : nullptr, ldo, stride_o, tall, whole},
         batch, s);
     top = next;
     ex = en;

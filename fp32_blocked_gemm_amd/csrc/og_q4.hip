@@ -279,18 +279,20 @@ struct Planes<_Float16> {
 };
 
 // 128 k of a wave's operands, as loaded.
-template <class T, int MT>
+template <class T, int MT, int NT>
 struct Chunk {
-  u32x4 w;
-  Group gr[4];
+  u32x4 w[NT];
+  Group gr[NT];  // of the lane's row and its lane group's 32 k
   Eight<T> x[MT][4];
   template <bool FULL>
   __device__ __forceinline__ void load(const Problem &p, const T *const (&a)[MT], const bool (&in)[MT],
-                                       int64_t n, int c, int g) {
-    const int k = c * 128;
-    w = load_codes<FULL>(p.q + n * p.ldq, k + 32 * g, p.k);
+                                       const int64_t (&n)[NT], int c, int g) {
+    const int k = c * 128, u = group_of(p, min(k + 32 * g, p.k - 1));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) gr[j].load(p, n, group_of(p, min(k + 32 * j, p.k - 1)));
+    for (int t = 0; t < NT; ++t) {
+      w[t] = load_codes<FULL>(p.q + n[t] * p.ldq, k + 32 * g, p.k);
+      gr[t].load(p, n[t], u);
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -299,29 +301,29 @@ struct Chunk {
   }
 };
 
-// MT x 16 rows of A and 16 weight rows per block; k split among W waves (their
-// sums meet in LDS, in wave order), so that even a 4096-row layer has sixteen
-// waves on every compute unit asking for its bytes at once.  Each lane takes
-// 16 bytes (32 codes) of one weight row, 128 k in all; four lane-swap
+// MT x 16 rows of A and NT x 16 weight rows per block; k split among W waves
+// (their sums meet in LDS, in wave order), so that even a 4096-row layer has
+// sixteen waves on every compute unit asking for its bytes at once.  Each lane
+// takes 16 bytes (32 codes) of a weight row, 128 k in all; four lane-swap
 // instructions transpose the dwords among the four lane groups so that each of
 // the next four matrix-core instructions (16 x 16 x 32) covers 32 consecutive
-// k, that is, one group of scales.  The operands of the next 128 k are read
-// ahead.
-template <class T, int W, int MT>
+// k, that is, one group of scales, which one lane group has loaded.  The
+// operands of the next 128 k are read ahead.
+template <class T, int W, int MT, int NT>
 __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
   using Pl = Planes<T>;
   constexpr int P = Pl::P;
-  __shared__ float sums[W][16 * MT][17];
+  __shared__ float sums[W][16 * MT][16 * NT + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
+  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
   const int chunks = (p.k + 127) / 128;
   const int c0 = (int)((int64_t)chunks * wave / W), c1 = (int)((int64_t)chunks * (wave + 1) / W);
 
-  // lane i's rows of A (fragment rows) and row of W (fragment column)
+  // lane i's rows of A (fragment rows) and of W (fragment columns)
   const T *a[MT];
   bool in[MT];
-  Chunk<T, MT> next;
+  Chunk<T, MT, NT> next;
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + 16 * t + i;
@@ -332,51 +334,66 @@ __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) next.x[t][j].v[e] = (T)0.0f;  // what rows past m hold
   }
-  const int64_t n = min(n0 + i, p.n - 1);
+  int64_t n[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) n[t] = min(n0 + 16 * t + i, p.n - 1);
   auto load = [&](int c) __attribute__((always_inline)) {
     if (c * 128 + 128 <= p.k) next.template load<true>(p, a, in, n, c, g);
     else next.template load<false>(p, a, in, n, c, g);
   };
-  // acc[t][r]: weight row i, A row m0 + 16 t + 4 g + r
-  f32x4 acc[MT];
+  // acc[u][t][r]: weight row 16 u + i, A row m0 + 16 t + 4 g + r
+  f32x4 acc[NT][MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[u][t] = f32x4{0, 0, 0, 0};
 
   if (c0 < c1) load(c0);
   for (int c = c0; c < c1; ++c) {
-    const Chunk<T, MT> now = next;
+    const Chunk<T, MT, NT> now = next;
     if (c + 1 < c1) load(c + 1);
-    // dword d of lane group g (k 32 g + 8 d) to dword g of lane group d
-    const u32x2 s0 = __builtin_amdgcn_permlane32_swap(now.w[0], now.w[2], false, false);
-    const u32x2 s1 = __builtin_amdgcn_permlane32_swap(now.w[1], now.w[3], false, false);
-    const u32x2 lo = __builtin_amdgcn_permlane16_swap(s0[0], s1[0], false, false);
-    const u32x2 hi = __builtin_amdgcn_permlane16_swap(s0[1], s1[1], false, false);
-    const uint32_t d[4] = {lo[0], lo[1], hi[0], hi[1]};
+    typename Pl::V x[MT][4][P];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const f16x2 mz = now.gr[j].minus_zero();
-      const f16x2 q[4] = {codes<0>(d[j], mz), codes<1>(d[j], mz), codes<2>(d[j], mz), codes<3>(d[j], mz)};
-      const typename Pl::V w = Pl::weights(q);
-      const float s = now.gr[j].scale(p.s_type);
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        typename Pl::V x[P];
-        Pl::split(now.x[t][j], x);
-        f32x4 sum = {0, 0, 0, 0};
+      for (int j = 0; j < 4; ++j) Pl::split(now.x[t][j], x[t][j]);
 #pragma unroll
-        for (int h = P - 1; h >= 0; --h) sum = Pl::mfma(x[h], w, sum);
+    for (int u = 0; u < NT; ++u) {
+      // dword d of lane group g (k 32 g + 8 d) to dword g of lane group d
+      const u32x2 s0 = __builtin_amdgcn_permlane32_swap(now.w[u][0], now.w[u][2], false, false);
+      const u32x2 s1 = __builtin_amdgcn_permlane32_swap(now.w[u][1], now.w[u][3], false, false);
+      const u32x2 lo = __builtin_amdgcn_permlane16_swap(s0[0], s1[0], false, false);
+      const u32x2 hi = __builtin_amdgcn_permlane16_swap(s0[1], s1[1], false, false);
+      const uint32_t d[4] = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(s, sum[r], acc[t][r]);
+      for (int j = 0; j < 4; ++j) {
+        // the group that lane group j loaded
+        const Group gr{(uint32_t)__shfl((int)now.gr[u].s, i + 16 * j),
+                       (uint32_t)__shfl((int)now.gr[u].z, i + 16 * j)};
+        const f16x2 mz = gr.minus_zero();
+        const f16x2 q[4] = {codes<0>(d[j], mz), codes<1>(d[j], mz), codes<2>(d[j], mz), codes<3>(d[j], mz)};
+        const typename Pl::V w = Pl::weights(q);
+        const float s = gr.scale(p.s_type);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+          for (int h = P - 1; h >= 0; --h) sum = Pl::mfma(x[t][j][h], w, sum);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(s, sum[r], acc[u][t][r]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int u = 0; u < NT; ++u)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sums[wave][16 * t + 4 * g + r][i] = acc[t][r];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wave][16 * t + 4 * g + r][16 * u + i] = acc[u][t][r];
   __syncthreads();
-  for (int o = threadIdx.x; o < MT * 256; o += W * 64) {
-    const int row = o >> 4, col = o & 15;
+  for (int o = threadIdx.x; o < MT * NT * 256; o += W * 64) {
+    const int row = o / (16 * NT), col = o % (16 * NT);
     float v = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) v += sums[w][row][col];
@@ -418,9 +435,10 @@ void run_rows(const Problem &p, hipStream_t s) {
     hipLaunchKernelGGL((row_kernel<T, M, R, 1>), dim3((groups + 3) / 4), block, 0, s, p);
 }
 
-template <class T, int W, int MT>
+template <class T, int W, int MT, int NT>
 void run_blocks(const Problem &p, hipStream_t s) {
-  hipLaunchKernelGGL((block_kernel<T, W, MT>), dim3((p.n + 15) / 16, (p.m + 16 * MT - 1) / (16 * MT)),
+  hipLaunchKernelGGL((block_kernel<T, W, MT, NT>),
+                     dim3((p.n + 16 * NT - 1) / (16 * NT), (p.m + 16 * MT - 1) / (16 * MT)),
                      dim3(W * 64), 0, s, p);
 }
 
@@ -435,8 +453,15 @@ void run(const Problem &p, hipStream_t s) {
   if (p.m == 2) return run_rows<T, 2, 4>(p, s);
   if (p.m == 3) return run_rows<T, 3, 4>(p, s);
   if (p.m == 4) return run_rows<T, 4, 4>(p, s);
-  if (p.m <= 16) return run_blocks<T, sizeof(T) == 4 ? 8 : 16, 1>(p, s);
-  return run_blocks<T, 8, 2>(p, s);
+  // Two tiles of weight rows a block read A half as often (11008 x 4096, 64
+  // bf16 rows of A: 77 -> 51 us) where that leaves every compute unit a block;
+  // sixteen waves where fp32's planes do not need the registers of eight.
+  constexpr bool wide = sizeof(T) == 4;
+  const bool many = p.n >= 32 * 256;
+  if (p.m <= 16) return many ? run_blocks<T, 8, 1, 2>(p, s) : run_blocks<T, wide ? 8 : 16, 1, 1>(p, s);
+  if constexpr (!wide)
+    if (many) return run_blocks<T, 8, 2, 2>(p, s);
+  return run_blocks<T, 8, 2, 1>(p, s);
 }
 
 }  // namespace og::q4

@@ -441,16 +441,17 @@ int launch(Args g, const typename Epi::Args &e, int batches, hipStream_t s) {
 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// A tile and what it costs: microseconds a block spends on a stage, alone on
-// its compute unit on an idle card and as its share of a full one (measured on
-// products of 128 to 14336 columns, within a fifth).
-template <class S_, int ALONE, int SHARE>  // nanoseconds
+// A tile and what it costs: nanoseconds a block spends on a stage, alone on an
+// idle card, as one of 256 (one a compute unit) and as its share of a compute
+// unit that has more (measured on products of 128 to 14336 columns; of the
+// tiles listed the choice is within a tenth of the fastest on those).
+template <class S_, int ALONE, int ONE, int SHARE>
 struct Choice {
   using S = S_;
   static double time(bool sym, int64_t M, int64_t N, int64_t K, int64_t batch) {
     const int64_t tm = (M + S::BM - 1) / S::BM, tn = (N + S::BN - 1) / S::BN;
     const int64_t n = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
-    const double per = n <= 256 ? ALONE + (SHARE - ALONE) * (n / 256.0) : (n + 255) / 256 * SHARE;
+    const double per = n <= 256 ? ALONE + (ONE - ALONE) * (n / 256.0) : (n + 255) / 256 * SHARE;
     return (double)((K + depth(S::P) - 1) / depth(S::P)) * per;
   }
 };
@@ -459,30 +460,34 @@ struct Choices {};
 
 // The tiles by number of planes.  Large ones reuse each loaded value more
 // often (a compute unit loads about 30 bytes a cycle at most), small ones
-// spread a small product over more compute units.  Symmetric products need
-// square tiles; with both operands transposed two planes of 256 x 256 need
-// more registers than there are.
+// spread a small product over more compute units; 128 x 128 comes with two
+// blocks a compute unit for many tiles and with four stages in flight for few.
+// Symmetric products need square tiles; with both operands transposed two
+// planes of 256 x 256 need more registers than there are.
 template <class E, int P, bool TT>
 struct Tiles {
-  using type = Choices<Choice<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 1400, 1700>,
-                       Choice<Shape<E, 1, 192, 192, 2, 4, 3, 1>, 900, 1100>,
-                       Choice<Shape<E, 1, 128, 128, 2, 2, 2, 2>, 500, 510>,
-                       Choice<Shape<E, 1, 64, 64, 2, 2, 4, 2>, 210, 220>>;
+  using type = Choices<Choice<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 1250, 1600, 1700>,
+                       Choice<Shape<E, 1, 192, 192, 2, 4, 3, 1>, 720, 1050, 1100>,
+                       Choice<Shape<E, 1, 128, 128, 2, 2, 2, 2>, 630, 640, 510>,
+                       Choice<Shape<E, 1, 128, 128, 2, 4, 4, 1>, 450, 600, 640>,
+                       Choice<Shape<E, 1, 64, 64, 2, 2, 4, 2>, 200, 210, 190>>;
 };
 template <class E>
 struct Tiles<E, 2, true> {
-  using type = Choices<Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 1150, 1420>,
-                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 660, 630>,
-                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 226, 230>,
-                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
+  using type = Choices<Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 900, 1250, 1420>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 640, 700, 640>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 4, 1>, 560, 680, 760>,
+                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 220, 230, 230>,
+                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 150, 160, 129>>;
 };
 template <class E>
 struct Tiles<E, 2, false> {
-  using type = Choices<Choice<Shape<E, 2, 256, 256, 2, 4, 2, 1>, 1300, 2250>,
-                       Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 1150, 1420>,
-                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 660, 630>,
-                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 226, 230>,
-                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 160, 129>>;
+  using type = Choices<Choice<Shape<E, 2, 256, 256, 2, 4, 2, 1>, 1500, 2100, 2250>,
+                       Choice<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 900, 1250, 1420>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 640, 700, 640>,
+                       Choice<Shape<E, 2, 128, 128, 2, 4, 4, 1>, 560, 680, 760>,
+                       Choice<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 220, 230, 230>,
+                       Choice<Shape<E, 2, 32, 32, 1, 2, 4, 4>, 150, 160, 129>>;
 };
 
 // Runs a product on the tile with the least time; returns the number of tile
