@@ -1,5 +1,7 @@
 """Python binding of libog: exact and fast fp32 matrix product and NCHW
-convolution on MI355X (gfx950).
+convolution, and three operators around a language model's N x K weights (the
+product with 4-bit weights, the linear cross entropy with its gradient, the
+Newton-Schulz update) on MI355X (gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libog.so`` behind the C ABI of ``include/og.h``.  Torch supplies
@@ -399,7 +401,8 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
 
     G: float32 or bfloat16, [..., m, n], the last two dimensions a matrix with contiguous
     rows; any leading dimensions are a batch (a view that does not reduce to one batch
-    stride is refused).  out may be G itself."""
+    stride is refused).  out may be G itself.  Coefficients that may lift the singular values
+    past 2^37 before the last step are refused."""
     torch = _torch()
     if G.dim() < 2:
         raise ValueError("expected a tensor of at least two dimensions")

@@ -56,7 +56,8 @@ struct Rows {
   int *most;
 };
 
-// One block: the rows' places by a running count, in order.  Rows that do not
+// One block: the rows' places by a running count, in order (a launch's time up
+// to some thousand rows: 1000 in 3.5 us, 4096 in 8).  Rows that do not
 // count get their loss here (forward): 0 for the ignored index, NaN for a
 // target outside the vocabulary.
 __global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int64_t *target,
@@ -125,7 +126,8 @@ __device__ __forceinline__ f32x4 load4(const T *p, int left) {
 
 // `rows` rows of `cols` bf16 values, padded with zeros to ld columns.  With
 // pos, row i goes to place pos[i], and a row without a place clears its row of
-// `clear` instead (the gradient of an ignored row).
+// `clear` instead (the gradient of an ignored row).  Bound by the bytes: 4096
+// rows of 4096 in 19 us.
 template <bool VEC>
 __global__ __launch_bounds__(256) void copy_kernel(int rows, int cols, const __bf16 *x, int64_t ldx,
                                                    const int *pos, uint16_t *out, int64_t ld,
@@ -241,7 +243,11 @@ __device__ __forceinline__ f32x4 logits(f32x4 v, int xexp, const int *wexp, int 
 }
 
 // Epilogue of the forward product: each row's maximum over the tile's columns
-// and the sum of exp against it, and the target's logit where it lies here.
+// and the sum of exp against it, and the target's logit where it lies here.  Two
+// numbers a row and tile go to memory where the logits would be BN.  One bf16 row
+// against 32768 x 4096 is bound by W's bytes (55 us, 4.9 TB/s), 3891 rows by the
+// matrix cores (874 us, 1195 TFLOP/s), 700 fp32 rows against 50021 x 768 too (160
+// to 186 us, 290 to 335 TFLOP/s of fp32 operations, 3 of the matrix cores' each).
 struct LseArgs {
   float2 *part;  // [tile column][n]
   const int *target;
@@ -303,7 +309,8 @@ struct Lse {
   }
 };
 
-// Joins the tiles of 8 rows per block: 32 threads a row.
+// Joins the tiles of 8 rows per block: 32 threads a row.  (4 to 10 us: a launch
+// and a few dependent loads.)
 __global__ __launch_bounds__(256) void finish_kernel(Rows r, const float2 *part, int n, int tiles,
                                                      float *loss, float *lse) {
   __shared__ float2 sh[32][8];
@@ -311,11 +318,20 @@ __global__ __launch_bounds__(256) void finish_kernel(Rows r, const float2 *part,
   const int count = *r.count;
   float top = -INFINITY, sum = 0;
   if (m < count)
-    for (int t = w; t < tiles; t += 32) {
-      const float2 p = part[(int64_t)t * n + m];
-      const float to = fmaxf(top, p.x), from = to == -INFINITY ? 0.0f : to;
-      sum = sum * __builtin_amdgcn_exp2f((top - from) * kLog2e) +
-            p.y * __builtin_amdgcn_exp2f((p.x - from) * kLog2e);
+    for (int t0 = w; t0 < tiles; t0 += 32 * 4) {
+      float2 p[4];  // four loads in flight
+      float to = top;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int t = t0 + 32 * q;
+        p[q] = t < tiles ? part[(int64_t)t * n + m] : float2{-INFINITY, 0};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to = fmaxf(to, p[q].x);
+      const float from = to == -INFINITY ? 0.0f : to;
+      sum *= __builtin_amdgcn_exp2f((top - from) * kLog2e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += p[q].y * __builtin_amdgcn_exp2f((p[q].x - from) * kLog2e);
       top = to;
     }
   sh[w][threadIdx.x & 7] = {top, sum};
@@ -334,6 +350,7 @@ __global__ __launch_bounds__(256) void finish_kernel(Rows r, const float2 *part,
 }
 
 // Epilogue of the recomputed logits: g in planes, zero beyond the vocabulary.
+// Bound by the matrix cores (3891 x 16384 x 4096 bf16 463 us, 1128 TFLOP/s).
 struct GradArgs {
   uint16_t *g;
   int64_t ld;
@@ -407,7 +424,9 @@ __device__ __forceinline__ void store4(T *to, const f32x4 v, int left, bool whol
 
 // Epilogue of dX and dW.  The sum so far (dX, over the pieces) is kept in fp32
 // and rounded once, with the last piece; a product whose k is split stores its
-// parts for join_kernel.
+// parts for join_kernel.  Bound by the matrix cores where there are tiles enough
+// (3891 x 16384 x 4096 bf16: dX 422 us, 1239 TFLOP/s, dW 443 us), else by the few
+// tiles (700 x 8191 x 384 fp32: dX 29 us and 5 of joining, dW 23).
 struct OutArgs {
   float *sum;    // the sum over pieces, or the parts; not used by a single piece
   int64_t lds;
@@ -492,15 +511,15 @@ struct Plan {
 // Parts of k of an m x n product: as many as make up two tiles of 64 x 64 for
 // each compute unit, of at least 512 k each (one part costs its own fp32 copy
 // of the result and a pass that adds the copies: 1000 x 384 over 8191 took 107
-// us whole, 48 in eight parts).
+// us whole, 48 in five parts, 34 since with smaller tiles).
 int parts_of(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = std::max<int64_t>(1, (m + 63) / 64 * ((n + 63) / 64));
   return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, k / 512, 16}));
 }
 
 // A piece keeps g (and the planes of its weights) at up to 2^26 values a
-// plane: large enough to fill the card with tiles (8192 columns of 4096 rows
-// are 512 of them), small enough to stay in the 256 MB last-level cache.
+// plane (128 MB): large enough to fill the card with tiles (16384 columns of 4096
+// rows are 1024 of them), small enough to stay in the 256 MB last-level cache.
 Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   Plan p;
   p.planes = type == OG_F32 ? 2 : 1;
@@ -517,7 +536,7 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   p.wexp_at = take(p.planes == 2 ? p.piece * 4 : 0);
   p.x_at = take(p.planes * n * p.dp * 2);
   p.w_at = take(p.planes * p.piece * p.dp * 2);
-  p.part_at = grad ? at : take((round_up(v, p.piece) / 32) * n * 8);
+  p.part_at = grad ? at : take((round_up(v, p.piece) / (p.planes == 2 ? 32 : 64)) * n * 8);
   p.g_at = grad ? take(p.planes * n * p.piece * 2) : at;
   p.sum_at = grad ? take(n * p.dp * 4) : at;
   const int64_t piece = std::min(p.piece, v);
@@ -599,7 +618,8 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
                r.xexp, nullptr, nullptr, s);
   float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
   const bool in_place = readable<T>(c);
-  const int64_t piece = in_place ? c.v : p.piece;
+  // (a launch's tiles stay far below 2^32 threads)
+  const int64_t piece = in_place ? std::max<int64_t>(256, (int64_t(1) << 36) / c.n / 256 * 256) : p.piece;
   int tiles = 0;
   for (int64_t v0 = 0; v0 < c.v; v0 += piece) {
     const int rows = (int)std::min(piece, c.v - v0);

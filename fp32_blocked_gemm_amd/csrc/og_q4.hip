@@ -11,7 +11,7 @@
 // is multiplied by the whole numbers q - z, and the group's scale multiplies
 // the fp32 sum of its terms (at least 32 of them).
 //
-//  - Up to 4 rows of A: row_kernel, fp32 multiply-adds that take the fp16
+//  - Up to 3 rows of A (fp32: 4): row_kernel, fp32 multiply-adds that take the fp16
 //    code as an operand.  A lane holds 32 consecutive k of A in registers and
 //    runs them against the same 32 of several weight rows.
 //  - More: block_kernel on the matrix cores, 16 weight rows x 16 rows of A.
@@ -188,7 +188,10 @@ __device__ __forceinline__ void row_piece(const Problem &p, const int64_t (&row)
 }
 
 // Up to 4 rows of A.  Block: 4 waves; KS of them share R weight rows, each
-// taking every KS-th piece of 2048 k (64 lanes x 32).
+// taking every KS-th piece of 2048 k (64 lanes x 32).  Bound by the bytes of the
+// codes and, for small layers, by the time of one load after another: 4096 x
+// 4096 by one bf16 row 6.1 us (8.7 MB), 11008 x 4096 11.5 us, by a fp32 row with
+// groups of 32 and zero points 30 MB in 11 us.
 template <class T, int M, int R, int KS>
 __global__ __launch_bounds__(256) void row_kernel(Problem p) {
   __shared__ float part[4][M * R];
@@ -308,7 +311,9 @@ struct Chunk {
 // instructions transpose the dwords among the four lane groups so that each of
 // the next four matrix-core instructions (16 x 16 x 32) covers 32 consecutive
 // k, that is, one group of scales, which one lane group has loaded.  The
-// operands of the next 128 k are read ahead.
+// operands of the next 128 k are read ahead.  Bound by the codes' conversion (two
+// operations for two codes, once per 16 or 32 rows of A) and by latency: 16 bf16
+// rows on 4096 x 4096 10.5 us (0.9 TB/s of codes), on 11008 x 4096 24 us, 64 rows 49.
 template <class T, int W, int MT, int NT>
 __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
   using Pl = Planes<T>;
@@ -402,12 +407,10 @@ __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
   }
 }
 
-// Rows of fewer than 31 codes (16 bytes): a thread an output.
+// Rows of fewer than 31 codes (16 bytes, what the others load at once): a thread an output.
 template <class T>
-__global__ __launch_bounds__(256) void short_kernel(Problem p) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void short_one(const Problem &p, int64_t at) {
   const int m = (int)(at / p.n), n = (int)(at - (int64_t)m * p.n);
-  if (m >= p.m) return;
   const T *a = static_cast<const T *>(p.a) + m * p.lda;
   const uint8_t *q = p.q + n * p.ldq;
   float sum = 0, s = 0;  // (a single group: p.group >= 32 > k)
@@ -420,10 +423,17 @@ __global__ __launch_bounds__(256) void short_kernel(Problem p) {
   }
   static_cast<T *>(p.c)[m * p.ldc + n] = (T)(s * sum);
 }
+template <class T>
+__global__ __launch_bounds__(256) void short_kernel(Problem p) {
+  const int64_t total = (int64_t)p.m * p.n, step = (int64_t)gridDim.x * 256;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += step) short_one<T>(p, at);
+}
 
 template <class T, int M, int R>
 void run_rows(const Problem &p, hipStream_t s) {
   const int groups = (p.n + R - 1) / R;
+  // As many waves share a row as its pieces keep busy (one row of bf16: 1024 x
+  // 8192 by one wave 10.7 us, by four 4.8; 11008 x 2048 7.2 and 10.3).
   const int pieces = (p.k + 2047) / 2048;
   const int ks = pieces >= 4 ? 4 : pieces >= 2 ? 2 : 1;
   const dim3 block(256);
@@ -445,19 +455,26 @@ void run_blocks(const Problem &p, hipStream_t s) {
 template <class T>
 void run(const Problem &p, hipStream_t s) {
   if (p.k < 31) {
-    const int64_t blocks = ((int64_t)p.m * p.n + 255) / 256;
+    const int64_t blocks = std::min<int64_t>(((int64_t)p.m * p.n + 255) / 256, 1 << 20);
     hipLaunchKernelGGL(short_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, s, p);
     return;
   }
+  // Row kernel and matrix cores, 4096 x 4096, by rows of A: bf16 1 6.1 and 8.6
+  // us, 2 7.4 and 8.8, 4 10.0 and 9.2; fp32 (three products) 1 6.9 and 14.6, 4
+  // 14.0 and 15.4, 5 15.3 there.
+  constexpr bool wide = sizeof(T) == 4;
   if (p.m == 1) return run_rows<T, 1, 4>(p, s);
   if (p.m == 2) return run_rows<T, 2, 4>(p, s);
   if (p.m == 3) return run_rows<T, 3, 4>(p, s);
-  if (p.m == 4) return run_rows<T, 4, 4>(p, s);
-  // Two tiles of weight rows a block read A half as often (11008 x 4096, 64
-  // bf16 rows of A: 77 -> 51 us) where that leaves every compute unit a block;
-  // sixteen waves where fp32's planes do not need the registers of eight.
-  constexpr bool wide = sizeof(T) == 4;
-  const bool many = p.n >= 32 * 256;
+  if constexpr (wide)
+    if (p.m == 4) return run_rows<T, 4, 4>(p, s);
+  // Two tiles of weight rows a block read A half as often, where that leaves
+  // every compute unit a block (one tile and two: 64 bf16 rows of A on 4096 x
+  // 4096 24.0 and 17.9 us, on 11008 x 4096 61.9 and 48.7; 16 on 8192 x 4096 19.2
+  // and 13.9, fp32 29.1 and 23.1; but 16 on 4096 x 4096, 128 blocks, 10.5 and
+  // 13.5); sixteen waves where fp32's planes do not need the registers of eight.
+  const int tall = p.m <= 16 ? 16 : 32;
+  const bool many = (int64_t)((p.n + 31) / 32) * ((p.m + tall - 1) / tall) >= 256;
   if (p.m <= 16) return many ? run_blocks<T, 8, 1, 2>(p, s) : run_blocks<T, wide ? 8 : 16, 1, 1>(p, s);
   if constexpr (!wide)
     if (many) return run_blocks<T, 8, 2, 2>(p, s);
@@ -486,8 +503,9 @@ extern "C" og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *
     return fail(OG_ERR_INVALID_ARG, "a row stride is below its row: lda %lld, ldq %lld, lds %lld, "
                 "ldz %lld, ldc %lld", (long long)lda, (long long)ldq, (long long)lds, (long long)ldz,
                 (long long)ldc);
-  if (m > (1 << 19) || n > (1 << 30) || k > (1 << 28) || group > (1 << 30))
-    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld, k %lld or group %lld: at most 2^19, 2^30, 2^28, 2^30",
+  // (n: a row kernel's launch has up to 64 n threads, of fewer than 2^32)
+  if (m > (1 << 19) || n > (1 << 25) || k > (1 << 28) || group > (1 << 30))
+    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld, k %lld or group %lld: at most 2^19, 2^25, 2^28, 2^30",
                 (long long)m, (long long)n, (long long)k, (long long)group);
   if (m * n > (int64_t(1) << 38))
     return fail(OG_ERR_TOO_LARGE, "%lld x %lld outputs: at most 2^38", (long long)m, (long long)n);

@@ -281,8 +281,9 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
  * Operators of language models around the N x K product (og_gemm_nt_f32's
  * right operand: each row holds the k weights of one output).  They take
  * fp32, bf16 or fp16 tensors as stated, sum in fp32 and run on the bf16 and
- * fp16 matrix cores; the modes above and og_set_variant do not apply to
- * them.  Results repeat bit for bit from run to run (no atomics).  A
+ * fp16 matrix cores (single rows of the 4-bit product on fp32 multiply-adds);
+ * the modes above and og_set_variant do not apply to them.  Results repeat
+ * bit for bit from run to run (no sum depends on the order of blocks).  A
  * workspace is device memory of the caller's, 256-byte aligned, of at least
  * the bytes its _workspace function returns; it holds nothing from one call
  * to the next, and calls that may run at the same time (other streams,
@@ -313,8 +314,8 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
  * Requirements: m, n, k >= 0; group a multiple of 32, >= 32; lda >= max(1,k),
  * ldq >= max(1, ceil(k/2)), lds and ldz >= max(1, ceil(k/group)), ldc >=
  * max(1,n); pointers non-null as in og_gemm_f32.  m or n 0: nothing is done;
- * k == 0: every output is +0.  OG_ERR_TOO_LARGE when m exceeds 2^19, n or
- * group 2^30, k 2^28 or m*n 2^38.  No workspace.
+ * k == 0: every output is +0.  OG_ERR_TOO_LARGE when m exceeds 2^19, n 2^25,
+ * group 2^30, k 2^28 or m*n 2^38.  C must not overlap an input.  No workspace.
  */
 og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *A, int type, int64_t lda,
                         const uint8_t *Q, int64_t ldq, const void *S, int scale_type, int64_t lds,
@@ -330,12 +331,15 @@ og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *A, int type
  *
  * G and O are of `type` (OG_F32 or OG_BF16); O may be G itself with the same
  * strides, and must not overlap it otherwise.  |G| is summed in 64 bits.
- * The products hold X, A and b A + c A A in bf16 planes: three for OG_F32
- * (24 bits, fp32 accuracy), two for OG_BF16 (16 bits; the result is rounded
- * to bf16 once).  G = 0 with eps > 0 gives 0; a G that is not finite gives
- * NaN.  The step's intermediate values must stay within fp32's range, which
- * they do for coefficients that keep the singular values bounded.
- * Requirements: 1 <= steps <= 64; a, b, c, eps finite, eps >= 0; ldg, ldo >=
+ * X is held as two fp16 planes (22 bits) times a power of two.  For OG_F32 A
+ * and b A + c A A are too, and every product takes both planes (errors of fp32
+ * products); for OG_BF16 the products take one plane of each (11 bits), X
+ * keeps both between the steps, and the result is rounded to bf16 once.  G = 0
+ * with eps > 0 gives 0; a G that is not finite gives NaN.
+ * Requirements: 1 <= steps <= 64; a, b, c, eps finite, eps >= 0; the singular
+ * values that X could have before a step, from [0, 1] on through the
+ * polynomial a x + b x^3 + c x^5, at most 2^37 and, the largest of them, at
+ * least 2^-23 (or all zero); |b x^2 + c x^4| at most 2^74; ldg, ldo >=
  * max(1, n); with batch > 1 strideg >= 0 (0: one matrix for all) and strideo
  * >= (m-1)*ldo + n; m, n <= 2^18, batch <= 65535 (OG_ERR_TOO_LARGE); a
  * workspace.  batch, m or n 0: nothing is done.
@@ -358,10 +362,11 @@ int64_t og_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int type
  * A row whose target is ignore_index (any value, one inside [0, v) too) does
  * not count: its loss and lse are 0 and its row of X is not used (it may hold
  * anything).  A row whose target is neither ignore_index nor in [0, v) gets
- * the loss NaN, the lse 0 and otherwise does not count.  The products run on
- * the bf16 matrix cores with fp32 sums: bf16 tensors as they are, fp32 ones
- * in three bf16 planes (24 bits; fp32 accuracy).  X and W of rows that count
- * must be finite: a value that is not makes the results it enters NaN.
+ * the loss NaN, the lse 0 and otherwise does not count.  bf16 tensors are
+ * multiplied as they are; of fp32 ones each row of X and W is held as two fp16
+ * planes times a power of two of its own: 22 bits of each value, down to 2^-38
+ * of the row's largest.  X and W of rows that count must be finite: a value
+ * that is not makes the results it enters NaN (a logit of -inf adds nothing).
  * Requirements: n >= 0, v, d >= 1; ldx, ldw >= d; n <= 2^24, v <= 2^28,
  * d <= 2^18, ldw <= 2^22 (OG_ERR_TOO_LARGE); loss and lse n floats each; a
  * workspace of og_linear_cross_entropy_workspace(n, v, d, type, 0) bytes.
@@ -381,12 +386,17 @@ og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X
  *     dX = g W  (n x d, row stride lddx),   dW = g^T X  (v x d, lddw)
  *
  * both of `type`, overwritten; either may be NULL (not wanted).  The logits
- * are recomputed in pieces of the vocabulary; g is held in one bf16 plane for
- * OG_BF16 and in three for OG_F32, the sums over the vocabulary and over the
- * rows in fp32, rounded once.  Rows that do not count have zero gradient
- * whatever dloss and lse hold there, and add nothing to dW; n == 0 clears
- * dW.  Otherwise as above, with a workspace of
- * og_linear_cross_entropy_workspace(n, v, d, type, 1) bytes.
+ * are recomputed in pieces of the vocabulary; the sums over the vocabulary and
+ * over the rows are fp32, rounded once.  g is rounded to bf16 for OG_BF16.  For
+ * OG_F32 it has 22 bits, down to about 2^-37 of M / (max |X_i| max |W_j|), M
+ * the largest |dloss_i| max |X_i| of any row times the largest |W|: what is
+ * below that adds nothing, so rows whose dloss is many orders smaller than
+ * another's, and entries of dW that only tiny probabilities make, have the
+ * errors of M's size rather than of their own.  Rows that do not count have
+ * zero gradient whatever dloss and lse hold there, and add nothing to dW;
+ * n == 0 clears dW.  The outputs must not overlap the inputs.  Otherwise as
+ * above, with a workspace of og_linear_cross_entropy_workspace(n, v, d, type,
+ * 1) bytes.
  */
 og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const void *X, int64_t ldx,
                                        const void *W, int64_t ldw, int type, const int64_t *target,

@@ -59,6 +59,44 @@ def test_several_pieces_of_the_vocabulary(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n,v,d", [(9000, 9001, 24), (9000, 9001, 25), (20000, 9001, 72), (40, 9001, 8200)])
+def test_two_and_three_pieces(n, v, d, dtype):
+    """dX summed over two and three pieces (a piece holds 2^26 values of g or of W), with its sum
+    over a piece whole or (the last) split; d = 25: bf16 weights that are copied first."""
+    say(f"linear_ce {n}x{v}x{d} {dtype}")
+    check(*make(n, v, d, dtype, seed=n + d))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n,v,d", [
+    (4000, 5000, 776), (1000, 5000, 4104), (9000, 100, 776), (9000, 100, 1000), (500, 1300, 4104),
+    (20000, 900, 264), (5000, 100, 2056),
+])
+def test_every_tile(n, v, d, dtype):
+    """Sizes that together bring each product of the operator to each of its tiles."""
+    say(f"linear_ce {n}x{v}x{d} {dtype}")
+    check(*make(n, v, d, dtype, seed=n + v))
+
+
+def test_rows_of_all_sizes():
+    """fp32 rows of X and W and values of dloss from tiny to large and zero, each row of the
+    planes to a power of its own."""
+    t = torch()
+    x, w, target, dloss = make(140, 260, 72, "float32", seed=13)
+    gen = t.Generator().manual_seed(14)
+    up = 2.0 ** t.randint(-60, 61, (140, 1), generator=gen).cuda()
+    x, w = x * up / 2.0 ** 60, w * 2.0 ** t.randint(-100, 5, (260, 1), generator=gen).cuda()
+    x[7], w[11], dloss[13] = 0, 0, 0
+    dloss *= 2.0 ** t.randint(-30, 31, (140,), generator=gen).cuda()
+    check(x, w, target, dloss)
+    dloss.zero_()
+    loss, lse, dx, dw = check(x, w, target, dloss)
+    assert (dx == 0).all() and (dw == 0).all()
+    x.zero_()
+    check(x, w, target, dloss)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_large_tiles(dtype):
     n, v, d = 1500, 12000, 136
     say(f"linear_ce {n}x{v}x{d} {dtype}")

@@ -52,6 +52,24 @@ def test_large_tiles(dtype):
         check(og.newton_schulz(g), g, what=shape)
 
 
+@pytest.mark.parametrize("dtype,r,k,batch", [
+    ("bfloat16", 257, 257, 1), ("bfloat16", 331, 331, 32), ("bfloat16", 405, 405, 48),
+    ("bfloat16", 331, 531, 64), ("bfloat16", 257, 514, 12), ("bfloat16", 479, 479, 64),
+    ("float32", 130, 130, 24), ("float32", 200, 200, 64), ("float32", 331, 331, 64),
+    ("float32", 405, 405, 48), ("float32", 997, 997, 16), ("bfloat16", 200, 200, 64),
+])
+def test_every_tile(dtype, r, k, batch):
+    """Batches that together bring each product to each of its tiles: two matrices in turn, all of
+    whose results repeat bit for bit."""
+    t = torch()
+    say(f"newton_schulz {batch} of {r}x{k} {dtype}")
+    two = make((2, r, k), dtype, seed=r + k)
+    out = og.newton_schulz(two[t.arange(batch) % 2], steps=2)
+    check(out[:2], two[:batch], steps=2, what=(r, k, batch))
+    for b in range(2, batch):
+        assert t.equal(out[b], out[b % 2]), b
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_batches_views_and_gaps(dtype):
     t = torch()

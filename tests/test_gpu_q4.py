@@ -43,6 +43,18 @@ def test_shapes(m, n, k, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 16, 17, 40])
+def test_lengths_around_a_load_and_wide_layers(m, dtype):
+    """k around the 32 codes of a load and where a row's pieces divide among the waves; weights
+    enough for two tiles of rows a block."""
+    for n, k in ((70, 30), (70, 31), (70, 32), (70, 33), (9, 2047), (9, 4128), (9, 8193), (8200, 95),
+                 (8250, 256)):
+        a, q, s, z = make(m, n, k, 32, dtype, seed=m + n + k)
+        say(f"q4 {m}x{n}x{k} {dtype}")
+        check(og.gemm_nt_q4(a, q, s, zeros=z, group=32), a, q, s, z, 32, (m, n, k))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_strides_offsets_and_gaps(dtype):
     """Row strides, odd byte offsets of the codes, a NaN sentinel in every gap of the inputs
     and one in the output's that must survive."""

@@ -43,7 +43,7 @@ def test_q4_rejects_before_launch(L, kw):
     assert L.og_last_error()
 
 
-@pytest.mark.parametrize("kw", [dict(m=(1 << 19) + 1), dict(n=(1 << 30) + 1, ldc=1 << 31),
+@pytest.mark.parametrize("kw", [dict(m=(1 << 19) + 1), dict(n=(1 << 25) + 1, ldc=1 << 31),
                                 dict(k=(1 << 28) + 1, lda=1 << 31, ldq=1 << 30, lds=1 << 30),
                                 dict(m=1 << 19, n=1 << 30, ldc=1 << 30)])
 def test_q4_too_large(L, kw):
@@ -127,6 +127,7 @@ def _ns(L, batch=1, m=3, n=5, G=P, ldg=5, sg=0, type=0, steps=5, a=3.4, b=-4.8, 
     dict(a=float("nan")), dict(b=float("inf")), dict(c=float("-inf")), dict(eps=-1e-7),
     dict(eps=float("nan")), dict(ldg=4), dict(ldo=4), dict(G=NULL), dict(O=NULL), dict(ws=NULL),
     dict(bytes=100), dict(ws=ODD), dict(batch=2, sg=-15, so=15), dict(batch=2, sg=15, so=14),
+    dict(a=1e4, b=0, c=0, steps=4), dict(a=1e-4, b=0, c=0, steps=3), dict(b=1e30), dict(a=4, b=2, c=3, steps=20),
 ])
 def test_ns_rejects_before_launch(L, kw):
     assert _ns(L, **kw) == og.OG_ERR_INVALID_ARG
