@@ -16,8 +16,11 @@
 // piece and runs both products on it.  All of it is bound by the matrix cores:
 // 2 n v d operations forward, 6 n v d backward.
 //
-// bf16 tensors run as they are, g in bf16 (whose rounding is that of the
-// gradients themselves).  fp32 ones run as two fp16 planes (og_tile.hpp), each
+// bf16 tensors run as they are, g in bf16 and divided by the largest |dloss|,
+// by which the sums are multiplied in fp32: where all rows weigh the same (a
+// mean), the target's entry p - 1 then rounds by its p alone, and not every row's
+// by the same error of the weight (4096 x 32768 x 4096: errors of dX and dW
+// 0.0019 for 0.0023 to 0.0032, 0.0017 of them their own rounding).  fp32 ones run as two fp16 planes (og_tile.hpp), each
 // row of X and W times a power of two of its own that brings its largest value
 // to [2^13, 2^14).  The logits undo both powers.  For the gradients, whose sums
 // run over rows of W and of X, g is stored divided by both (and times one power
@@ -54,7 +57,22 @@ struct Rows {
   // fp32: the largest exponent of |dloss| x row maximum of X, and of a row
   // maximum of W, each + kBias (0: none)
   int *most;
+  float *scale;   // bf16: the largest finite |dloss| of the rows that count, or 1
 };
+
+// The largest of the wave's (non-negative) values, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+#define OG_ROR(N)                                                                                  \
+  v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v),      \
+                                                                  0x120 + N, 0xf, 0xf, true)))
+  OG_ROR(8);
+  OG_ROR(4);
+  OG_ROR(2);
+  OG_ROR(1);
+#undef OG_ROR
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
 
 // One block: the rows' places by a running count, in order (a launch's time up
 // to some thousand rows: 1000 in 3.5 us, 4096 in 8).  Rows that do not
@@ -66,6 +84,7 @@ __global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int6
   __shared__ int waves[16];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int done = 0;
+  float largest = 0;
   for (int i0 = 0; i0 < n; i0 += 1024) {
     const int i = i0 + threadIdx.x;
     const int64_t t = i < n ? target[i] : ignore;
@@ -84,8 +103,10 @@ __global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int6
       r.row[at] = i;
       r.target[at] = (int)t;
       if (lse_in) {
+        const float d = dloss[i];
         r.lse[at] = lse_in[i];
-        r.dloss[at] = dloss[i];
+        r.dloss[at] = d;
+        if (__builtin_isfinite(d)) largest = fmaxf(largest, fabsf(d));
       }
     } else if (i < n) {
       r.pos[i] = -1;
@@ -97,7 +118,13 @@ __global__ __launch_bounds__(1024) void rows_kernel(int n, int64_t v, const int6
     done += all;
     __syncthreads();
   }
+  __shared__ float tops[16];
+  largest = wave_max(largest);
+  if (lane == 0) tops[w] = largest;
+  __syncthreads();
   if (threadIdx.x == 0) {
+    for (int k = 1; k < 16; ++k) largest = fmaxf(largest, tops[k]);
+    *r.scale = largest > 0 ? largest : 1.0f;
     *r.count = done;
     r.most[0] = r.most[1] = 0;
   }
@@ -149,20 +176,6 @@ __global__ __launch_bounds__(256) void copy_kernel(int rows, int cols, const __b
     for (int e = 0; e < 4; ++e) h[e] = (__bf16)v[e];
     *reinterpret_cast<bf16x4 *>(out + to * ld + c) = h;
   }
-}
-
-// The largest of the wave's (non-negative) values, in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-#define OG_ROR(N)                                                                                  \
-  v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v),      \
-                                                                  0x120 + N, 0xf, 0xf, true)))
-  OG_ROR(8);
-  OG_ROR(4);
-  OG_ROR(2);
-  OG_ROR(1);
-#undef OG_ROR
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // The same for fp32: two planes of each row times its power of two, whose
@@ -355,7 +368,7 @@ struct GradArgs {
   uint16_t *g;
   int64_t ld;
   const int *target;
-  const float *lse, *dloss;
+  const float *lse, *dloss, *scale;
   const int *xexp, *wexp;
   const int *most;
   int v0;
@@ -369,11 +382,12 @@ struct Grad {
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
     const int common = P == 2 ? common_exponent(e.most) : 0;
+    const float by = *e.scale;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
-      const float l = e.lse[m], d = e.dloss[m];
+      const float l = e.lse[m], d = P == 2 ? e.dloss[m] : e.dloss[m] / by;
       const int want = e.target[m] - e.v0 - nc;
       const int xexp = P == 2 ? e.xexp[m] : 0;
       uint16_t *to = e.g + m * e.ld;
@@ -438,6 +452,7 @@ struct OutArgs {
   const int *row;  // null: row m is row m of out
   const int *exp;  // fp32: the exponents of the rows, less the common one
   const int *most;
+  const float *scale;  // bf16: what g was divided by
 };
 template <class T>
 struct Out {
@@ -448,6 +463,7 @@ struct Out {
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
     const int common = S::P == 2 ? common_exponent(e.most) : 0;
+    const float by = *e.scale;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
@@ -463,6 +479,9 @@ struct Out {
         if constexpr (S::P == 2) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = __builtin_ldexpf(v[q], up);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] *= by;
         }
         if (!e.first) {
           const f32x4 was = *reinterpret_cast<const f32x4 *>(sum + n);
@@ -554,7 +573,7 @@ Rows rows_of(char *at, int64_t n) {
   int *p = reinterpret_cast<int *>(at + 256);
   return Rows{reinterpret_cast<int *>(at), p, p + s, p + 2 * s, reinterpret_cast<float *>(p + 3 * s),
               reinterpret_cast<float *>(p + 4 * s), reinterpret_cast<float *>(p + 5 * s), p + 6 * s,
-              reinterpret_cast<int *>(at) + 1};
+              reinterpret_cast<int *>(at) + 1, reinterpret_cast<float *>(at) + 3};
 }
 
 void operand_rows(int64_t rows, int64_t cols, const __bf16 *x, int64_t ldx, const int *pos,
@@ -642,7 +661,8 @@ void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s)
   }
   float *from = reinterpret_cast<float *>(ws);
   g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, 0, nullptr, o.exp, o.most};
+  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, 0, nullptr, o.exp, o.most,
+                     o.scale};
   product<Element<T>, P, TA, true, Out<T>>(g, part, parts, s);
   const int64_t quads = (int64_t)g.M * ((g.N + 3) / 4);
   hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
@@ -678,17 +698,19 @@ void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss
       const Operand W = weights<T, P>(p, c, v0, rows, in_place, r.most + 1, s);
       product<Element<T>, P, false, false, Grad<P>>(
           Args{X, W, n, rows, d, r.count, 0, 0, 0, 0},
-          GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, r.xexp, wexp, r.most, (int)v0}, 1, s);
+          GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, r.scale, r.xexp, wexp, r.most, (int)v0},
+          1, s);
       if (dx)
         summed<T, P, false>(Args{G, W, n, d, rows, r.count, 0, 0, 0, 0}, p.dx_parts,
                             OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, 0, v0 == 0,
-                                    v0 + p.piece >= c.v, dx, lddx, whole(dx, lddx), r.row, r.xexp, r.most},
+                                    v0 + p.piece >= c.v, dx, lddx, whole(dx, lddx), r.row, r.xexp, r.most,
+                                    r.scale},
                             n, c.ws + p.parts_at, s);
     }
     if (dw)
       summed<T, P, true>(Args{G, X, rows, d, n, r.count, 1, 0, 0, 0}, p.dw_parts,
                          OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, whole(dw, lddw), nullptr,
-                                 wexp, r.most},
+                                 wexp, r.most, r.scale},
                          std::min(p.piece, c.v), c.ws + p.parts_at, s);
   }
 }

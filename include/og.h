@@ -387,8 +387,8 @@ og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X
  *
  * both of `type`, overwritten; either may be NULL (not wanted).  The logits
  * are recomputed in pieces of the vocabulary; the sums over the vocabulary and
- * over the rows are fp32, rounded once.  g is rounded to bf16 for OG_BF16.  For
- * OG_F32 it has 22 bits, down to about 2^-37 of M / (max |X_i| max |W_j|), M
+ * over the rows are fp32, rounded once.  For OG_BF16 g, divided by the largest
+ * |dloss|, is rounded to bf16.  For OG_F32 it has 22 bits, down to about 2^-37 of M / (max |X_i| max |W_j|), M
  * the largest |dloss_i| max |X_i| of any row times the largest |W|: what is
  * below that adds nothing, so rows whose dloss is many orders smaller than
  * another's, and entries of dW that only tiny probabilities make, have the

@@ -235,6 +235,21 @@ def test_gradient_against_differences():
             assert (got - diff).abs() <= bound
 
 
+def test_a_common_weight_costs_no_bits():
+    """bf16: all rows with the weight c against all with 1.  Both are the same sums, c times and
+    rounded to bf16 once each, half a step (and fp32's roundings) apart; c = 1 + 2^-8 is the
+    number that a rounding to bf16 would move most."""
+    t = torch()
+    x, w, target, dloss = make(200, 500, 64, "bfloat16", seed=15)
+    loss, lse = og.linear_cross_entropy(x, w, target)
+    c = 1 + 2.0 ** -8
+    one = og.linear_cross_entropy_grad(x, w, target, lse, t.ones_like(dloss))
+    two = og.linear_cross_entropy_grad(x, w, target, lse, t.full_like(dloss, c))
+    for a, b in zip(one, two):
+        a, b = a.double(), b.double()
+        within(b, c * a, ref.half_step(t.bfloat16) * (c * a.abs() + b.abs()) * (1 + 2.0 ** -20), "weight")
+
+
 def test_same_bits_every_run():
     t = torch()
     x, w, target, dloss = make(400, 1500, 128, "bfloat16", seed=11)
