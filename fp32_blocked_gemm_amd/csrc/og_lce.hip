@@ -519,8 +519,92 @@ __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, const int
   }
 }
 
+// Few rows of fp32 in the forward call (up to kFew): no planes, whose making
+// alone would read and write as many bytes as W has.  Plain fp32 multiply-adds,
+// each weight read once; bound by W's bytes and, at eight rows, as much by the
+// multiply-adds (25543 x 2048: 8 rows 110 us, 1.9 TB/s; 9 rows by planes 147).
+constexpr int kFew = 8, kFewWaves = 1024;
+
+__device__ __forceinline__ float wave_sum(float v) {
+#define OG_ROR(N)                                                                                  \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + N,   \
+                                                          0xf, 0xf, true))
+  OG_ROR(8);
+  OG_ROR(4);
+  OG_ROR(2);
+  OG_ROR(1);
+#undef OG_ROR
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// The logits of N rows, four vocabulary rows a wave at a time.  Each wave's
+// running maximum and sum go to part as a tile's would.
+template <int N, bool VEC>
+__global__ __launch_bounds__(256) void few_logits_kernel(Rows r, int n, int64_t v, int d, const float *x,
+                                                         int64_t ldx, const float *w, int64_t ldw,
+                                                         float2 *part) {
+  constexpr int R = 4;
+  int count = *r.count;
+  if (count == 0) return;
+  // kept in a vector register, and with it what the rows' places give: they are
+  // more than the scalar registers hold
+  asm volatile("" : "+v"(count));
+  const int lane = threadIdx.x & 63, wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float *xp[N];  // from the lane's first column on
+  float top[N], sum[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    xp[i] = x + r.row[min(i, count - 1)] * ldx + 4 * lane;
+    top[i] = -INFINITY;
+    sum[i] = 0;
+  }
+  for (int64_t j0 = (int64_t)wave * R; j0 < v; j0 += (int64_t)gridDim.x * 4 * R) {
+    float acc[N][R];
+    const float *wp[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      wp[q] = w + min(j0 + q, v - 1) * ldw + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i][q] = 0;
+    }
+    for (int c = 0; c < d; c += 256) {
+      const int left = d - c - 4 * lane;
+      f32x4 b[R];
+#pragma unroll
+      for (int q = 0; q < R; ++q) b[q] = load4<float, VEC>(wp[q] + c, left);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const f32x4 a = load4<float, VEC>(xp[i] + c, left);
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][q] = fmaf(a[e], b[q][e], acc[i][q]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int place = min(i, count - 1), want = r.target[place] - (int)j0;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const float z = wave_sum(acc[i][q]);
+        if (j0 + q >= v) continue;
+        if (want == q && lane == 0 && i < count) r.zt[i] = z;
+        const float to = fmaxf(top[i], z), from = to == -INFINITY ? 0.0f : to;
+        sum[i] = sum[i] * __builtin_amdgcn_exp2f((top[i] - from) * kLog2e) +
+                 __builtin_amdgcn_exp2f((z - from) * kLog2e);
+        top[i] = to;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 0 && i < count) part[(int64_t)wave * n + i] = {top[i], sum[i]};
+}
+
 struct Plan {
   int planes;
+  bool few;             // forward, fp32 of up to kFew rows
   int64_t dp;           // d padded
   int64_t piece;        // vocabulary rows of a piece
   int dx_parts, dw_parts;  // parts of k of a piece's gradient products
@@ -543,6 +627,7 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   Plan p;
   p.planes = type == OG_F32 ? 2 : 1;
   p.dp = round_up(d, 64);
+  p.few = !grad && p.planes == 2 && n > 0 && n <= kFew;
   const int64_t most = (int64_t(1) << 26) / std::max(n, p.dp) / 256 * 256;
   p.piece = std::min(round_up(v, 256), std::max<int64_t>(2048, most));
   int64_t at = 0;
@@ -552,6 +637,12 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
     return here;
   };
   p.rows_at = take(256 + 7 * round_up(n, 64) * 4);
+  if (p.few) {
+    p.part_at = take(kFewWaves * n * 8);
+    p.wexp_at = p.x_at = p.w_at = p.g_at = p.sum_at = p.parts_at = p.total = at;
+    p.dx_parts = p.dw_parts = 1;
+    return p;
+  }
   p.wexp_at = take(p.planes == 2 ? p.piece * 4 : 0);
   p.x_at = take(p.planes * n * p.dp * 2);
   p.w_at = take(p.planes * p.piece * p.dp * 2);
@@ -626,6 +717,32 @@ bool readable(const Call &c) {
 template <class T>
 using Element = std::conditional_t<std::is_same_v<T, float>, _Float16, __bf16>;
 
+template <class T>
+int whole(const T *p, int64_t ld) {
+  return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
+}
+
+template <int N, bool VEC>
+void few_forward(const Call &c, const Rows &r, float2 *part, int waves, hipStream_t s) {
+  hipLaunchKernelGGL((few_logits_kernel<N, VEC>), dim3(waves / 4), dim3(256), 0, s, r, (int)c.n, c.v,
+                     (int)c.d, static_cast<const float *>(c.x), c.ldx, static_cast<const float *>(c.w),
+                     c.ldw, part);
+}
+// f(N, VEC) for a call of few rows.
+template <class F>
+void few(const Call &c, F f) {
+  const bool vec = c.ldx % 4 == 0 && c.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(c.w) % 16 == 0;
+  auto by = [&](auto n) {
+    if (vec) f(n, std::true_type());
+    else f(n, std::false_type());
+  };
+  if (c.n <= 2) by(std::integral_constant<int, 2>());
+  else if (c.n <= 4) by(std::integral_constant<int, 4>());
+  else by(std::integral_constant<int, kFew>());
+}
+int few_waves(int64_t v) { return (int)std::min<int64_t>(kFewWaves, (v + 15) / 16 * 4); }
+
 template <class T, int P>
 void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t s) {
   const Rows r = rows_of(c.ws + p.rows_at, c.n);
@@ -633,6 +750,14 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
   const int *wexp = reinterpret_cast<const int *>(c.ws + p.wexp_at);
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, (int)c.n, c.v, c.target, c.ignore, r,
                      (const float *)nullptr, (const float *)nullptr, loss, lse);
+  if (p.few) {
+    float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
+    const int waves = few_waves(c.v);
+    few(c, [&](auto n, auto vec) { few_forward<n(), vec()>(c, r, part, waves, s); });
+    hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((c.n + 7) / 8)), dim3(256), 0, s, r, part,
+                       (int)c.n, waves, loss, lse);
+    return;
+  }
   operand_rows(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, (T *)nullptr, 0,
                r.xexp, nullptr, nullptr, s);
   float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
@@ -669,11 +794,6 @@ void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s)
                      dim3(256), 0, s, g.M, g.N, g.count_is_k ? nullptr : g.count, parts, from,
                      part.part, o.sum, o.lds, o.first, o.last, static_cast<T *>(o.out), o.ldo, o.whole,
                      o.row);
-}
-
-template <class T>
-int whole(const T *p, int64_t ld) {
-  return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
 }
 
 template <class T, int P>

@@ -363,7 +363,7 @@ int64_t og_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int type
  * not count: its loss and lse are 0 and its row of X is not used (it may hold
  * anything).  A row whose target is neither ignore_index nor in [0, v) gets
  * the loss NaN, the lse 0 and otherwise does not count.  bf16 tensors are
- * multiplied as they are; of fp32 ones each row of X and W is held as two fp16
+ * multiplied as they are, and so are up to eight fp32 rows; of more each row of X and W is held as two fp16
  * planes times a power of two of its own: 22 bits of each value, down to 2^-38
  * of the row's largest.  X and W of rows that count must be finite: a value
  * that is not makes the results it enters NaN (a logit of -inf adds nothing).

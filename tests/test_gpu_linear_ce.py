@@ -68,6 +68,28 @@ def test_two_and_three_pieces(n, v, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9])
+def test_few_rows(n, dtype):
+    """Rows around those that a kernel of their own takes, layers that give each wave many rows
+    and none, columns that end inside a load, rows that do not count among them and strides that
+    are not whole loads."""
+    t = torch()
+    for v, d in ((1, 3), (17, 260), (1023, 255), (1025, 64), (5003, 1000), (40000, 65)):
+        x, w, target, dloss = make(n, v, d, dtype, seed=n + v, ignored=0.3)
+        say(f"linear_ce {n}x{v}x{d} {dtype}")
+        loss, lse, dx, dw = check(x, w, target, dloss)
+        for need in ((True, False), (False, True)):
+            one = og.linear_cross_entropy_grad(x, w, target, lse, dloss, need=need)
+            assert all(a is None or t.equal(a, b) for a, b in zip(one, (dx, dw)))
+        wide = t.full((v, d + 3), float("nan"), dtype=w.dtype, device="cuda")[:, 1:d + 1]
+        wide.copy_(w)
+        check(x, wide, target, dloss)
+        target.fill_(IGNORE)
+        loss, lse, dx, dw = check(x.fill_(float("nan")), w, target, dloss)
+        assert (dx == 0).all() and (dw == 0).all() and (loss == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("n,v,d", [
     (4000, 5000, 776), (1000, 5000, 4104), (9000, 100, 776), (9000, 100, 1000), (500, 1300, 4104),
     (20000, 900, 264), (5000, 100, 2056),
