@@ -20,13 +20,17 @@
 // by which the sums are multiplied in fp32: where all rows weigh the same (a
 // mean), the target's entry p - 1 then rounds by its p alone, and not every row's
 // by the same error of the weight (4096 x 32768 x 4096: errors of dX and dW
-// 0.0019 for 0.0023 to 0.0032, 0.0017 of them their own rounding).  fp32 ones run as two fp16 planes (og_tile.hpp), each
-// row of X and W times a power of two of its own that brings its largest value
-// to [2^13, 2^14).  The logits undo both powers.  For the gradients, whose sums
-// run over rows of W and of X, g is stored divided by both (and times one power
-// of two for all, c, that brings the largest possible value to 2^14): then each
-// product's own rows of W or X cancel inside the sum, and what is left is one
-// power of two for each row of the result.
+// 0.0019 for 0.0023 to 0.0032, 0.0017 of them their own rounding).
+//
+// fp32 ones run as two fp16 planes (og_tile.hpp).  For the logits each row of X (and,
+// forward, of W) has a power of two of its own that brings its largest value to
+// [2^13, 2^14); the epilogue undoes both.  The gradients' sums run over rows of W and
+// of X, whose powers cannot differ inside a sum, so they get planes of one common
+// power each: W's of its largest value, and a second set of X's, row i times the power
+// of two of dloss_i, of the largest |dloss_i| max |X_i| (scan_kernel finds both).  g is
+// stored as (p - [j = t]) times dloss_i's mantissa and 2^14: it serves both products,
+// keeps 22 bits down to probabilities of 2^-16 and some down to 2^-38 whatever the
+// sizes of the rows of X, W and dloss, and stays below 2^14 for rows of zeros too.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -54,8 +58,8 @@ struct Rows {
   float *dloss;
   float *zt;      // the target's logit (forward)
   int *xexp;      // fp32: the exponent of a row of X, by place
-  // fp32: the largest exponent of |dloss| x row maximum of X, and of a row
-  // maximum of W, each + kBias (0: none)
+  // fp32 gradient: the largest exponent of |dloss| x row maximum of X, and of W's
+  // maximum, each + kBias (0: none)
   int *most;
   float *scale;   // bf16: the largest finite |dloss| of the rows that count, or 1
 };
@@ -178,71 +182,150 @@ __global__ __launch_bounds__(256) void copy_kernel(int rows, int cols, const __b
   }
 }
 
-// The same for fp32: two planes of each row times its power of two, whose
-// exponent goes to exp (by place).  A wave takes a row: once for its maximum
-// (the first 768 columns stay in registers), once more for its planes.
-// `most`: the largest exponent of a maximum (and |weight| by place, where
-// given) of all, by an atomic maximum of each block's (which does not depend
-// on their order).  Bound by the bytes: 8191 rows of 384 in 9 us, 50021 of 768 in 54.
+// fp32 rows: a wave takes one, of which the first 768 columns stay in registers
+// between its maximum and its planes.
+constexpr int kHeld = 3;
+
+// The first columns of a row and the largest finite magnitude of all of it, in every lane.
+template <bool VEC>
+__device__ __forceinline__ float row_top(const float *row, int cols, int lane, f32x4 (&held)[kHeld]) {
+  float top = 0;
+  auto larger = [&](const f32x4 v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f);
+  };
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) held[q] = load4<float, VEC>(row + 4 * lane + 256 * q, cols - 4 * lane - 256 * q);
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) larger(held[q]);
+  for (int c = 4 * lane + 256 * kHeld; c < cols; c += 256) larger(load4<float, VEC>(row + c, cols - c));
+  return wave_max(top);
+}
+
+// Four columns' planes, times 2^e, zero beyond the row.
+__device__ __forceinline__ void store_planes(uint16_t *out, int c, f32x4 v, int e) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = __builtin_ldexpf(v[q], e);
+  f16x4 h, l;
+  split4(v, h, l);
+  *reinterpret_cast<f16x4 *>(out + column<2>(c, 0)) = h;
+  *reinterpret_cast<f16x4 *>(out + column<2>(c, 1)) = l;
+}
+
+// A row's planes, padded with zeros to `width` columns, times the power of two that brings its
+// largest value to [2^13, 2^14), whose exponent goes to *exp.  Returns that value.
+template <bool VEC>
+__device__ __forceinline__ float own_planes(const float *row, int cols, uint16_t *out, int width,
+                                            int *exp, int lane) {
+  f32x4 held[kHeld];
+  const float top = row_top<VEC>(row, cols, lane, held);
+  const int e2 = top > 0 ? 14 - (int)__builtin_amdgcn_frexp_expf(top) : 0;
+  if (lane == 0) *exp = e2;
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q)
+    if (4 * lane + 256 * q < width) store_planes(out, 4 * lane + 256 * q, held[q], e2);
+  for (int c = 4 * lane + 256 * kHeld; c < width; c += 256)
+    store_planes(out, c, load4<float, VEC>(row + c, cols - c), e2);
+  return top;
+}
+
+// copy_kernel for fp32: the planes of each row by its own power (forward).  Bound by the bytes:
+// 50021 rows of 768 in 54 us.
 template <bool VEC>
 __global__ __launch_bounds__(256) void planes_kernel(int rows, int cols, const float *x, int64_t ldx,
-                                                     const int *pos, uint16_t *out, int64_t ld,
-                                                     float *clear, int64_t ldc, int *exp,
-                                                     const float *weight, int *most) {
-  constexpr int kHeld = 3;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, width = (int)(ld / 2);
-  int seen = 0;
-  for (int i = blockIdx.x * 4 + w; i < rows; i += gridDim.x * 4) {
-    const float *row = x + i * ldx;
+                                                     const int *pos, uint16_t *out, int64_t ld, int *exp) {
+  const int lane = threadIdx.x & 63;
+  for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < rows; i += gridDim.x * 4) {
     const int to = pos ? pos[i] : i;
-    if (to < 0) {
-      if (clear)
-        for (int c = lane; c < cols; c += 64) clear[i * ldc + c] = 0.0f;
-      continue;
-    }
-    const float by = weight ? weight[to] : 0.5f;  // 0.5: exponent 0
-    f32x4 held[kHeld];
-    float top = 0;
-    auto larger = [&](const f32x4 v) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f);
-    };
-#pragma unroll
-    for (int q = 0; q < kHeld; ++q) held[q] = load4<float, VEC>(row + 4 * lane + 256 * q, cols - 4 * lane - 256 * q);
-#pragma unroll
-    for (int q = 0; q < kHeld; ++q) larger(held[q]);
-    for (int c = 4 * lane + 256 * kHeld; c < cols; c += 256) larger(load4<float, VEC>(row + c, cols - c));
-    top = wave_max(top);
-    const int e2 = top > 0 ? 14 - (int)__builtin_amdgcn_frexp_expf(top) : 0;
-    if (top > 0 && by != 0 && __builtin_isfinite(by))
-      seen = max(seen, kBias + (int)__builtin_amdgcn_frexp_expf(top) + (int)__builtin_amdgcn_frexp_expf(by));
-    if (lane == 0) exp[to] = e2;
-    auto store = [&](int c, f32x4 v) {
-      if (c >= width) return;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], e2);
-      f16x4 h, l;
-      split4(v, h, l);
-      *reinterpret_cast<f16x4 *>(out + to * ld + column<2>(c, 0)) = h;
-      *reinterpret_cast<f16x4 *>(out + to * ld + column<2>(c, 1)) = l;
-    };
-#pragma unroll
-    for (int q = 0; q < kHeld; ++q) store(4 * lane + 256 * q, held[q]);
-    for (int c = 4 * lane + 256 * kHeld; c < width; c += 256) store(c, load4<float, VEC>(row + c, cols - c));
-  }
-  if (most) {
-    __shared__ int block[4];
-    if (lane == 0) block[w] = seen;
-    __syncthreads();
-    if (threadIdx.x == 0) atomicMax(most, max(max(block[0], block[1]), max(block[2], block[3])));
+    if (to >= 0) own_planes<VEC>(x + i * ldx, cols, out + to * ld, (int)(ld / 2), exp + to, lane);
   }
 }
 
-// c of a call (see the top): |g| max |x| max |w| < 2^(both exponents), and the
-// row maxima are 2^13 of the planes' units at least, so that |g 2^c / (both
-// powers)| stays below 2^14.
-__device__ __forceinline__ int common_exponent(const int *most) {
-  return 40 - (most[0] ? most[0] - kBias : 0) - (most[1] ? most[1] - kBias : 0);
+// The fp32 gradient's operands, in two launches.
+struct Sides {
+  int n, d;
+  int64_t v;
+  const float *x, *w;  // (common_kernel: w and v are a piece's)
+  int64_t ldx, ldw, ld;  // ld: elements of a row of planes
+  Rows r;
+  uint16_t *x_own, *x_common, *w_common;
+  float *clear;  // the gradient of rows of X that do not count is zero
+  int64_t ldc;
+  int x_blocks;  // of the launch; the others are W's
+};
+
+// X's planes by row, and the exponents of both common powers: by an atomic maximum of each
+// block's, which does not depend on their order.  W is only read.  Blocks of 16 waves: what
+// the launch takes beyond the bytes' time is its atomics on one address (8191 x 384 and 1000
+// rows of X: 2300 blocks of 4 waves 29 us, 319 of 16 8).
+constexpr int kScanWaves = 16;
+template <bool VEC>
+__global__ __launch_bounds__(64 * kScanWaves) void scan_kernel(Sides a) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const bool first = (int)blockIdx.x < a.x_blocks;
+  int seen = 0;
+  if (first) {
+    for (int i = blockIdx.x * kScanWaves + w; i < a.n; i += a.x_blocks * kScanWaves) {
+      const int to = a.r.pos[i];
+      if (to < 0) {
+        if (a.clear)
+          for (int c = lane; c < a.d; c += 64) a.clear[i * a.ldc + c] = 0.0f;
+        continue;
+      }
+      const float by = a.r.dloss[to];
+      const float top = own_planes<VEC>(a.x + i * a.ldx, a.d, a.x_own + to * a.ld, (int)(a.ld / 2),
+                                        a.r.xexp + to, lane);
+      if (top > 0 && by != 0 && __builtin_isfinite(by))
+        seen = max(seen, kBias + (int)__builtin_amdgcn_frexp_expf(top) + (int)__builtin_amdgcn_frexp_expf(by));
+    }
+  } else {
+    const int block = blockIdx.x - a.x_blocks, blocks = gridDim.x - a.x_blocks;
+    float top = 0;
+    for (int64_t j = block * kScanWaves + w; j < a.v; j += blocks * kScanWaves) {
+      f32x4 held[kHeld];
+      top = fmaxf(top, row_top<VEC>(a.w + j * a.ldw, a.d, lane, held));
+    }
+    if (top > 0) seen = kBias + (int)__builtin_amdgcn_frexp_expf(top);
+  }
+  __shared__ int waves[kScanWaves];
+  if (lane == 0) waves[w] = seen;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kScanWaves; ++k) seen = max(seen, waves[k]);
+    if (seen) atomicMax(a.r.most + (first ? 0 : 1), seen);
+  }
+}
+
+// The exponent of a common power, which brings the largest value to [2^13, 2^14) (of dloss
+// times X: to [2^12, 2^14)).
+__device__ __forceinline__ int common_exponent(int most) { return most ? 14 - (most - kBias) : 0; }
+
+// Planes by the common powers: of a piece of W, and (x_blocks not 0) of X times the powers of
+// two of dloss; a row of dloss zero, whose g is zero, is zero (the same sizes: 6 us).
+template <bool VEC>
+__global__ __launch_bounds__(256) void common_kernel(Sides a) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, width = (int)(a.ld / 2);
+  auto planes = [&](const float *row, uint16_t *out, int e) {
+    for (int c = 4 * lane; c < width; c += 256) store_planes(out, c, load4<float, VEC>(row + c, a.d - c), e);
+  };
+  if ((int)blockIdx.x < a.x_blocks) {
+    const int e = common_exponent(a.r.most[0]);
+    for (int i = blockIdx.x * 4 + w; i < a.n; i += a.x_blocks * 4) {
+      const int to = a.r.pos[i];
+      if (to < 0) continue;
+      const float by = a.r.dloss[to];
+      uint16_t *out = a.x_common + to * a.ld;
+      if (by != 0) {
+        planes(a.x + i * a.ldx, out, e + (int)__builtin_amdgcn_frexp_expf(by));
+      } else {
+        for (int c = 4 * lane; c < width; c += 256) store_planes(out, c, f32x4{0, 0, 0, 0}, 0);
+      }
+    }
+  } else {
+    const int e = common_exponent(a.r.most[1]);
+    for (int64_t j = (int64_t)(blockIdx.x - a.x_blocks) * 4 + w; j < a.v; j += (gridDim.x - a.x_blocks) * 4)
+      planes(a.w + j * a.ldw, a.w_common + j * a.ld, e);
+  }
 }
 
 // Four logits: fp32 sums as they are, or less their rows' powers of two.
@@ -369,8 +452,8 @@ struct GradArgs {
   int64_t ld;
   const int *target;
   const float *lse, *dloss, *scale;
-  const int *xexp, *wexp;
-  const int *most;
+  const int *xexp;
+  const int *most;  // of W
   int v0;
 };
 template <int P>
@@ -381,23 +464,25 @@ struct Grad {
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
-    const int common = P == 2 ? common_exponent(e.most) : 0;
+    const int wexp = P == 2 ? common_exponent(*e.most) : 0;
     const float by = *e.scale;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
-      const float l = e.lse[m], d = P == 2 ? e.dloss[m] : e.dloss[m] / by;
+      const float l = e.lse[m], dl = e.dloss[m];
+      const float d = P == 2 ? __builtin_ldexpf(dl, 14 - (int)__builtin_amdgcn_frexp_expf(dl)) : dl / by;
       const int want = e.target[m] - e.v0 - nc;
-      const int xexp = P == 2 ? e.xexp[m] : 0;
+      const int up = P == 2 ? -(e.xexp[m] + wexp) : 0;
       uint16_t *to = e.g + m * e.ld;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
         if (n >= e.ld / P) continue;
-        f32x4 v = logits<P>(acc[i][j], xexp, e.wexp, n, t.N);
+        f32x4 v = acc[i][j];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          if constexpr (P == 2) v[q] = __builtin_ldexpf(v[q], up);
           const float p = __builtin_amdgcn_exp2f((v[q] - l) * kLog2e);
           v[q] = n + q < t.N ? (want == 16 * j + q ? p - 1.0f : p) * d : 0.0f;
         }
@@ -407,13 +492,7 @@ struct Grad {
           for (int q = 0; q < 4; ++q) h[q] = (__bf16)v[q];
           *reinterpret_cast<bf16x4 *>(to + n) = h;
         } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            v[q] = __builtin_ldexpf(v[q], common - xexp - e.wexp[min(n + q, t.N - 1)]);
-          f16x4 h, l2;
-          split4(v, h, l2);
-          *reinterpret_cast<f16x4 *>(to + column<2>(n, 0)) = h;
-          *reinterpret_cast<f16x4 *>(to + column<2>(n, 1)) = l2;
+          store_planes(to, n, v, 0);
         }
       }
     }
@@ -450,9 +529,9 @@ struct OutArgs {
   int64_t ldo;
   int whole;       // four values of a row of out are one aligned store
   const int *row;  // null: row m is row m of out
-  const int *exp;  // fp32: the exponents of the rows, less the common one
-  const int *most;
-  const float *scale;  // bf16: what g was divided by
+  const int *most;      // fp32: of the other operand, whose common power is undone
+  const float *weight;  // fp32, dX: dloss, of whose power of two g was relieved; else null
+  const float *scale;   // bf16: what g was divided by
 };
 template <class T>
 struct Out {
@@ -462,13 +541,13 @@ struct Out {
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
-    const int common = S::P == 2 ? common_exponent(e.most) : 0;
+    const int common = S::P == 2 ? 14 + common_exponent(*e.most) : 0;
     const float by = *e.scale;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
-      const int up = S::P == 2 ? e.exp[m] - common : 0;
+      const int up = S::P == 2 && e.weight ? (int)__builtin_amdgcn_frexp_expf(e.weight[m]) - common : -common;
       T *to = static_cast<T *>(e.out) + (e.row ? e.row[m] : m) * e.ldo;
       float *sum = e.sum + t.batch * e.part + m * e.lds;
 #pragma unroll
@@ -608,7 +687,7 @@ struct Plan {
   int64_t dp;           // d padded
   int64_t piece;        // vocabulary rows of a piece
   int dx_parts, dw_parts;  // parts of k of a piece's gradient products
-  int64_t rows_at, wexp_at, x_at, w_at, part_at, g_at, sum_at, parts_at, total;
+  int64_t rows_at, wexp_at, x_at, x2_at, w_at, part_at, g_at, sum_at, parts_at, total;
 };
 
 // Parts of k of an m x n product: as many as make up two tiles of 64 x 64 for
@@ -639,12 +718,13 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   p.rows_at = take(256 + 7 * round_up(n, 64) * 4);
   if (p.few) {
     p.part_at = take(kFewWaves * n * 8);
-    p.wexp_at = p.x_at = p.w_at = p.g_at = p.sum_at = p.parts_at = p.total = at;
+    p.wexp_at = p.x_at = p.x2_at = p.w_at = p.g_at = p.sum_at = p.parts_at = p.total = at;
     p.dx_parts = p.dw_parts = 1;
     return p;
   }
-  p.wexp_at = take(p.planes == 2 ? p.piece * 4 : 0);
+  p.wexp_at = take(p.planes == 2 && !grad ? p.piece * 4 : 0);
   p.x_at = take(p.planes * n * p.dp * 2);
+  p.x2_at = grad && p.planes == 2 ? take(p.planes * n * p.dp * 2) : at;  // by the common power
   p.w_at = take(p.planes * p.piece * p.dp * 2);
   p.part_at = grad ? at : take((round_up(v, p.piece) / (p.planes == 2 ? 32 : 64)) * n * 8);
   p.g_at = grad ? take(p.planes * n * p.piece * 2) : at;
@@ -668,8 +748,8 @@ Rows rows_of(char *at, int64_t n) {
 }
 
 void operand_rows(int64_t rows, int64_t cols, const __bf16 *x, int64_t ldx, const int *pos,
-                  uint16_t *out, int64_t dp, __bf16 *clear, int64_t ldc, int *, const float *,
-                  int *, hipStream_t s) {
+                  uint16_t *out, int64_t dp, int *, hipStream_t s, __bf16 *clear = nullptr,
+                  int64_t ldc = 0) {
   const dim3 grid((unsigned)std::min<int64_t>((rows * (dp / 4) + 255) / 256, 8192));
   const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 8 == 0;
   const auto kernel = vec ? copy_kernel<true> : copy_kernel<false>;
@@ -677,13 +757,11 @@ void operand_rows(int64_t rows, int64_t cols, const __bf16 *x, int64_t ldx, cons
                      clear, ldc);
 }
 void operand_rows(int64_t rows, int64_t cols, const float *x, int64_t ldx, const int *pos,
-                  uint16_t *out, int64_t dp, float *clear, int64_t ldc, int *exp,
-                  const float *weight, int *most, hipStream_t s) {
-  const dim3 grid((unsigned)std::min<int64_t>((rows + 3) / 4, most ? 1024 : 4096));
+                  uint16_t *out, int64_t dp, int *exp, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>((rows + 3) / 4, 4096));
   const bool vec = ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   const auto kernel = vec ? planes_kernel<true> : planes_kernel<false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (int)rows, (int)cols, x, ldx, pos, out, 2 * dp,
-                     clear, ldc, exp, weight, most);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, (int)rows, (int)cols, x, ldx, pos, out, 2 * dp, exp);
 }
 
 struct Call {
@@ -696,15 +774,13 @@ struct Call {
 };
 
 // Rows [v0, v0 + c) of W as an operand: in place where the kernels can read
-// it (bf16, whole aligned granules of 8), else its planes in the workspace.
+// it (bf16, whole aligned granules of 8), else its copy or planes in the workspace.
 template <class T, int P>
-Operand weights(const Plan &p, const Call &c, int64_t v0, int64_t rows, bool in_place,
-                int *most, hipStream_t s) {
+Operand weights(const Plan &p, const Call &c, int64_t v0, int64_t rows, bool in_place, hipStream_t s) {
   const T *w = static_cast<const T *>(c.w) + v0 * c.ldw;
   if (in_place) return Operand{reinterpret_cast<const uint16_t *>(w), c.ldw, 0};
   uint16_t *to = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
-  operand_rows(rows, c.d, w, c.ldw, nullptr, to, p.dp, (T *)nullptr, 0,
-               reinterpret_cast<int *>(c.ws + p.wexp_at), nullptr, most, s);
+  operand_rows(rows, c.d, w, c.ldw, nullptr, to, p.dp, reinterpret_cast<int *>(c.ws + p.wexp_at), s);
   return Operand{to, P * p.dp, 0};
 }
 template <class T>
@@ -728,11 +804,15 @@ void few_forward(const Call &c, const Rows &r, float2 *part, int waves, hipStrea
                      (int)c.d, static_cast<const float *>(c.x), c.ldx, static_cast<const float *>(c.w),
                      c.ldw, part);
 }
+// Whether four fp32 values of a row of X or W are one aligned load.
+bool whole_loads(const Call &c) {
+  return c.ldx % 4 == 0 && c.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(c.w) % 16 == 0;
+}
 // f(N, VEC) for a call of few rows.
 template <class F>
 void few(const Call &c, F f) {
-  const bool vec = c.ldx % 4 == 0 && c.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(c.w) % 16 == 0;
+  const bool vec = whole_loads(c);
   auto by = [&](auto n) {
     if (vec) f(n, std::true_type());
     else f(n, std::false_type());
@@ -758,8 +838,7 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
                        (int)c.n, waves, loss, lse);
     return;
   }
-  operand_rows(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, (T *)nullptr, 0,
-               r.xexp, nullptr, nullptr, s);
+  operand_rows(c.n, c.d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, r.xexp, s);
   float2 *part = reinterpret_cast<float2 *>(c.ws + p.part_at);
   const bool in_place = readable<T>(c);
   // (a launch's tiles stay far below 2^32 threads)
@@ -767,7 +846,7 @@ void forward(const Plan &p, const Call &c, float *loss, float *lse, hipStream_t 
   int tiles = 0;
   for (int64_t v0 = 0; v0 < c.v; v0 += piece) {
     const int rows = (int)std::min(piece, c.v - v0);
-    const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, nullptr, s);
+    const Operand X{x, P * p.dp, 0}, W = weights<T, P>(p, c, v0, rows, in_place, s);
     tiles += product<Element<T>, P, false, false, Lse<P>>(
         Args{X, W, (int)c.n, rows, (int)c.d, r.count, 0, 0, 0, 0},
         LseArgs{part, r.target, r.zt, r.xexp, wexp, (int)c.n, (int)v0, tiles}, 1, s);
@@ -786,7 +865,7 @@ void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s)
   }
   float *from = reinterpret_cast<float *>(ws);
   g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, 0, nullptr, o.exp, o.most,
+  const OutArgs part{from, o.lds, room * o.lds, 1, 0, nullptr, 0, 0, nullptr, o.most, o.weight,
                      o.scale};
   product<Element<T>, P, TA, true, Out<T>>(g, part, parts, s);
   const int64_t quads = (int64_t)g.M * ((g.N + 3) / 4);
@@ -796,41 +875,64 @@ void summed(Args g, int parts, OutArgs o, int64_t room, char *ws, hipStream_t s)
                      o.row);
 }
 
+// The launches of the fp32 gradient's operands (see Sides).
+void scan(const Plan &p, const Call &c, const Rows &r, float *dx, int64_t lddx, hipStream_t s) {
+  auto blocks = [](int64_t rows) { return (int)std::min<int64_t>((rows + kScanWaves - 1) / kScanWaves, 256); };
+  const Sides a{(int)c.n, (int)c.d, c.v, static_cast<const float *>(c.x), static_cast<const float *>(c.w), c.ldx,
+                c.ldw, 2 * p.dp, r, reinterpret_cast<uint16_t *>(c.ws + p.x_at), nullptr, nullptr, dx, lddx,
+                blocks(c.n)};
+  const auto kernel = whole_loads(c) ? scan_kernel<true> : scan_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(a.x_blocks + blocks(c.v)), dim3(64 * kScanWaves), 0, s, a);
+}
+Operand common(const Plan &p, const Call &c, const Rows &r, int64_t v0, int64_t rows, bool x, hipStream_t s) {
+  auto blocks = [](int64_t rows) { return (int)std::min<int64_t>((rows + 3) / 4, 4096); };
+  uint16_t *w = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
+  const Sides a{(int)c.n, (int)c.d, rows, static_cast<const float *>(c.x),
+                static_cast<const float *>(c.w) + v0 * c.ldw, c.ldx, c.ldw, 2 * p.dp, r, nullptr,
+                reinterpret_cast<uint16_t *>(c.ws + p.x2_at), w, nullptr, 0, x ? blocks(c.n) : 0};
+  const auto kernel = whole_loads(c) ? common_kernel<true> : common_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(a.x_blocks + blocks(rows)), dim3(256), 0, s, a);
+  return Operand{w, a.ld, 0};
+}
+
 template <class T, int P>
 void gradient(const Plan &p, const Call &c, const float *lse, const float *dloss, T *dx,
               int64_t lddx, T *dw, int64_t lddw, hipStream_t s) {
   const Rows r = rows_of(c.ws + p.rows_at, c.n);
   uint16_t *x = reinterpret_cast<uint16_t *>(c.ws + p.x_at);
   uint16_t *g = reinterpret_cast<uint16_t *>(c.ws + p.g_at);
-  const int *wexp = reinterpret_cast<const int *>(c.ws + p.wexp_at);
   const int n = (int)c.n, d = (int)c.d;
-  const Operand X{x, P * p.dp, 0}, G{g, P * p.piece, 0};
+  // X for the logits and for dW
+  const Operand X{x, P * p.dp, 0}, G{g, P * p.piece, 0},
+      X2{P == 2 ? reinterpret_cast<uint16_t *>(c.ws + p.x2_at) : x, P * p.dp, 0};
   // (n = 0 runs this too: it clears what the epilogues read)
   hipLaunchKernelGGL(rows_kernel, dim3(1), dim3(1024), 0, s, n, c.v, c.target, c.ignore, r, lse,
                      dloss, (float *)nullptr, (float *)nullptr);
-  if (n > 0)
-    operand_rows(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, dx, lddx, r.xexp,
-                 r.dloss, r.most, s);
+  if (n > 0) {
+    if constexpr (P == 2) scan(p, c, r, dx, lddx, s);
+    else operand_rows(n, d, static_cast<const T *>(c.x), c.ldx, r.pos, x, p.dp, nullptr, s, dx, lddx);
+  }
   const bool in_place = readable<T>(c);
   for (int64_t v0 = 0; v0 < c.v; v0 += p.piece) {
     const int rows = (int)std::min(p.piece, c.v - v0);
     if (n > 0) {
-      const Operand W = weights<T, P>(p, c, v0, rows, in_place, r.most + 1, s);
+      Operand W;
+      if constexpr (P == 2) W = common(p, c, r, v0, rows, v0 == 0 && dw, s);
+      else W = weights<T, P>(p, c, v0, rows, in_place, s);
       product<Element<T>, P, false, false, Grad<P>>(
           Args{X, W, n, rows, d, r.count, 0, 0, 0, 0},
-          GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, r.scale, r.xexp, wexp, r.most, (int)v0},
-          1, s);
+          GradArgs{g, P * p.piece, r.target, r.lse, r.dloss, r.scale, r.xexp, r.most + 1, (int)v0}, 1, s);
       if (dx)
         summed<T, P, false>(Args{G, W, n, d, rows, r.count, 0, 0, 0, 0}, p.dx_parts,
                             OutArgs{reinterpret_cast<float *>(c.ws + p.sum_at), p.dp, 0, v0 == 0,
-                                    v0 + p.piece >= c.v, dx, lddx, whole(dx, lddx), r.row, r.xexp, r.most,
+                                    v0 + p.piece >= c.v, dx, lddx, whole(dx, lddx), r.row, r.most + 1, r.dloss,
                                     r.scale},
                             n, c.ws + p.parts_at, s);
     }
     if (dw)
-      summed<T, P, true>(Args{G, X, rows, d, n, r.count, 1, 0, 0, 0}, p.dw_parts,
+      summed<T, P, true>(Args{G, X2, rows, d, n, r.count, 1, 0, 0, 0}, p.dw_parts,
                          OutArgs{nullptr, p.dp, 0, 1, 1, dw + v0 * lddw, lddw, whole(dw, lddw), nullptr,
-                                 wexp, r.most, r.scale},
+                                 r.most, nullptr, r.scale},
                          std::min(p.piece, c.v), c.ws + p.parts_at, s);
   }
 }

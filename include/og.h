@@ -388,11 +388,13 @@ og_status og_linear_cross_entropy(int64_t n, int64_t v, int64_t d, const void *X
  * both of `type`, overwritten; either may be NULL (not wanted).  The logits
  * are recomputed in pieces of the vocabulary; the sums over the vocabulary and
  * over the rows are fp32, rounded once.  For OG_BF16 g, divided by the largest
- * |dloss|, is rounded to bf16.  For OG_F32 it has 22 bits, down to about 2^-37 of M / (max |X_i| max |W_j|), M
- * the largest |dloss_i| max |X_i| of any row times the largest |W|: what is
- * below that adds nothing, so rows whose dloss is many orders smaller than
- * another's, and entries of dW that only tiny probabilities make, have the
- * errors of M's size rather than of their own.  Rows that do not count have
+ * |dloss|, is rounded to bf16.  For OG_F32 g / dloss keeps 22 bits of
+ * probabilities down to 2^-16, of smaller ones what lies above 2^-39: an entry of
+ * dW that only probabilities below that make is 0.  That holds whatever the
+ * sizes of the rows of X, W and dloss; rows of zeros are no exception.  Here W is
+ * held as two fp16 planes times one power of two for all of it (22 bits of each
+ * value, down to 2^-38 of the largest), and so is, for dW, X with each row times
+ * its dloss, down to 2^-37 of the largest such value.  Rows that do not count have
  * zero gradient whatever dloss and lse hold there, and add nothing to dW;
  * n == 0 clears dW.  The outputs must not overlap the inputs.  Otherwise as
  * above, with a workspace of og_linear_cross_entropy_workspace(n, v, d, type,
