@@ -1,5 +1,5 @@
-// og_ns.hip -- og_newton_schulz_f32 / _bf16: the orthogonalised update of a
-// matrix by Newton-Schulz products.
+// og_ns.hip -- og_newton_schulz: the orthogonalised update of a matrix by
+// Newton-Schulz products.
 //
 //   X = G / (|G| + eps)   (the Frobenius norm; the shorter side as rows, r <= k)
 //   each step:  A = X X^T,  B = b A + c A A,  X <- a X + B X
@@ -15,9 +15,10 @@
 // through a X).
 //
 // Each matrix is stored times a power of two that its largest possible value
-// sets: the singular values of X stay below s (1 at first, then the largest
-// |p| over [0, s]), those of A below s^2 and those of B below the largest
-// |b x^2 + c x^4|, all found on the host from the coefficients alone.
+// sets: the singular values of X stay below s (at first the power of two from
+// |G| / (|G| + eps) on, 1 where eps is small, then the largest |p| over [0, s]),
+// those of A below s^2 and those of B below the largest |b x^2 + c x^4|.  The
+// first s is known on the device only, and with it the others (pack_kernel).
 //
 // A and A A are symmetric: only the tiles on and below the diagonal are
 // computed and each is stored to both places, a quarter of the step's work at
@@ -106,12 +107,80 @@ __global__ __launch_bounds__(256) void norm_kernel(Input in, double *part) {
   if (threadIdx.x == 0) part[batch * kNormBlocks + blockIdx.x] = sum[0];
 }
 
+// The polynomial a x + b x^3 + c x^5 of a step, and b x^2 + c x^4 of B, with their extreme values
+// besides those at the ends: the squares of their places and the values there (place 0: none).
+struct Poly {
+  double a, b, c;
+  double next_at[2], next_top[2], factor_at, factor_top;
+  __host__ __device__ double p(double x) const { return fabs((a + (b + c * x * x) * x * x) * x); }
+  __host__ __device__ double f(double square) const { return fabs((b + c * square) * square); }
+  // The largest over [0, s]; a hundredth more is for the roundings.
+  __host__ __device__ double largest_next(double s) const {
+    double top = p(s);
+    for (int i = 0; i < 2; ++i)
+      if (next_at[i] > 0 && next_at[i] < s * s && next_top[i] > top) top = next_top[i];
+    return top * 1.01;
+  }
+  __host__ __device__ double largest_factor(double s) const {
+    const double top = f(s * s);
+    return (factor_at > 0 && factor_at < s * s && factor_top > top ? factor_top : top) * 1.01;
+  }
+};
+Poly poly(double a, double b, double c) {
+  Poly p{a, b, c, {0, 0}, {0, 0}, 0, 0};
+  // where the derivative, a quadratic in x^2, is zero
+  const double d = 9 * b * b - 20 * a * c;
+  if (c == 0) {
+    if (b != 0) p.next_at[0] = -a / (3 * b);
+  } else if (d >= 0) {
+    p.next_at[0] = (-3 * b + std::sqrt(d)) / (10 * c);
+    p.next_at[1] = (-3 * b - std::sqrt(d)) / (10 * c);
+  }
+  for (int i = 0; i < 2; ++i)
+    if (p.next_at[i] > 0) p.next_top[i] = p.p(std::sqrt(p.next_at[i]));
+  if (c != 0) p.factor_at = -b / (2 * c);
+  p.factor_top = p.f(p.factor_at);
+  return p;
+}
+
+// The exponent that brings values up to `bound` to 2^14 (a quarter of fp16's
+// range: the bound is exact arithmetic's).
+__device__ __forceinline__ int exponent(double bound, int most) {
+  int e = 0;
+  if (bound > 0 && bound < HUGE_VAL) frexp(bound, &e);
+  return min(most, max(-60, 14 - e));
+}
+// Of X: values below 2^-144 vanish, as they do in fp32.
+constexpr int kMostX = 120;
+
+constexpr int kMaxSteps = 64;
+// What the epilogues of a step multiply by, (a, c) of each of its three products.
+struct Factors {
+  float2 of[kMaxSteps][3];
+};
+// X's singular values are at most 2^q at first, its planes times 2^ex.
+__device__ void factors(const Poly &p, int q, int ex, int steps, Factors &to) {
+  double top = ldexp(1.0, q);
+  for (int i = 0; i < steps; ++i) {
+    const int ea = exponent(top * top, 400), eb = exponent(p.largest_factor(top), 800);
+    const double next = p.largest_next(top);
+    const int en = i + 1 == steps ? 0 : exponent(next, kMostX);
+    to.of[i][0] = {0.0f, (float)ldexp(1.0, ea - 2 * ex)};
+    to.of[i][1] = {(float)ldexp(p.b, eb - ea), (float)ldexp(p.c, eb - 2 * ea)};
+    to.of[i][2] = {(float)ldexp(p.a, en - ex), (float)ldexp(1.0, en - eb - ex)};
+    top = next;
+    ex = en;
+  }
+}
+
 // X's planes from G: 64 x 64 tiles through LDS (G is read along its rows
-// whichever way X lies), padded with zeros to a multiple of 64 columns.  Bound
-// by the bytes of both planes: 4096 x 11008 bf16 (270 MB) in 88 us.
+// whichever way X lies), padded with zeros to a multiple of 64 columns.  One thread
+// of a matrix's first block writes the factors of all steps.  Bound by the bytes of
+// both planes: 4096 x 11008 bf16 (270 MB) in 88 us.
 template <class T, int P, bool TALL>
 __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part, int blocks,
-                                                   float eps, float scale, Wide<P> x) {
+                                                   float eps, Poly poly, int steps, Factors *out,
+                                                   Wide<P> x) {
   __shared__ float tile[64][65];
   __shared__ double factor;
   const int batch = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
@@ -129,7 +198,14 @@ __global__ __launch_bounds__(256) void pack_kernel(Input in, const double *part,
     double s = 0;
     for (int i = threadIdx.x; i < blocks; i += 64) s += part[batch * kNormBlocks + i];
     for (int h = 32; h > 0; h >>= 1) s += __shfl_xor(s, h);
-    if (threadIdx.x == 0) factor = scale / (sqrt(s) + (double)eps);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(s), size = norm / (norm + (double)eps);
+      int q = 0;  // (a matrix of zeros or one that is not finite is so with any power)
+      if (size > 0 && size < 1 && frexp(size, &q) == 0.5) --q;
+      const int ex = min(13 - q, kMostX);
+      factor = ldexp(1.0, ex) / (norm + (double)eps);
+      if (blockIdx.x == 0 && blockIdx.y == 0) factors(poly, q, ex, steps, out[batch]);
+    }
   }
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
@@ -191,7 +267,8 @@ struct Square {
 template <int P>
 struct SymArgs {
   Square<P> out, was;  // was.p null: acc c alone
-  float a, c;
+  const Factors *by;   // by matrix
+  int step, product;   // by->of[step][product]: a and c
 };
 template <int P>
 struct Sym {
@@ -202,6 +279,7 @@ struct Sym {
                                                const Args &e) {
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
     const int width = (int)(e.out.ld / P);
+    const float2 by = e.by[t.batch].of[e.step][e.product];
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
@@ -213,7 +291,7 @@ struct Sym {
         if (e.was.p && in) v = e.was.load(t.batch, m, n);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          v[q] = m < t.M && n + q < t.N ? fmaf(e.c, acc[i][j][q], e.a * v[q]) : 0.0f;
+          v[q] = m < t.M && n + q < t.N ? fmaf(by.y, acc[i][j][q], by.x * v[q]) : 0.0f;
         e.out.store(t.batch, m, n, v, in, t.tile_m != t.tile_n && m < width, t.N);
       }
     }
@@ -227,7 +305,8 @@ struct Sym {
 template <int P>
 struct NextArgs {
   Wide<P> x, out;
-  float a, c;
+  const Factors *by;  // by->of[step][2]: a and c
+  int step;
   void *o;  // the result, after the last step; else null
   int64_t ldo, batch_o;
   int tall;   // the result is X's transpose
@@ -241,6 +320,7 @@ struct Next {
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t,
                                                const Args &e) {
     const int mr = t.m0 + (t.lane & 15), nc = t.n0 + 4 * (t.lane >> 4);
+    const float2 by = e.by[t.batch].of[e.step][2];
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = mr + 16 * i;
@@ -250,7 +330,7 @@ struct Next {
         if (m >= t.M || n >= e.x.width) continue;
         f32x4 v = e.x.load(t.batch, m, n);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(e.c, acc[i][j][q], e.a * v[q]) : 0.0f;
+        for (int q = 0; q < 4; ++q) v[q] = n + q < t.N ? fmaf(by.y, acc[i][j][q], by.x * v[q]) : 0.0f;
         if (!e.o) {
           e.out.store(t.batch, m, n, v);
         } else {
@@ -275,8 +355,8 @@ struct Next {
 struct Plan {
   int r, k, planes;                      // planes of A, B and of the products' operands
   int64_t rp, kp;                        // r and k padded to blocks of 64
-  int64_t x_bytes, a_bytes, norm_bytes;  // of one buffer, over the batch
-  int64_t total() const { return norm_bytes + 2 * x_bytes + 2 * a_bytes; }
+  int64_t x_bytes, a_bytes, norm_bytes, factor_bytes;  // of one buffer, over the batch
+  int64_t total() const { return norm_bytes + factor_bytes + 2 * x_bytes + 2 * a_bytes; }
 };
 
 Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
@@ -289,106 +369,58 @@ Plan plan(int64_t batch, int64_t m, int64_t n, int type) {
   p.x_bytes = round_up(batch * 2 * p.r * p.kp * 2, 256);
   p.a_bytes = round_up(batch * p.planes * p.r * p.rp * 2, 256);
   p.norm_bytes = round_up(batch * kNormBlocks * 8, 256);
+  p.factor_bytes = round_up(batch * (int64_t)sizeof(Factors), 256);
   return p;
 }
 
-// The largest |a x + b x^3 + c x^5| over [0, s]: at s or where the derivative
-// is zero (a quadratic in x^2); and |b x^2 + c x^4|, the same for its own.  A
-// hundredth more is for the roundings.
-double largest_next(double a, double b, double c, double s) {
-  auto p = [&](double x) { return std::fabs((a + (b + c * x * x) * x * x) * x); };
-  double top = p(s);
-  auto at = [&](double square) {
-    if (square > 0 && square < s * s) top = std::max(top, p(std::sqrt(square)));
-  };
-  const double d = 9 * b * b - 20 * a * c;
-  if (c == 0) {
-    if (b != 0) at(-a / (3 * b));
-  } else if (d >= 0) {
-    at((-3 * b + std::sqrt(d)) / (10 * c));
-    at((-3 * b - std::sqrt(d)) / (10 * c));
-  }
-  return top * 1.01;
-}
-double largest_factor(double b, double c, double s) {
-  auto f = [&](double square) { return std::fabs((b + c * square) * square); };
-  double top = f(s * s);
-  if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < s * s) top = std::max(top, f(-b / (2 * c)));
-  return top * 1.01;
-}
-
-// The exponent that brings values up to `bound` to 2^14 (a quarter of fp16's
-// range: the bound is exact arithmetic's).
-int exponent(double bound) {
-  int e = 0;
-  if (bound > 0 && std::isfinite(bound)) std::frexp(bound, &e);
-  return std::min(60, std::max(-60, 14 - e));
-}
-
 // Whether every matrix has its power of two: the bounds of X before each step
-// within [2^-23, 2^37] (or zero), so that A's stay within the exponents above,
-// and those of B below 2^74.
-bool in_range(int steps, double a, double b, double c) {
+// within [2^-23, 2^37] (or zero) where it starts at 1, so that A's stay within the
+// exponents above, and those of B below 2^74.
+bool in_range(int steps, const Poly &p) {
   double top = 1;
   for (int i = 0; i < steps; ++i) {
     if (top != 0 && !(top >= std::ldexp(1.0, -23) && top <= std::ldexp(1.0, 37))) return false;
-    if (!(largest_factor(b, c, top) <= std::ldexp(1.0, 74))) return false;
-    top = largest_next(a, b, c, top);
+    if (!(p.largest_factor(top) <= std::ldexp(1.0, 74))) return false;
+    top = p.largest_next(top);
   }
   return true;
 }
 
 template <class T, int P>
-void run(const Plan &p, const Input &in, int batch, int steps, float a, float b, float c, float eps,
-         void *o, int64_t ldo, int64_t stride_o, char *ws, hipStream_t s) {
+void run(const Plan &p, const Input &in, int batch, int steps, const Poly &poly, float eps, void *o,
+         int64_t ldo, int64_t stride_o, char *ws, hipStream_t s) {
   double *norm = reinterpret_cast<double *>(ws);
+  Factors *by = reinterpret_cast<Factors *>(ws + p.norm_bytes);
+  char *planes = ws + p.norm_bytes + p.factor_bytes;
   const bool tall = in.m > in.n;
   const bool whole = !tall && ldo % 4 == 0 && stride_o % 4 == 0 &&
                      reinterpret_cast<uintptr_t>(o) % (4 * sizeof(T)) == 0;
   const int64_t lda = P * p.rp, ab = p.r * lda;
   Wide<P> x[2];
   for (int i = 0; i < 2; ++i) {
-    x[i].p = reinterpret_cast<uint16_t *>(ws + p.norm_bytes + i * p.x_bytes);
+    x[i].p = reinterpret_cast<uint16_t *>(planes + i * p.x_bytes);
     x[i].ld = P * p.kp;
     x[i].batch = p.r * x[i].ld;
     x[i].plane = batch * x[i].batch;
     x[i].width = (int)p.kp;
   }
-  Square<P> A{reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes), lda, ab};
-  Square<P> B{reinterpret_cast<uint16_t *>(ws + p.norm_bytes + 2 * p.x_bytes + p.a_bytes), lda, ab};
-  double top = 1;  // of X's singular values
-  int ex = exponent(top);
+  Square<P> A{reinterpret_cast<uint16_t *>(planes + 2 * p.x_bytes), lda, ab};
+  Square<P> B{reinterpret_cast<uint16_t *>(planes + 2 * p.x_bytes + p.a_bytes), lda, ab};
   const int blocks = std::min(kNormBlocks, in.m);
   hipLaunchKernelGGL(norm_kernel<T>, dim3(blocks, batch), dim3(256), 0, s, in, norm);
   const dim3 grid((unsigned)(p.kp / 64), (unsigned)(p.rp / 64), batch);
-  const float first = std::ldexp(1.0f, ex);
-  if (tall)
-    hipLaunchKernelGGL((pack_kernel<T, P, true>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       first, x[0]);
-  else
-    hipLaunchKernelGGL((pack_kernel<T, P, false>), grid, dim3(256), 0, s, in, norm, blocks, eps,
-                       first, x[0]);
+  const auto pack = tall ? pack_kernel<T, P, true> : pack_kernel<T, P, false>;
+  hipLaunchKernelGGL(pack, grid, dim3(256), 0, s, in, norm, blocks, eps, poly, steps, by, x[0]);
   for (int i = 0; i < steps; ++i) {
     const Wide<P> &from = x[i & 1], &to = x[(i + 1) & 1];
-    const bool last = i + 1 == steps;
-    const int ea = exponent(top * top);
-    const int eb = exponent(largest_factor(b, c, top));
-    const double next = largest_next(a, b, c, top);
-    const int en = last ? 0 : exponent(next);
     const Operand X{from.p, from.ld, from.batch}, OA{A.p, lda, ab}, OB{B.p, lda, ab};
-    product<_Float16, P, false, false, Sym<P>>(
-        Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0, 0},
-        SymArgs<P>{A, Square<P>{nullptr, 0, 0}, 0, std::ldexp(1.0f, ea - 2 * ex)}, batch, s);
-    product<_Float16, P, false, false, Sym<P>>(
-        Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0, 0},
-        SymArgs<P>{B, A, std::ldexp(b, eb - ea), std::ldexp(c, eb - 2 * ea)}, batch, s);
+    product<_Float16, P, false, false, Sym<P>>(Args{X, X, p.r, p.r, p.k, nullptr, 0, 0, 0, 0},
+                                               SymArgs<P>{A, Square<P>{nullptr, 0, 0}, by, i, 0}, batch, s);
+    product<_Float16, P, false, false, Sym<P>>(Args{OA, OA, p.r, p.r, p.r, nullptr, 0, 0, 0, 0},
+                                               SymArgs<P>{B, A, by, i, 1}, batch, s);
     product<_Float16, P, false, true, Next<P, T>>(
         Args{OB, X, p.r, p.k, p.r, nullptr, 0, 0, 0, 0},
-        NextArgs<P>{from, to, std::ldexp(a, en - ex), std::ldexp(1.0f, en - eb - ex),
-                    last ? o : nullptr, ldo, stride_o, tall, whole},
-        batch, s);
-    top = next;
-    ex = en;
+        NextArgs<P>{from, to, by, i, i + 1 == steps ? o : nullptr, ldo, stride_o, tall, whole}, batch, s);
   }
 }
 
@@ -424,10 +456,11 @@ og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, i
   using namespace og::host;
   og_status st = og::ns::check_sizes(batch, m, n, type);
   if (st != OG_OK) return st;
-  if (steps < 1 || steps > 64) return fail(OG_ERR_INVALID_ARG, "steps %d: 1 to 64", steps);
+  if (steps < 1 || steps > og::ns::kMaxSteps) return fail(OG_ERR_INVALID_ARG, "steps %d: 1 to 64", steps);
   if (!(eps >= 0) || !std::isfinite(eps) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
     return fail(OG_ERR_INVALID_ARG, "eps must be finite and not negative, a, b and c finite");
-  if (!og::ns::in_range(steps, a, b, c))
+  const og::ns::Poly poly = og::ns::poly(a, b, c);
+  if (!og::ns::in_range(steps, poly))
     return fail(OG_ERR_INVALID_ARG, "coefficients that may bring X's singular values out of "
                 "[2^-23, 2^37] before the last step, or b A + c A A past 2^74");
   if (ldg < std::max<int64_t>(1, n) || ldo < std::max<int64_t>(1, n))
@@ -447,13 +480,13 @@ og_status og_newton_schulz(int64_t batch, int64_t m, int64_t n, const void *G, i
   if ((st = check_device()) != OG_OK) return st;
   const og::ns::Input in{G, ldg, strideg, (int)m, (int)n};
   if (type == OG_F32)
-    og::ns::run<float, 2>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+    og::ns::run<float, 2>(p, in, (int)batch, steps, poly, eps, O, ldo, strideo,
                           static_cast<char *>(workspace), current_stream());
   else if (p.planes == 2)
-    og::ns::run<__bf16, 2>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+    og::ns::run<__bf16, 2>(p, in, (int)batch, steps, poly, eps, O, ldo, strideo,
                            static_cast<char *>(workspace), current_stream());
   else
-    og::ns::run<__bf16, 1>(p, in, (int)batch, steps, a, b, c, eps, O, ldo, strideo,
+    og::ns::run<__bf16, 1>(p, in, (int)batch, steps, poly, eps, O, ldo, strideo,
                            static_cast<char *>(workspace), current_stream());
   return check_launch("newton_schulz");
 }

@@ -331,7 +331,9 @@ og_status og_gemm_nt_q4(int64_t m, int64_t n, int64_t k, const void *A, int type
  *
  * G and O are of `type` (OG_F32 or OG_BF16); O may be G itself with the same
  * strides, and must not overlap it otherwise.  |G| is summed in 64 bits.
- * X is held as two fp16 planes (22 bits) times a power of two.  For OG_F32 A
+ * X is held as two fp16 planes times a power of two of its own (22 bits of each
+ * value, down to 2^-37 of the largest singular value that X can have before the
+ * step, from |G| / (|G| + eps) on: a G far below eps keeps its bits).  For OG_F32 A
  * and b A + c A A are too, and every product takes both planes (errors of fp32
  * products); for OG_BF16 the products take one plane of each (11 bits), X
  * keeps both between the steps, and the result is rounded to bf16 once.  G = 0
