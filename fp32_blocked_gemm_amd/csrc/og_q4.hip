@@ -290,11 +290,13 @@ struct Chunk {
   template <bool FULL>
   __device__ __forceinline__ void load(const Problem &p, const T *const (&a)[MT], const bool (&in)[MT],
                                        const int64_t (&n)[NT], int c, int g) {
-    const int k = c * 128, u = group_of(p, min(k + 32 * g, p.k - 1));
+    const int k = c * 128, u = group_of(p, k + 32 * g);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       w[t] = load_codes<FULL>(p.q + n[t] * p.ldq, k + 32 * g, p.k);
-      gr[t].load(p, n[t], u);
+      // (a lane group past the row has a zero sum, which an infinite scale would make NaN)
+      if (FULL || k + 32 * g < p.k) gr[t].load(p, n[t], u);
+      else gr[t] = Group{0, 0};
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
