@@ -245,12 +245,16 @@ struct Planes {
       if constexpr (P == 1) {
         out[0][e] = x.v[from];
       } else {
-        float r = x.v[from];
+        // by cutting, not rounding: each plane takes the next 8 bits, 24 in all, and the largest
+        // values have no bf16 above them to become infinite (a NaN is made quiet first: its
+        // highest mantissa bit then stays)
+        float r = __builtin_canonicalizef(x.v[from]);
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-          const __bf16 h = (__bf16)r;
-          out[q][e] = h;
-          r = __builtin_isfinite((float)h) ? r - (float)h : 0.0f;
+          const uint32_t top = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
+          const float h = __builtin_bit_cast(float, top);
+          out[q][e] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
+          r = __builtin_isfinite(h) ? r - h : 0.0f;
         }
       }
     }

@@ -1,5 +1,5 @@
-"""The product with 4-bit weights: infinite and NaN scales, activations that
-are not finite and every zero point, through each of its kernels (by rows
+"""The product with 4-bit weights: infinite and NaN scales, activations at the
+ends of their types and every zero point, through each of its kernels (by rows
 of A)."""
 import pytest
 
@@ -60,6 +60,24 @@ def test_activations_that_are_not_finite(m, dtype):
             rest = [i for i in range(m) if i != m // 2]
             exact, bound = ref.q4(a[rest], q, s, None, group)
             assert ((out[rest] - exact).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("m", ROWS)
+def test_the_largest_fp32_activations(m):
+    """Values past the largest bf16 (up to the largest fp32) times 1 or -1, halved by the scale."""
+    t = torch()
+    n, k, group = 20, 160, 32
+    q = t.full((n, k // 2), 0x99, dtype=t.uint8, device="cuda")
+    q[1::2] = 0x77
+    s = t.full((n, k // group), 0.5, device="cuda")
+    top = t.finfo(t.float32).max
+    for p, value in ((0, top), (33, -top), (159, 3.39e38), (64, 3.3961775e38), (65, -3.4e38)):
+        a = t.zeros((m, k), device="cuda")
+        a[:, p] = value
+        say(f"q4 {m}x{n}x{k} {value} at {p}")
+        out = og.gemm_nt_q4(a, q, s, group=group)
+        exact, bound = ref.q4(a, q, s, None, group)
+        assert ((out.double() - exact).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
