@@ -307,9 +307,13 @@ int og_gemm_choice(int64_t m, int64_t n, int64_t k, int mode);
  * OG_BF16 or OG_F16 each).  C is overwritten, its gaps are not.
  *
  * A is multiplied by the whole numbers q - z with fp32 sums (of fp16 and bf16
- * activations exactly, of fp32 ones to 24 bits); each sum of at least 32 terms
- * is multiplied by its group's scale in fp32.  Infinities and NaN act as in
- * the formula.  The weights are read once for each 32 rows of A: it is the
+ * activations exactly, of fp32 ones to 24 bits); the sum of 32 terms, p from a
+ * multiple of 32 on, is multiplied by its group's scale in fp32.  Infinities and
+ * NaN act in that order: as in the formula where they are activations (times
+ * q - z = 0 they are NaN), while a scale that is not finite multiplies the sums of
+ * 32 terms, whose single zeros it does not make NaN; and a sum before its scale
+ * that leaves fp32's range is infinite whatever the scale.
+ * The weights are read once for each 32 rows of A: it is the
  * product of single tokens and small batches.
  * Requirements: m, n, k >= 0; group a multiple of 32, >= 32; lda >= max(1,k),
  * ldq >= max(1, ceil(k/2)), lds and ldz >= max(1, ceil(k/group)), ldc >=

@@ -41,6 +41,32 @@ def test_scales_that_are_not_finite(k, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m", ROWS)
+def test_scales_multiply_sums_of_32(m, dtype):
+    """Activations and codes with zeros, signs and sums of zero among them: infinite scales give
+    what they give times each sum of 32 terms.  Whole numbers below 2^12 times a half: the finite
+    results are exact in fp32 and rounded once."""
+    t = torch()
+    n, k, group = 50, 320, 64
+    gen = t.Generator().manual_seed(m)
+    q = t.randint(0, 256, (n, k // 2), generator=gen, dtype=t.uint8).cuda()
+    a = t.randint(-1, 2, (m, k), generator=gen).to(getattr(t, dtype)).cuda()
+    a[:, 96:128] = 0
+    s = t.full((n, k // group), 0.5, device="cuda")
+    s[::3, 0], s[1::5, 1], s[2::7, 4], s[::11, 4] = float("inf"), float("-inf"), float("inf"), float("-inf")
+    sums = (ref.q4_weights(q, t.ones_like(s), None, k, group)[None] * a.double()[:, None]).view(m, n, k // 32, 32).sum(3)
+    want = (sums * s.double().repeat_interleave(2, 1)[None]).sum(2)
+    say(f"q4 {m}x{n}x{k} {dtype}")
+    out = og.gemm_nt_q4(a, q, s, group=group).double()
+    assert want.isinf().any() and want.isnan().any()
+    assert t.equal(out.isnan(), want.isnan())
+    inf = want.isinf()
+    assert t.equal(out[inf], want[inf])
+    fin = want.isfinite()
+    assert ((out - want).abs()[fin] <= ref.half_step(getattr(t, dtype)) * want.abs()[fin]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", ROWS)
 def test_activations_that_are_not_finite(m, dtype):
     t = torch()
     n, k, group = 40, 320, 64
