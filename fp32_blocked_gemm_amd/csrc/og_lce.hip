@@ -16,6 +16,9 @@
 // piece and runs both products on it.  All of it is bound by the matrix cores:
 // 2 n v d operations forward, 6 n v d backward.
 //
+// (The gradient comes with lse and dloss after the forward call, so the logits are
+// computed twice; nothing is kept between the calls.)
+//
 // bf16 tensors run as they are, g in bf16 and divided by the largest |dloss|,
 // by which the sums are multiplied in fp32: where all rows weigh the same (a
 // mean), the target's entry p - 1 then rounds by its p alone, and not every row's
@@ -600,8 +603,9 @@ __global__ __launch_bounds__(256) void join_kernel(int rows, int cols, const int
 
 // Few rows of fp32 in the forward call (up to kFew): no planes, whose making
 // alone would read and write as many bytes as W has.  Plain fp32 multiply-adds,
-// each weight read once; bound by W's bytes and, at eight rows, as much by the
-// multiply-adds (25543 x 2048: 8 rows 110 us, 1.9 TB/s; 9 rows by planes 147).
+// each weight read once; bound by the latency of a wave's loads of W (25543 x 2048:
+// 1 row 70 us, 8 rows 108, 1.9 TB/s; with X read from one place all along 108, with a
+// quarter of the multiply-adds 103; 9 rows by planes 147).
 constexpr int kFew = 8, kFewWaves = 1024;
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -725,6 +729,8 @@ Plan plan(int64_t n, int64_t v, int64_t d, int type, bool grad) {
   p.wexp_at = take(p.planes == 2 && !grad ? p.piece * 4 : 0);
   p.x_at = take(p.planes * n * p.dp * 2);
   p.x2_at = grad && p.planes == 2 ? take(p.planes * n * p.dp * 2) : at;  // by the common power
+  // (of bf16 W only where its rows cannot be read in place, which its stride and alignment
+  // decide: the size function knows neither)
   p.w_at = take(p.planes * p.piece * p.dp * 2);
   p.part_at = grad ? at : take((round_up(v, p.piece) / (p.planes == 2 ? 32 : 64)) * n * 8);
   p.g_at = grad ? take(p.planes * n * p.piece * 2) : at;

@@ -260,10 +260,13 @@ struct Square {
 
 // Epilogue of the symmetric products: out = was a + acc c; each tile below
 // the diagonal is stored to its mirror too (straight from the registers:
-// through LDS, as whole rows, it took 36 us where this takes 33).  Bound by the
-// matrix cores for large matrices (4096 x 11008: A 184 GFLOP and A A 69 in 255 us
-// together, 994 TFLOP/s), by the number of tiles for small ones (777 x 1531 8 us
-// each, 128 x 512 5.5).
+// through LDS, as whole rows, it took 36 us where this takes 33; without the mirror
+// an update of 4096 x 11008 takes 3320 us for 3476, of 12 x 768 x 768 fp32 534 for
+// 571).  Bound by the matrix cores for large matrices (4096 x 11008: A 184 GFLOP and
+// A A 69 in 255 us together, 994 TFLOP/s), by the number of tiles for small ones
+// (777 x 1531 8 us each, 128 x 512 6), in between by both and the epilogue, which
+// nothing overlaps with one block a compute unit (12 of 768 x 768 fp32: 31 us, of which
+// the 24 stages of its 252 tiles are 16).
 template <int P>
 struct SymArgs {
   Square<P> out, was;  // was.p null: acc c alone
@@ -299,9 +302,9 @@ struct Sym {
 };
 
 // Epilogue of X <- a X + B X: out = x a + acc c, the next step's X, or the
-// result in its own type and orientation.  4096 x 11008: 431 us, 857 TFLOP/s, of
+// result in its own type and orientation.  4096 x 11008: 430 us, 859 TFLOP/s, of
 // which X's planes, read and written (360 MB), are 80 us at the rate of a copy;
-// 12 of 768 x 768 fp32 54 us.
+// 12 of 768 x 768 fp32 52 us.
 template <int P>
 struct NextArgs {
   Wide<P> x, out;

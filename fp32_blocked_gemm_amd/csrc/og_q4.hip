@@ -189,9 +189,9 @@ __device__ __forceinline__ void row_piece(const Problem &p, const int64_t (&row)
 
 // Up to 4 rows of A.  Block: 4 waves; KS of them share R weight rows, each
 // taking every KS-th piece of 2048 k (64 lanes x 32).  Bound by the bytes of the
-// codes and, for small layers, by the time of one load after another: 4096 x
-// 4096 by one bf16 row 6.1 us (8.7 MB), 11008 x 4096 11.5 us, by a fp32 row with
-// groups of 32 and zero points 30 MB in 11 us.
+// codes and, for small layers, by the time of one load after another (calls in a
+// graph, weights in turn): 4096 x 4096 by one bf16 row 5.2 us (8.7 MB), 11008 x 4096
+// 8.7, by a fp32 row 10.2.
 template <class T, int M, int R, int KS>
 __global__ __launch_bounds__(256) void row_kernel(Problem p) {
   __shared__ float part[4][M * R];
@@ -317,9 +317,11 @@ struct Chunk {
 // instructions transpose the dwords among the four lane groups so that each of
 // the next four matrix-core instructions (16 x 16 x 32) covers 32 consecutive
 // k, that is, one group of scales, which one lane group has loaded.  The
-// operands of the next 128 k are read ahead.  Bound by the codes' conversion (two
-// operations for two codes, once per 16 or 32 rows of A) and by latency: 16 bf16
-// rows on 4096 x 4096 10.5 us (0.9 TB/s of codes), on 11008 x 4096 24 us, 64 rows 49.
+// operands of the next 128 k are read ahead.  Bound by the latency of those
+// reads: 16 bf16 rows take 10.0 us on 4096 x 4096 (0.9 TB/s of codes), 20.4 on 4096 x
+// 11008 and 22.3 on 11008 x 4096; with the codes not converted 8.8, 18.6 and 19.1, with
+// A read from one place all along (it comes from L2 once per block, four times the
+// codes' bytes) 10.1, 18.9 and 24.0.  64 rows on 11008 x 4096 take 44.
 template <class T, int W, int MT, int NT>
 __global__ __launch_bounds__(W * 64) void block_kernel(Problem p) {
   using Pl = Planes<T>;
@@ -439,7 +441,7 @@ template <class T, int M, int R>
 void run_rows(const Problem &p, hipStream_t s) {
   const int groups = (p.n + R - 1) / R;
   // As many waves share a row as its pieces keep busy (one row of bf16: 1024 x
-  // 8192 by one wave 10.7 us, by four 4.8; 11008 x 2048 7.2 and 10.3).
+  // 8192 by one wave 8.3 us, by four 3.5; 11008 x 2048 6.2 and 8.4).
   const int pieces = (p.k + 2047) / 2048;
   const int ks = pieces >= 4 ? 4 : pieces >= 2 ? 2 : 1;
   const dim3 block(256);
@@ -465,9 +467,9 @@ void run(const Problem &p, hipStream_t s) {
     hipLaunchKernelGGL(short_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, s, p);
     return;
   }
-  // Row kernel and matrix cores, 4096 x 4096, by rows of A: bf16 1 6.1 and 8.6
-  // us, 2 7.4 and 8.8, 4 10.0 and 9.2; fp32 (three products) 1 6.9 and 14.6, 4
-  // 14.0 and 15.4, 5 15.3 there.
+  // Row kernel and matrix cores, 4096 x 4096, by rows of A: bf16 1 5.2 and 7.8
+  // us, 3 7.4 and 8.2, 4 8.7 and 8.3; fp32 (three products) 1 6.1 and 12.3, 4
+  // 12.4 and 12.9, 5 12.9 there.
   constexpr bool wide = sizeof(T) == 4;
   if (p.m == 1) return run_rows<T, 1, 4>(p, s);
   if (p.m == 2) return run_rows<T, 2, 4>(p, s);
@@ -476,9 +478,9 @@ void run(const Problem &p, hipStream_t s) {
     if (p.m == 4) return run_rows<T, 4, 4>(p, s);
   // Two tiles of weight rows a block read A half as often, where that leaves
   // every compute unit a block (one tile and two: 64 bf16 rows of A on 4096 x
-  // 4096 24.0 and 17.9 us, on 11008 x 4096 61.9 and 48.7; 16 on 8192 x 4096 19.2
-  // and 13.9, fp32 29.1 and 23.1; but 16 on 4096 x 4096, 128 blocks, 10.5 and
-  // 13.5); sixteen waves where fp32's planes do not need the registers of eight.
+  // 4096 21.8 and 15.6 us, on 11008 x 4096 56.4 and 44.1; 16 on 8192 x 4096 17.1
+  // and 12.9, fp32 27.2 and 19.6; but 16 on 4096 x 4096, 128 blocks, 9.6 and
+  // 12.5); sixteen waves where fp32's planes do not need the registers of eight.
   const int tall = p.m <= 16 ? 16 : 32;
   const bool many = (int64_t)((p.n + 31) / 32) * ((p.m + tall - 1) / tall) >= 256;
   if (p.m <= 16) return many ? run_blocks<T, 8, 1, 2>(p, s) : run_blocks<T, wide ? 8 : 16, 1, 1>(p, s);
