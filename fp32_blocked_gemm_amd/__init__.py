@@ -11,6 +11,7 @@ the calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -95,6 +96,15 @@ def lib() -> ctypes.CDLL:
     L.og_linear_cross_entropy_grad.restype = ctypes.c_int
     L.og_linear_cross_entropy_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int]
     L.og_linear_cross_entropy_workspace.restype = _i64
+    L.og_grad_norm.argtypes = [_i64, _vp, _vp, _vp, _i64]
+    L.og_grad_norm.restype = ctypes.c_int
+    L.og_clip_grad_norm.argtypes = [_i64, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp, _i64]
+    L.og_clip_grad_norm.restype = ctypes.c_int
+    L.og_grad_norm_workspace.argtypes = []
+    L.og_grad_norm_workspace.restype = _i64
+    L.og_logit_penalties.argtypes = [_i64, _i64, _vp, _i64, ctypes.c_int, _i64, _vp, _i64, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64]
+    L.og_logit_penalties.restype = ctypes.c_int
     L.og_last_error.argtypes = []
     L.og_last_error.restype = ctypes.c_char_p
     L.og_version.argtypes = []
@@ -498,3 +508,130 @@ def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=No
          _ld(W), code, target.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(), *args,
          ws.data_ptr(), ws.numel())
     return tuple(outs)
+
+
+def _run_of(t):
+    """(rows, cols, row stride) of a tensor as runs of elements: one run where its elements
+    follow one another in memory."""
+    if t.is_contiguous() or (t.dim() == 2 and t.t().is_contiguous()):
+        return 1, t.numel(), t.numel()
+    if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
+        return t.shape[0], t.shape[1], t.stride(0)
+    raise ValueError("a gradient must be contiguous, or 2-D with contiguous rows or columns")
+
+
+def _grads(grads, out):
+    """The table of og_grad_norm's tensors, and their device."""
+    torch = _torch()
+    code = _type(grads[0], (F32, BF16, F16))
+    dev = _one_device(grads[0])
+    table = array.array("q")
+    for x, y in zip(grads, grads if out is None else out):
+        code = _TYPES.get(x.dtype)
+        if code is None:
+            _type(x, (F32, BF16, F16))
+        if x.device != dev or y.device != dev:
+            raise ValueError("tensors must be on one device")
+        if y is x or y.stride() == x.stride() or (x.is_contiguous() and y.is_contiguous()):
+            rows, cols, ldx = _run_of(x)
+            ldy = ldx
+        elif x.dim() == 2 and y.dim() == 2:
+            rows, cols, ldx, ldy = *x.shape, _ld(x), _ld(y)
+        else:
+            raise ValueError("an output must have its gradient's layout")
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError("an output must have its gradient's shape and type")
+        table.extend((x.data_ptr(), y.data_ptr(), rows, cols, ldx, ldy, code))
+    return table, dev
+
+
+def grad_norm(grads, workspace=None):
+    """The Euclidean norm over all elements of the tensors `grads` (og_grad_norm), a tensor of
+    one float32.  Types float32, bfloat16 and float16, mixed as they come; contiguous tensors
+    or 2-D ones with contiguous rows or columns."""
+    return _grad_norm(list(grads), None, None, 0.0, workspace)
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, workspace=None):
+    """Scales the tensors `grads` by min(1, max_norm / (norm + eps)), norm the Euclidean norm
+    over all their elements, which is returned as a tensor of one float32
+    (og_clip_grad_norm).  In place, or into the tensors `out`, of the same shapes, types and
+    layouts.  The host does not wait: a norm that is not finite is seen in what is returned."""
+    grads = list(grads)
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("one output for each gradient expected")
+    return _grad_norm(grads, out, float(max_norm), float(eps), workspace)
+
+
+def _grad_norm(grads, out, max_norm, eps, workspace):
+    if not grads:
+        raise ValueError("at least one tensor expected")
+    torch = _torch()
+    L = lib()
+    table, dev = _grads(grads, out)
+    at = table.buffer_info()[0]
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = _workspace(L.og_grad_norm_workspace(), workspace, dev)
+    if max_norm is None:
+        _run(dev, L.og_grad_norm, len(grads), at, norm.data_ptr(), ws.data_ptr(), ws.numel())
+    else:
+        _run(dev, L.og_clip_grad_norm, len(grads), at, max_norm, eps, norm.data_ptr(), ws.data_ptr(),
+             ws.numel())
+    return norm
+
+
+def logit_penalties(logits, tokens=None, lengths=None, prompt_lengths=None, repetition=None,
+                    frequency=None, presence=None, bias=None, mask=None, out=None):
+    """Penalties for the tokens each row holds, a bias and a mask on logits [n, v] of float32,
+    bfloat16 or float16 (og_logit_penalties).
+
+    tokens [n, t] int64, of which row i's first lengths[i] count (int64; None: all), generated
+    from prompt_lengths[i] on (int64; None: all were); repetition, frequency and presence [n]
+    float32; bias [v], [1, v] or [n, v] float32; mask [ceil(v / 32)], [1, .] or [n, .] int32,
+    bit j % 32 of word j // 32 set where token j is allowed.  What is None is left out.
+    out may be logits itself."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("expected 2-D logits")
+    n, v = logits.shape
+    code = _type(logits, (F32, BF16, F16))
+    if out is None:
+        out = torch.empty((n, v), dtype=logits.dtype, device=logits.device)
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and type")
+    given = [logits, out]
+    t = ldt = 0
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != n or tokens.dtype != torch.int64:
+            raise ValueError(f"tokens must be [{n}, t] int64")
+        t, ldt = tokens.shape[1], _ld(tokens)
+        given.append(tokens)
+    elif not (repetition is None and frequency is None and presence is None):
+        raise ValueError("a penalty without tokens")
+    vectors = []
+    for what, x, dtype in (("lengths", lengths, torch.int64), ("prompt_lengths", prompt_lengths, torch.int64),
+                           ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
+                           ("presence", presence, torch.float32)):
+        if x is not None:
+            _vector(x, n, dtype, what)
+            given.append(x)
+        vectors.append(None if x is None else x.data_ptr())
+    rows = []
+    for what, x, dtype, cols in (("bias", bias, torch.float32, v), ("mask", mask, torch.int32, (v + 31) // 32)):
+        if x is None:
+            rows += [None, 0]
+            continue
+        if x.dim() == 1:
+            x = x.unsqueeze(0)
+        if x.dim() != 2 or x.dtype != dtype or x.shape[1] != cols or x.shape[0] not in (1, n):
+            raise ValueError(f"{what} must be {dtype}, [{cols}], [1, {cols}] or [{n}, {cols}]")
+        given.append(x)
+        rows += [x.data_ptr(), 0 if x.shape[0] == 1 else _ld(x)]
+        if x.shape[0] == 1:
+            _ld(x)  # (columns contiguous)
+    dev = _one_device(*given)
+    _run(dev, lib().og_logit_penalties, n, v, logits.data_ptr(), _ld(logits), code, t,
+         None if tokens is None else tokens.data_ptr(), ldt, *vectors, *rows, out.data_ptr(), _ld(out))
+    return out

@@ -415,6 +415,80 @@ og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const vo
  * 1 the gradient's.  Needs no device. */
 int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int type, int grad);
 
+/*
+ * The Euclidean norm over all elements of `count` tensors, as a model's
+ * gradients are: norm = sqrt(sum x^2), the squares of fp32, bf16 or fp16
+ * values exact and added in 64 bits in a fixed order, the norm rounded to fp32
+ * once.  A tensor is rows x cols elements, row i from x + i ldx on (elements of
+ * its type); a single row or ldx == cols is a run of rows * cols elements
+ * whatever its shape was.  `grads` is read on the host, before the call returns.
+ * Requirements: types OG_F32, OG_BF16 or OG_F16; ldx >= cols for more than one
+ * row; x non-null where there are elements; at most 2^20 tensors of 2^40
+ * elements; norm one float; a workspace of og_grad_norm_workspace() bytes.
+ * No tensor, or none with an element: the norm is 0.
+ */
+typedef struct {
+  const void *x;
+  void *y; /* og_clip_grad_norm: the result, x itself (with ldy == ldx) for in place */
+  int64_t rows, cols, ldx, ldy;
+  int64_t type;
+} og_grad;
+og_status og_grad_norm(int64_t count, const og_grad *grads, float *norm, void *workspace,
+                       int64_t workspace_bytes);
+
+/*
+ * The same norm, and the tensors scaled so that all together are no longer
+ * than max_norm:
+ *
+ *     y = x min(1, max_norm / (norm + eps))
+ *
+ * for each tensor, the factor computed in 64 bits and rounded to 24 (of any
+ * size), the product rounded to fp32 and to the tensor's type.  Where the factor is 1, y = x
+ * bit for bit and tensors in place are not written.  A norm that is infinite
+ * makes finite elements 0 and infinite ones NaN, one that is NaN makes all of
+ * them NaN (the caller sees it in `norm`).
+ * Requirements besides: max_norm and eps finite, >= 0; y non-null and ldy >=
+ * cols as for x; no two tensors begin at one y, and no y overlaps another
+ * tensor's x or y.
+ */
+og_status og_clip_grad_norm(int64_t count, const og_grad *grads, float max_norm, float eps, float *norm,
+                            void *workspace, int64_t workspace_bytes);
+/* Bytes of both calls' workspace.  Needs no device. */
+int64_t og_grad_norm_workspace(void);
+
+/*
+ * Penalties, a bias and a mask on logits Z (n x v, row stride ldz), a row per
+ * sequence, before a token is drawn from them.  Row i's tokens are
+ * tokens[i*ldt + p], 0 <= p < lengths[i]; from prompt_lengths[i] on they were
+ * generated, before it they are its prompt.  For token j, z = Z[i*ldz + j]:
+ *
+ *     z = z > 0 ? z / repetition[i] : z * repetition[i]     j among the tokens
+ *     z = z - frequency[i] * c - presence[i]                j c > 0 times generated
+ *     z = z + bias[i*ldb + j]
+ *     z = -infinity                                         mask bit j of row i is 0
+ *     O[i*ldo + j] = z
+ *
+ * each operation rounded to fp32, z rounded to the logits' type once.  The mask bit of j
+ * is bit j % 32 of the word mask[i*ldm + j/32].  Any of lengths (NULL: t each),
+ * prompt_lengths (NULL: 0, all were generated), repetition, frequency,
+ * presence, bias and mask may be NULL: that step is left out.  ldb and ldm may be 0: one
+ * row for all.  Lengths outside [0, t] count as the nearest end, and tokens
+ * outside [0, v) (a padding's) not at all; nothing past a row's length is used.
+ * A row whose mask has no bit set is -infinity throughout; a masked logit
+ * is -infinity whatever it was.
+ * O may be Z itself with the same stride; logits that no step changes are then
+ * not written.  Otherwise O must not overlap an input.
+ * Requirements: type OG_F32, OG_BF16 or OG_F16; n, v, t >= 0; ldz, ldo >=
+ * max(1, v); ldt >= max(1, t); ldb 0 or >= v; ldm 0 or >= ceil(v/32); tokens
+ * non-null where t > 0 and a penalty is given; n <= 2^24, v <= 2^28, t < 2^31
+ * (OG_ERR_TOO_LARGE).  n or v 0: nothing is done.  No workspace.
+ */
+og_status og_logit_penalties(int64_t n, int64_t v, const void *Z, int64_t ldz, int type, int64_t t,
+                             const int64_t *tokens, int64_t ldt, const int64_t *lengths,
+                             const int64_t *prompt_lengths, const float *repetition,
+                             const float *frequency, const float *presence, const float *bias,
+                             int64_t ldb, const uint32_t *mask, int64_t ldm, void *O, int64_t ldo);
+
 /* Description of the calling thread's last error ("" after a success). */
 const char *og_last_error(void);
 

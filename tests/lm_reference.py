@@ -171,3 +171,52 @@ def newton_schulz(g, steps, coeffs, eps):
         x = nxt
     err = err + half_step(g.dtype) * (x.norm() + err)
     return (x.t() if g.shape[0] > g.shape[1] else x), err
+
+
+# -- logit_penalties ---------------------------------------------------------
+
+def logit_penalties(z, tokens, lengths, prompts, repetition, frequency, presence, bias, mask):
+    """(exact, bound), a row and a token at a time on the host.  Each of up to five operations
+    rounds to fp32 (2^-24 of its result, to which the sizes of all terms are a bound; half of
+    the smallest subnormal), the end to the type."""
+    n, v = z.shape
+    x = z.to(F64).cpu()
+    size = torch.zeros_like(x)
+    host = lambda t: None if t is None else t.cpu()  # noqa: E731
+    tokens, lengths, prompts, repetition, frequency, presence, bias, mask = map(
+        host, (tokens, lengths, prompts, repetition, frequency, presence, bias, mask))
+    for i in range(n):
+        seen, made = {}, {}
+        if tokens is not None:
+            t = tokens.shape[1]
+            stop = t if lengths is None else min(max(int(lengths[i]), 0), t)
+            for p, tok in enumerate(tokens[i, :stop].tolist()):
+                if 0 <= tok < v:
+                    seen[tok] = True
+                    if p >= (0 if prompts is None else int(prompts[i])):
+                        made[tok] = made.get(tok, 0) + 1
+        for tok in seen:
+            if repetition is not None:
+                r = float(repetition[i])
+                x[i, tok] = x[i, tok] / r if x[i, tok] > 0 else x[i, tok] * r
+            if tok in made:
+                for by in ([] if frequency is None else [float(frequency[i]) * made[tok]]) + (
+                        [] if presence is None else [float(presence[i])]):
+                    size[i, tok] += x[i, tok].abs() + abs(by)
+                    x[i, tok] -= by
+            size[i, tok] += x[i, tok].abs()
+        if bias is not None:
+            b = bias if bias.dim() == 1 or bias.shape[0] == 1 else bias[i]
+            size[i] += x[i].abs() + b.reshape(-1).abs()
+            x[i] += b.reshape(-1).to(F64)
+        if mask is not None:
+            m = mask if mask.dim() == 1 or mask.shape[0] == 1 else mask[i]
+            words = m.reshape(-1).tolist()
+            for j in range(v):
+                if not words[j // 32] >> (j % 32) & 1:
+                    x[i, j], size[i, j] = float("-inf"), 0
+    over = x.to(z.dtype).isinf()  # (past the type's range)
+    x[over] = x[over].sign() * float("inf")
+    e = size * 2.0 ** -24 * 1.01 + 2.0 ** -148
+    e = e + half_step(z.dtype) * (x.abs() + e) + torch.finfo(z.dtype).smallest_normal * torch.finfo(z.dtype).eps
+    return x, e
