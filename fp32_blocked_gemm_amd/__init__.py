@@ -32,7 +32,12 @@ BF16 = 1
 F16 = 2
 ACT_NONE = 0
 ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
 _ACTS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, ACT_NONE: ACT_NONE, ACT_RELU: ACT_RELU}
+_EPI_ACTS = {**_ACTS, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU,
+             ACT_GELU: ACT_GELU, ACT_GELU_TANH: ACT_GELU_TANH, ACT_SILU: ACT_SILU}
 _MODES = {"exact": EXACT, "fast": FAST, "fast_mfma": FAST_MFMA, EXACT: EXACT, FAST: FAST,
           FAST_MFMA: FAST_MFMA}
 
@@ -96,6 +101,15 @@ def lib() -> ctypes.CDLL:
     L.og_linear_cross_entropy_grad.restype = ctypes.c_int
     L.og_linear_cross_entropy_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int]
     L.og_linear_cross_entropy_workspace.restype = _i64
+    L.og_gemm_nt_epi.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp,
+                                 _i64, _vp, _i64, _vp, _i64, _vp, _i64]
+    L.og_gemm_nt_epi.restype = ctypes.c_int
+    L.og_gemm_nt_epi_grad.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i64,
+                                      ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _vp, _i64]
+    L.og_gemm_nt_epi_grad.restype = ctypes.c_int
+    for f in (L.og_gemm_nt_epi_workspace, L.og_gemm_nt_epi_grad_workspace):
+        f.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+        f.restype = _i64
     L.og_grad_norm.argtypes = [_i64, _vp, _vp, _vp, _i64]
     L.og_grad_norm.restype = ctypes.c_int
     L.og_clip_grad_norm.argtypes = [_i64, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp, _i64]
@@ -507,6 +521,109 @@ def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=No
     _run(dev, lib().og_linear_cross_entropy_grad, n, v, d, X.data_ptr(), _ld(X), W.data_ptr(),
          _ld(W), code, target.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(), *args,
          ws.data_ptr(), ws.numel())
+    return tuple(outs)
+
+
+def _act(act) -> int:
+    if act not in _EPI_ACTS:
+        raise ValueError(f"act must be None, 'relu', 'gelu', 'gelu_tanh' or 'silu', not {act!r}")
+    return _EPI_ACTS[act]
+
+
+def _product_shapes(A, B):
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("expected 2-D A and B")
+    m, k = A.shape
+    n, k2 = B.shape
+    if k != k2:
+        raise ValueError(f"inner sizes differ: {k} vs {k2}")
+    code = _type(A, (F32, BF16, F16))
+    if B.dtype != A.dtype:
+        raise ValueError("A and B must have the same type")
+    return m, n, k, code
+
+
+def _matrix(t, rows, cols, dtype, what):
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or t.dtype != dtype:
+        raise ValueError(f"{what} must be [{rows}, {cols}] of {dtype}")
+
+
+def gemm_nt_epi_workspace(m, n, k, dtype, grad=False) -> int:
+    """Bytes gemm_nt_epi (grad: its gradient) needs, dtype F32, BF16 or F16."""
+    f = lib().og_gemm_nt_epi_grad_workspace if grad else lib().og_gemm_nt_epi_workspace
+    b = int(f(m, n, k, dtype))
+    _check(min(b, 0))
+    return b
+
+
+def gemm_nt_epi(A, B, bias=None, act=None, residual=None, out=None, pre=None, need_pre=False, workspace=None):
+    """C = act(A @ B.T + bias) + residual (og_gemm_nt_epi), B given as n x k.  A [m, k], B, bias
+    [n] and residual [m, n] of one type, float32, bfloat16 or float16; act None, 'relu',
+    'gelu', 'gelu_tanh' or 'silu'.  The residual may be out.  With need_pre (or a tensor pre to
+    hold it) returns (C, A @ B.T + bias), which gemm_nt_epi_grad wants; else C."""
+    torch = _torch()
+    m, n, k, code = _product_shapes(A, B)
+    act = _act(act)
+    if out is None:
+        out = torch.empty((m, n), dtype=A.dtype, device=A.device)
+    if pre is None and need_pre:
+        pre = torch.empty((m, n), dtype=A.dtype, device=A.device)
+    _matrix(out, m, n, A.dtype, "out")
+    given = [A, B, out]
+    if bias is not None:
+        _vector(bias, n, A.dtype, "bias")
+        given.append(bias)
+    extra = []
+    for t, what in ((residual, "residual"), (pre, "pre")):
+        if t is None:
+            extra += [None, 0]
+            continue
+        _matrix(t, m, n, A.dtype, what)
+        given.append(t)
+        extra += [t.data_ptr(), _ld(t)]
+    dev = _one_device(*given)
+    size = lib().og_gemm_nt_epi_workspace(m, n, k, code)
+    ws = None if size == 0 and workspace is None else _workspace(size, workspace, dev)
+    _run(dev, lib().og_gemm_nt_epi, m, n, k, A.data_ptr(), _ld(A), B.data_ptr(), _ld(B), code,
+         None if bias is None else bias.data_ptr(), act, *extra, out.data_ptr(), _ld(out),
+         *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())))
+    return out if pre is None else (out, pre)
+
+
+def gemm_nt_epi_grad(dC, A, B, pre=None, act=None, need=(True, True, True), dA=None, dB=None, dbias=None,
+                     workspace=None):
+    """(dA, dB, dbias) of gemm_nt_epi for dC [m, n], from the `pre` it returned (not read where
+    act is None); the residual's gradient is dC (og_gemm_nt_epi_grad).  need: which of the
+    three are wanted; the others are None."""
+    torch = _torch()
+    m, n, k, code = _product_shapes(A, B)
+    act = _act(act)
+    _matrix(dC, m, n, A.dtype, "dC")
+    if act != ACT_NONE:
+        if pre is None:
+            raise ValueError("the gradient of an activation needs pre")
+        _matrix(pre, m, n, A.dtype, "pre")
+    elif pre is not None:
+        pre = None
+    outs = []
+    for t, shape, wanted, what in ((dA, (m, k), need[0], "dA"), (dB, (n, k), need[1], "dB"),
+                                   (dbias, (n,), need[2], "dbias")):
+        if not wanted:
+            outs.append(None)
+            continue
+        if t is None:
+            t = torch.empty(shape, dtype=A.dtype, device=A.device)
+        if len(shape) == 1:
+            _vector(t, n, A.dtype, what)
+        else:
+            _matrix(t, *shape, A.dtype, what)
+        outs.append(t)
+    dev = _one_device(dC, A, B, *([] if pre is None else [pre]), *[t for t in outs if t is not None])
+    args = [p for t in outs[:2] for p in ((None, 0) if t is None else (t.data_ptr(), _ld(t)))]
+    ws = _workspace(lib().og_gemm_nt_epi_grad_workspace(m, n, k, code), workspace, dev)
+    _run(dev, lib().og_gemm_nt_epi_grad, m, n, k, dC.data_ptr(), _ld(dC), A.data_ptr(), _ld(A), B.data_ptr(),
+         _ld(B), code, None if pre is None else pre.data_ptr(), 0 if pre is None else _ld(pre), act, *args,
+         None if outs[2] is None else outs[2].data_ptr(), ws.data_ptr(), ws.numel())
     return tuple(outs)
 
 

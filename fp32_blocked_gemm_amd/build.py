@@ -20,10 +20,10 @@ OBJDIR = os.path.join(HERE, "_build")
 API = os.path.join(CSRC, "og_api.hip")
 UNITS = os.path.join(CSRC, "og_units.hip")
 N_UNITS = 17  # kernel groups of og_units.hip, compiled in parallel
-OPERATORS = [os.path.join(CSRC, f) for f in ("og_clip.hip", "og_lce.hip", "og_logits.hip", "og_ns.hip",
-                                                  "og_q4.hip")]  # one object each
+OPERATORS = [os.path.join(CSRC, f) for f in ("og_clip.hip", "og_epi.hip", "og_epi_grad.hip", "og_lce.hip",
+                                                  "og_logits.hip", "og_ns.hip", "og_q4.hip")]  # one object each
 SOURCES = [API, UNITS, *OPERATORS]
-HEADERS = [os.path.join(CSRC, f) for f in ("og_host.hpp", "og_kernels.hpp", "og_launch.hpp",
+HEADERS = [os.path.join(CSRC, f) for f in ("og_epi.hpp", "og_host.hpp", "og_kernels.hpp", "og_launch.hpp",
                                            "og_tile.hpp")] + [os.path.join(INCLUDE, "og.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,331 @@
+// og_epi.hpp -- what og_gemm_nt_epi and its gradient share: the activations
+// with their derivatives, the operands of the tile product (og_tile.hpp) and
+// its epilogue, and products whose k is split.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <limits>
+#include <type_traits>
+
+#include "og.h"
+#include "og_host.hpp"
+#include "og_tile.hpp"
+
+namespace og::epi {
+
+using namespace og::tile;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The logistic function s of x, and 1 - s, neither by a difference of near values.
+__device__ __forceinline__ void logistic(float x, float &s, float &rest) {
+  const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e), one = 1.0f / (1.0f + e), other = e * one;
+  s = x >= 0 ? one : other;
+  rest = x >= 0 ? other : one;
+}
+
+// Phi(x), the normal distribution, accurate in its tail too.
+__device__ __forceinline__ float normal(float x) { return 0.5f * erfcf(-0.70710678118654752f * x); }
+
+constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kCube = 0.044715f;
+
+// act(x).  Far to the left, where the value is 0 in fp32, x times 0 would make an infinity NaN.
+__device__ __forceinline__ float act_of(float x, int act) {
+  float s, rest;
+  switch (act) {
+    case OG_ACT_RELU: return x > 0 ? x : x == x ? 0.0f : x;
+    case OG_ACT_GELU: return x < -20 ? -0.0f : x * normal(x);
+    case OG_ACT_GELU_TANH:
+      logistic(kTanh * x * (1.0f + kCube * x * x), s, rest);
+      return x < -20 ? -0.0f : x * s;
+    case OG_ACT_SILU: logistic(x, s, rest); return x < -120 ? -0.0f : x * s;
+    default: return x;
+  }
+}
+
+// act'(x); 0 and 1 far to the left and the right.
+__device__ __forceinline__ float slope_of(float x, int act) {
+  float s, rest;
+  switch (act) {
+    case OG_ACT_RELU: return x > 0 ? 1.0f : x == x ? 0.0f : x;
+    case OG_ACT_GELU:
+      if (fabsf(x) > 20) return x > 0 ? 1.0f : 0.0f;
+      return normal(x) + x * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * x * x);
+    case OG_ACT_GELU_TANH:
+      if (fabsf(x) > 20) return x > 0 ? 1.0f : 0.0f;
+      logistic(kTanh * x * (1.0f + kCube * x * x), s, rest);
+      return s + x * s * rest * kTanh * (1.0f + 3.0f * kCube * x * x);
+    case OG_ACT_SILU:
+      if (fabsf(x) > 120) return x > 0 ? 1.0f : 0.0f;
+      logistic(x, s, rest);
+      return s + s * x * rest;
+    default: return 1.0f;
+  }
+}
+
+inline bool valid_act(int act) { return act >= OG_ACT_NONE && act <= OG_ACT_SILU; }
+
+// Elements of the matrix cores: 16-bit types as given, fp32 as two fp16 planes.
+template <class T>
+using Element = std::conditional_t<std::is_same_v<T, float>, _Float16, T>;
+template <class T>
+constexpr int kPlanes = sizeof(T) == 4 ? 2 : 1;
+
+// Whether four values of a row are one aligned access.
+template <class T>
+int whole(const T *p, int64_t ld) {
+  return ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
+}
+
+template <class T>
+__device__ __forceinline__ f32x4 load4(const T *p, int left, bool vec) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  f32x4 v = {0, 0, 0, 0};
+  if (vec && left >= 4) {
+    const T4 h = *reinterpret_cast<const T4 *>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) v[e] = (float)p[e];
+  }
+  return v;
+}
+template <class T>
+__device__ __forceinline__ void store4(T *to, const f32x4 v, int left, bool vec) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  T4 h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = (T)v[e];
+  if (vec && left >= 4) {
+    *reinterpret_cast<T4 *>(to) = h;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) to[e] = h[e];
+  }
+}
+
+// The power of two, as an exponent, by which a row or column of fp32 is held in planes: it
+// brings its largest finite magnitude `top` to [2^13, 2^14).
+__device__ __forceinline__ int power_of(float top) {
+  return top > 0 ? 14 - (int)__builtin_amdgcn_frexp_expf(top) : 0;
+}
+
+// Four columns' planes, times 2^e.
+__device__ __forceinline__ void store_planes(uint16_t *out, int c, f32x4 v, const int (&e)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = __builtin_ldexpf(v[q], e[q]);
+  f16x4 h, l;
+  split4(v, h, l);
+  *reinterpret_cast<f16x4 *>(out + column<2>(c, 0)) = h;
+  *reinterpret_cast<f16x4 *>(out + column<2>(c, 1)) = l;
+}
+
+// What becomes of a finished sum at (m, n):
+//   v = sum 2^(up - the powers of its row and column) + bias[n];  P = v;  C = act(v) + residual
+// (out is C of a forward product, dA or dW of the gradient's).
+struct Finish {
+  const float *mtop, *ntop;  // fp32: the largest magnitudes that give the powers; else null
+  int up;
+  const void *bias;
+  int act;
+  const void *residual;
+  int64_t ldr;
+  void *pre;
+  int64_t ldp;
+  void *out;
+  int64_t ldo;
+  int vec_b, vec_r, vec_p, vec_o;  // four values are one access
+};
+
+// Four neighbouring sums of row m from column n on, `left` of them inside.
+template <class T>
+__device__ __forceinline__ void finish(const Finish &f, int64_t m, int n, int left, f32x4 v, int mpower) {
+  if constexpr (kPlanes<T> == 2) {
+    if (f.mtop) {
+      const f32x4 top = load4(f.ntop + n, left, true);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], -mpower - power_of(top[e]));
+    }
+  } else {
+    if (f.up) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], f.up);
+    }
+  }
+  if (f.bias) {
+    const f32x4 b = load4(static_cast<const T *>(f.bias) + n, left, f.vec_b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += b[e];
+  }
+  if (f.pre) store4(static_cast<T *>(f.pre) + m * f.ldp + n, v, left, f.vec_p);
+  if (f.act != OG_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = act_of(v[e], f.act);
+  }
+  if (f.residual) {
+    const f32x4 r = load4(static_cast<const T *>(f.residual) + m * f.ldr + n, left, f.vec_r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += r[e];
+  }
+  store4(static_cast<T *>(f.out) + m * f.ldo + n, v, left, f.vec_o);
+}
+
+// The tile product's epilogue: finished, or (a product whose k is split) the part's sums.
+struct StoreArgs {
+  Finish f;
+  float *part;     // null: not split
+  int64_t ld, step;  // of a row of a part, and from one part to the next
+};
+template <class T>
+struct Store {
+  using Args = StoreArgs;
+  static constexpr bool kSymmetric = false;
+  template <class S>
+  static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t, const Args &e) {
+    const int nc = t.n0 + 4 * (t.lane >> 4);
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int m = t.m0 + 16 * i + (t.lane & 15);
+      if (m >= t.M) continue;
+      const int mpower = kPlanes<T> == 2 && e.f.mtop ? power_of(e.f.mtop[m]) : 0;
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const int n = nc + 16 * j;
+        if (n >= t.N) continue;
+        if (e.part) *reinterpret_cast<f32x4 *>(e.part + t.batch * e.step + m * e.ld + n) = acc[i][j];
+        else finish<T>(e.f, m, n, t.N - n, acc[i][j], mpower);
+      }
+    }
+  }
+};
+
+// Adds the parts of a split product in order and finishes.
+template <class T>
+static __global__ __launch_bounds__(256) void join_kernel(int M, int N, int parts, const float *part, int64_t ld,
+                                                   int64_t step, Finish f) {
+  const int per = (N + 3) / 4;
+  const int64_t total = (int64_t)M * per;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+    const int m = (int)(at / per), n = (int)(at - (int64_t)m * per) * 4;
+    f32x4 v = {0, 0, 0, 0};
+    for (int p = 0; p < parts; ++p) {
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(part + p * step + m * ld + n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += w[e];
+    }
+    finish<T>(f, m, n, N - n, v, kPlanes<T> == 2 && f.mtop ? power_of(f.mtop[m]) : 0);
+  }
+}
+
+// Parts of k: as many as take the least time by the tiles' measured stages, where the parts'
+// sums cost a launch and their bytes, written and read.
+constexpr int kMostParts = 16;
+template <class T, bool TT>
+int parts_of(int64_t M, int64_t N, int64_t K) {
+  using C = typename Tiles<Element<T>, kPlanes<T>, TT>::type;
+  double best = std::numeric_limits<double>::infinity();
+  int parts = 1;
+  for (int p = 1; p <= kMostParts && (p == 1 || K / p >= 256); p += p < 4 ? 1 : p) {
+    Args g{};
+    g.M = (int)M;
+    g.N = (int)N;
+    g.K = (int)K;
+    g.k_split = p > 1 ? (int)round_up((K + p - 1) / p, 64) : 0;
+    const double t = least(C(), false, g, p) + (p > 1 ? 4000 + 8.0 * p * M * N / 4000 : 0);
+    if (t < best) best = t, parts = p;
+  }
+  return parts;
+}
+
+// Bytes of a product's parts.
+template <class T, bool TT>
+int64_t parts_bytes(int64_t M, int64_t N, int64_t K) {
+  const int p = parts_of<T, TT>(M, N, K);
+  return p > 1 ? p * M * round_up(N, 4) * 4 : 0;
+}
+
+template <class T, bool TA, bool TB>
+void run_product(Args g, const Finish &f, char *ws, hipStream_t s) {
+  using E = Element<T>;
+  const int parts = parts_of<T, TA && TB>(g.M, g.N, g.K);
+  if (parts == 1) {
+    product<E, kPlanes<T>, TA, TB, Store<T>>(g, StoreArgs{f, nullptr, 0, 0}, 1, s);
+    return;
+  }
+  float *part = reinterpret_cast<float *>(ws);
+  const int64_t ld = round_up(g.N, 4), step = g.M * ld;
+  g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
+  product<E, kPlanes<T>, TA, TB, Store<T>>(g, StoreArgs{f, part, ld, step}, parts, s);
+  const int64_t quads = g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, s,
+                     g.M, g.N, parts, part, ld, step, f);
+}
+
+// Whether the tile product can read a 16-bit matrix where it lies.
+inline bool readable(const void *p, int64_t cols, int64_t ld) {
+  return cols % 8 == 0 && ld % 8 == 0 && ld <= (1 << 22) && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// Places in a workspace.
+struct Room {
+  int64_t at = 0;
+  int64_t take(int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  }
+};
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// Rows of 16-bit values, zero from cols to ld (a multiple of 8).
+static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int64_t ldx, int rows, int cols, uint16_t *out,
+                                                   int ld) {
+  const int per = ld / 8;
+  const int64_t total = (int64_t)rows * per;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+    const int64_t i = at / per;
+    const int c = (int)(at - i * per) * 8;
+    s16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? (short)x[i * ldx + c + e] : (short)0;
+    *reinterpret_cast<s16x8 *>(out + i * ld + c) = v;
+  }
+}
+
+// A 16-bit matrix as an operand.
+inline Operand operand16(const void *x, int64_t ld, int64_t rows, int64_t cols, int64_t padded, char *ws, hipStream_t s) {
+  if (rows == 0 || cols == 0 || readable(x, cols, ld)) return Operand{static_cast<const uint16_t *>(x), ld, 0};
+  uint16_t *to = reinterpret_cast<uint16_t *>(ws);
+  const int64_t granules = rows * (padded / 8);
+  hipLaunchKernelGGL(copy_kernel, dim3((unsigned)std::min<int64_t>((granules + 255) / 256, 8192)), dim3(256), 0, s,
+                     static_cast<const uint16_t *>(x), ld, (int)rows, (int)cols, to, (int)padded);
+  return Operand{to, padded, 0};
+}
+
+inline og_status check_sizes(int64_t m, int64_t n, int64_t k, int type) {
+  using og::host::fail;
+  if (type < OG_F32 || type > OG_F16)
+    return fail(OG_ERR_INVALID_ARG, "type %d: OG_F32, OG_BF16 or OG_F16", type);
+  if (m < 0 || n < 0 || k < 0)
+    return fail(OG_ERR_INVALID_ARG, "negative size: m %lld, n %lld, k %lld", (long long)m, (long long)n, (long long)k);
+  if (m > (1 << 24) || n > (1 << 20) || k > (1 << 20))
+    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld or k %lld: at most 2^24, 2^20 and 2^20", (long long)m, (long long)n,
+                (long long)k);
+  if (m * n > (int64_t(1) << 36) || m * k > (int64_t(1) << 36) || n * k > (int64_t(1) << 36))
+    return fail(OG_ERR_TOO_LARGE, "m %lld, n %lld, k %lld: at most 2^36 elements a matrix", (long long)m, (long long)n,
+                (long long)k);
+  return OG_OK;
+}
+
+}  // namespace og::epi

@@ -1,0 +1,332 @@
+// og_epi_grad.hip -- the gradient of og_gemm_nt_epi:
+//
+//   dP = dC act'(P);  dA = dP W;  dW = dP^T A;  dbias = sum over the rows of dP
+//
+// One sweep over dC and P forms dP and its column sums; two tile products
+// (og_tile.hpp) do the rest, with W and A as operands whose rows run along k
+// (the transposing reads).
+//
+// 16-bit types: dP is rounded to the type once (where an activation changes it;
+// else dC is read where it lies), the sums dbias from it before that.  fp16
+// holds half of dP where the slope may pass 1, so that none that dC holds
+// overflows.
+//
+// fp32: two fp16 planes.  A product's powers of two belong to the indices that
+// it does not sum over, so that every row and column of a gradient keeps the bits
+// of its own size: dA takes dP by rows and W by columns, dW takes dP and A by
+// columns.  A first sweep finds all largest magnitudes (by atomic maxima, whose
+// order does not matter), a second lays out the planes.
+#include "og_epi.hpp"
+
+namespace og::epi::grad {
+
+constexpr int kRows = 64, kCols = 256;  // of a block of a sweep: 4 waves, 4 columns a lane
+
+struct Matrix {
+  const void *x;
+  int64_t ldx;
+  const void *pre;   // null: x itself
+  int64_t ldp;
+  int act;
+  int rows, cols, width;  // width: padded columns of the outputs
+  int vec_x, vec_p;
+  int halve;              // fp16: the output is half the value
+  uint16_t *out;          // 16-bit types: the values (null: not wanted); fp32: planes by the row's power
+  uint16_t *out_c;        // fp32: planes by the column's power
+  float *rtop, *ctop;     // fp32: largest magnitudes (null: not wanted)
+  float *sums;            // column sums of the block's rows, [row block][width] (null: not wanted)
+  int blocks;             // of a launch
+};
+
+template <class T>
+__device__ __forceinline__ f32x4 value(const Matrix &a, int64_t i, int c) {
+  const int left = a.cols - c;
+  f32x4 v = load4(static_cast<const T *>(a.x) + i * a.ldx + c, left, a.vec_x);
+  if (a.pre) {
+    const f32x4 p = load4(static_cast<const T *>(a.pre) + i * a.ldp + c, left, a.vec_p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < left ? v[e] * slope_of(p[e], a.act) : 0.0f;
+  }
+  return v;
+}
+
+// One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
+// and largest magnitudes.
+template <class T, bool LAYOUT>
+__global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
+  __shared__ f32x4 of_waves[2][4][64];
+  int block = blockIdx.x;
+  const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
+  block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
+  const int across = (a.width + kCols - 1) / kCols, rb = block / across;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (block - rb * across) * kCols + 4 * lane, i0 = rb * kRows;
+  if constexpr (LAYOUT) {
+    if (c >= a.width) return;
+    int cpower[4] = {0, 0, 0, 0};
+    if (a.out_c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
+    }
+    for (int r = wave; r < kRows; r += 4) {
+      const int64_t i = i0 + r;
+      if (i >= a.rows) break;
+      const f32x4 v = value<T>(a, i, c);
+      if (a.out) {
+        const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
+        store_planes(a.out + i * a.width * 2, c, v, powers);
+      }
+      if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v, cpower);
+    }
+  } else {
+    f32x4 sum = {0, 0, 0, 0}, top = {0, 0, 0, 0};
+    for (int r = wave; r < kRows; r += 4) {
+      const int64_t i = i0 + r;
+      if (i >= a.rows) break;
+      const f32x4 v = c < a.width ? value<T>(a, i, c) : f32x4{0, 0, 0, 0};
+      f32x4 size;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum[e] += v[e];
+        size[e] = __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f;
+        top[e] = fmaxf(top[e], size[e]);
+      }
+      if constexpr (kPlanes<T> == 2) {
+        if (a.rtop) {
+          const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
+          if (lane == 0 && most > 0) atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
+        }
+      } else if (a.out && c < a.width) {
+        f32x4 h = v;
+        if (a.halve) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] *= 0.5f;
+        }
+        store4(reinterpret_cast<T *>(a.out) + i * a.width + c, h, a.width - c, true);
+      }
+    }
+    if (!a.sums && !a.ctop) return;
+    of_waves[0][wave][lane] = sum;
+    of_waves[1][wave][lane] = top;
+    __syncthreads();
+    if (wave || c >= a.width) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum[e] += of_waves[0][w][lane][e];
+        top[e] = fmaxf(top[e], of_waves[1][w][lane][e]);
+      }
+    if (a.sums) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c) = sum;
+    if (a.ctop) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float most = top[e];  // (a bit cast of a vector's element takes the first one's bits)
+        if (c + e < a.cols && most > 0)
+          atomicMax(reinterpret_cast<uint32_t *>(a.ctop + c + e), __builtin_bit_cast(uint32_t, most));
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(float *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+// dbias from the row blocks' sums: 64 columns a block, 16 threads each, in a fixed order in 64 bits.
+template <class T>
+__global__ __launch_bounds__(1024) void bias_kernel(const float *sums, int blocks, int cols, int width, T *out) {
+  __shared__ double of[16][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  double sum = 0;
+  if (c < cols)
+    for (int b = w; b < blocks; b += 16) sum += (double)sums[(int64_t)b * width + c];
+  of[w][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (w || c >= cols) return;
+  for (int k = 1; k < 16; ++k) sum += of[k][threadIdx.x];
+  out[c] = (T)(float)sum;
+}
+
+struct Call {
+  int64_t m, n, k;
+  const void *dc, *a, *w, *pre;
+  int64_t lddc, lda, ldw, ldp;
+  int act;
+  void *da, *dw, *dbias;
+  int64_t ldda, lddw;
+  char *ws;
+};
+
+struct Plan {
+  int64_t np, kp;
+  int64_t tops_at, p_at, pc_at, a_at, w_at, sums_at, parts_at, total;
+};
+
+template <class T>
+Plan plan(int64_t m, int64_t n, int64_t k) {
+  Plan p;
+  Room r;
+  constexpr int P = kPlanes<T>;
+  p.np = round_up(n, P == 2 ? 32 : 8);
+  p.kp = round_up(k, P == 2 ? 32 : 8);
+  p.tops_at = r.take(P == 2 ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
+  p.p_at = r.take(P * m * p.np * 2);
+  p.pc_at = r.take(P == 2 ? P * m * p.np * 2 : 0);
+  p.a_at = r.take(P * m * p.kp * 2);
+  p.w_at = r.take(P * n * p.kp * 2);
+  p.sums_at = r.take((m + kRows - 1) / kRows * p.np * 4);
+  p.parts_at = r.take(std::max(parts_bytes<T, false>(m, k, n), parts_bytes<T, true>(n, k, m)));
+  p.total = r.at;
+  return p;
+}
+Plan plan_of(int64_t m, int64_t n, int64_t k, int type) {
+  return type == OG_F32 ? plan<float>(m, n, k) : type == OG_BF16 ? plan<__bf16>(m, n, k) : plan<_Float16>(m, n, k);
+}
+
+int sweep_blocks(const Matrix &a) {
+  return (int)((int64_t)((a.rows + kRows - 1) / kRows) * ((a.width + kCols - 1) / kCols));
+}
+
+Finish output(void *out, int64_t ld, int vec, const float *mtop, const float *ntop, int up) {
+  return Finish{mtop, ntop, up, nullptr, OG_ACT_NONE, nullptr, 0, nullptr, 0, out, ld, 0, 0, 0, vec};
+}
+
+template <class T>
+void gradient(const Call &c, const Plan &p, hipStream_t s) {
+  constexpr int P = kPlanes<T>;
+  const int m = (int)c.m, n = (int)c.n, k = (int)c.k;
+  auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
+  const bool same = c.act == OG_ACT_NONE;
+  Matrix dp{};
+  dp.x = c.dc;
+  dp.ldx = c.lddc;
+  dp.pre = same ? nullptr : c.pre;
+  dp.ldp = c.ldp;
+  dp.act = c.act;
+  dp.rows = m;
+  dp.cols = n;
+  dp.width = (int)p.np;
+  dp.vec_x = whole(static_cast<const T *>(c.dc), c.lddc);
+  dp.vec_p = whole(static_cast<const T *>(c.pre), c.ldp);
+  dp.sums = c.dbias ? reinterpret_cast<float *>(c.ws + p.sums_at) : nullptr;
+  Operand rows, cols, A, W;  // dP by rows and by columns, A, W
+  const float *rtop = nullptr, *ctop = nullptr, *atop = nullptr, *wtop = nullptr;
+  int up = 0;
+  if constexpr (P == 2) {
+    float *tops = reinterpret_cast<float *>(c.ws + p.tops_at);
+    float *r = tops, *t = r + round_up(m, 64), *ta = t + round_up(n, 64), *tw = ta + round_up(k, 64);
+    const int64_t total = tw + round_up(k, 64) - tops;
+    auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
+      Matrix a{};
+      a.x = x;
+      a.ldx = ld;
+      a.rows = (int)count;
+      a.cols = k;
+      a.width = (int)p.kp;
+      a.vec_x = whole(static_cast<const T *>(x), ld);
+      a.ctop = top;
+      a.out_c = out;
+      return a;
+    };
+    Matrix ma{}, mw{};
+    if (c.da) {
+      dp.rtop = r;
+      dp.out = at(p.p_at);
+      mw = of(c.w, c.ldw, n, tw, at(p.w_at));
+    }
+    if (c.dw) {
+      dp.ctop = t;
+      dp.out_c = at(p.pc_at);
+      ma = of(c.a, c.lda, m, ta, at(p.a_at));
+    }
+    for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks(*x);
+    const int blocks = dp.blocks + ma.blocks + mw.blocks;
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
+                       tops, total);
+    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(256), 0, s, dp, ma, mw);
+    if (blocks > 0 && (c.da || c.dw))
+      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(256), 0, s, dp, ma, mw);
+    rows = Operand{at(p.p_at), 2 * p.np, 0};
+    cols = Operand{at(p.pc_at), 2 * p.np, 0};
+    A = Operand{at(p.a_at), 2 * p.kp, 0};
+    W = Operand{at(p.w_at), 2 * p.kp, 0};
+    rtop = r, ctop = t, atop = ta, wtop = tw;
+  } else {
+    const bool place = same && readable(c.dc, n, c.lddc);
+    if constexpr (std::is_same_v<T, _Float16>) dp.halve = c.act > OG_ACT_RELU;
+    up = dp.halve;
+    dp.out = place || !(c.da || c.dw) ? nullptr : at(p.p_at);
+    if (dp.out || dp.sums) {
+      dp.blocks = sweep_blocks(dp);
+      if (dp.blocks > 0)
+        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(256), 0, s, dp, Matrix{}, Matrix{});
+    }
+    rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
+    if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s);
+    if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
+  }
+  if (c.dbias)
+    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + kRows - 1) / kRows, n,
+                       dp.width, static_cast<T *>(c.dbias));
+  Args g{};
+  if (c.da && m > 0 && k > 0) {
+    g.a = rows, g.b = W, g.M = m, g.N = k, g.K = n;
+    run_product<T, false, true>(
+        g, output(c.da, c.ldda, whole(static_cast<T *>(c.da), c.ldda), rtop, wtop, up), c.ws + p.parts_at, s);
+  }
+  if (c.dw && n > 0 && k > 0) {
+    g.a = cols, g.b = A, g.M = n, g.N = k, g.K = m;
+    run_product<T, true, true>(
+        g, output(c.dw, c.lddw, whole(static_cast<T *>(c.dw), c.lddw), ctop, atop, up), c.ws + p.parts_at, s);
+  }
+}
+
+}  // namespace og::epi::grad
+
+extern "C" {
+
+int64_t og_gemm_nt_epi_grad_workspace(int64_t m, int64_t n, int64_t k, int type) {
+  const og_status st = og::epi::check_sizes(m, n, k, type);
+  if (st != OG_OK) return st;
+  og::host::ok();
+  return og::epi::grad::plan_of(m, n, k, type).total;
+}
+
+og_status og_gemm_nt_epi_grad(int64_t m, int64_t n, int64_t k, const void *dC, int64_t lddc, const void *A,
+                              int64_t lda, const void *W, int64_t ldw, int type, const void *P, int64_t ldp, int act,
+                              void *dA, int64_t ldda, void *dW, int64_t lddw, void *dbias, void *workspace,
+                              int64_t workspace_bytes) {
+  using namespace og::host;
+  using namespace og::epi;
+  using namespace og::epi::grad;
+  og_status st = check_sizes(m, n, k, type);
+  if (st != OG_OK) return st;
+  if (!valid_act(act)) return fail(OG_ERR_INVALID_ARG, "act %d: OG_ACT_NONE to OG_ACT_SILU", act);
+  const int64_t least_k = std::max<int64_t>(1, k), least_n = std::max<int64_t>(1, n);
+  if (lddc < least_n || (act != OG_ACT_NONE && ldp < least_n) || (dW && lda < least_k) || (dA && ldw < least_k) ||
+      (dA && ldda < least_k) || (dW && lddw < least_k))
+    return fail(OG_ERR_INVALID_ARG, "a row stride is below its row: lddc %lld, ldp %lld, lda %lld, ldw %lld, ldda "
+                "%lld, lddw %lld", (long long)lddc, (long long)ldp, (long long)lda, (long long)ldw, (long long)ldda,
+                (long long)lddw);
+  // what there is to write
+  const bool da = dA && m > 0 && k > 0, dw = dW && n > 0 && k > 0, db = dbias && n > 0;
+  if (!da && !dw && !db) return ok();
+  if (m > 0 && n > 0 && (!dC || (act != OG_ACT_NONE && !P) || (dw && !A) || (da && !W)))
+    return fail(OG_ERR_INVALID_ARG, "dC, P, A or W is null");
+  const Plan p = plan_of(m, n, k, type);
+  if (p.total > 0 && (!workspace || workspace_bytes < p.total))
+    return fail(OG_ERR_INVALID_ARG, "workspace of %lld bytes: %lld needed",
+                (long long)(workspace ? workspace_bytes : 0), (long long)p.total);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(OG_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if ((st = check_device()) != OG_OK) return st;
+  const Call c{m, n, k, dC, A, W, P, lddc, lda, ldw, ldp, act, da ? dA : nullptr, dw ? dW : nullptr,
+               db ? dbias : nullptr, ldda, lddw, static_cast<char *>(workspace)};
+  if (type == OG_F32) gradient<float>(c, p, current_stream());
+  else if (type == OG_BF16) gradient<__bf16>(c, p, current_stream());
+  else gradient<_Float16>(c, p, current_stream());
+  return check_launch("gemm_nt_epi_grad");
+}
+
+}  // extern "C"

@@ -79,6 +79,10 @@ typedef int og_status;
 
 #define OG_ACT_NONE 0 /* og_conv2d_f32_epi: no activation                                 */
 #define OG_ACT_RELU 1 /* og_conv2d_f32_epi: v > 0 ? v : +0 (a NaN stays NaN)              */
+/* og_gemm_nt_epi takes the two above and: */
+#define OG_ACT_GELU 2      /* v Phi(v), Phi the normal distribution                         */
+#define OG_ACT_GELU_TANH 3 /* v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3)))               */
+#define OG_ACT_SILU 4      /* v / (1 + exp(-v))                                             */
 
 /*
  * Matrix product, row-major ("Matrix product and convolution kernels",
@@ -414,6 +418,60 @@ og_status og_linear_cross_entropy_grad(int64_t n, int64_t v, int64_t d, const vo
 /* Bytes of the workspace, or a negative og_status; grad: 0 the forward call's,
  * 1 the gradient's.  Needs no device. */
 int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int type, int grad);
+
+/*
+ * og_gemm_nt_f32's product with an epilogue, of fp32, bf16 or fp16 tensors, all
+ * of one `type`:
+ *
+ *     v = sum over p of A[i*lda + p] * W[j*ldw + p] + bias[j]     (bias NULL: + 0)
+ *     P[i*ldp + j] = v                                            (P NULL: not stored)
+ *     C[i*ldc + j] = act(v) + residual[i*ldr + j]                 (residual NULL: + 0)
+ *
+ * act is OG_ACT_NONE to OG_ACT_SILU; it takes the fp32 v, not the rounded P, which
+ * is there for og_gemm_nt_epi_grad.  P and C are rounded to the type once.
+ * 16-bit tensors are multiplied as they are; of fp32 ones each row of A and W is
+ * held as two fp16 planes times a power of two of its own: 22 bits of each
+ * value, down to 2^-38 of the row's largest.  An fp32 row
+ * that holds an infinity or NaN makes the sums it enters NaN; 16-bit ones follow the
+ * formula.  act of -infinity is -0 (OG_ACT_NONE: itself; OG_ACT_RELU: +0), of NaN NaN.
+ * The residual may be C itself with the same stride; P must not be C, and neither may
+ * overlap an input otherwise.  The gaps of P and C are not written.
+ * Requirements: m, n, k >= 0; lda, ldw >= max(1, k); ldc (and ldr, ldp where given)
+ * >= max(1, n); A, W, C non-null as in og_gemm_nt_f32; a workspace of
+ * og_gemm_nt_epi_workspace(m, n, k, type) bytes (0: none).  m or n 0: nothing is
+ * done; k == 0: v is the bias.  OG_ERR_TOO_LARGE when m exceeds 2^24, n or k 2^20 or a
+ * matrix has more than 2^36 elements.
+ */
+og_status og_gemm_nt_epi(int64_t m, int64_t n, int64_t k, const void *A, int64_t lda, const void *W,
+                         int64_t ldw, int type, const void *bias, int act, const void *residual,
+                         int64_t ldr, void *P, int64_t ldp, void *C, int64_t ldc, void *workspace,
+                         int64_t workspace_bytes);
+/* Bytes of its workspace, or a negative og_status.  Needs no device. */
+int64_t og_gemm_nt_epi_workspace(int64_t m, int64_t n, int64_t k, int type);
+
+/*
+ * Its gradient for dC (m x n, row stride lddc), from the P that the forward call
+ * stored (OG_ACT_NONE: not read, may be NULL):
+ *
+ *     dP_ij = dC_ij act'(P_ij)         (the gradient of the residual is dC)
+ *     dA = dP W  (m x k, ldda),   dW = dP^T A  (n x k, lddw),   dbias_j = sum over i of dP_ij
+ *
+ * of `type` all, overwritten; each may be NULL (not wanted).  The slope of OG_ACT_RELU
+ * is 1 where P > 0, else 0; of a NaN it is NaN.  16-bit types: dP is rounded to
+ * the type for dA and dW, not for dbias.  fp32: each row of dP and column of W (for
+ * dA), each column of dP and of A (for dW) is held as two fp16 planes by a power
+ * of two of its own, as above.  dbias is summed in fp32 by 64 rows and in 64 bits
+ * over those.
+ * Requirements as above, with a workspace of og_gemm_nt_epi_grad_workspace(m, n, k, type)
+ * bytes; W is read for dA only, A for dW only.  The outputs must not overlap the
+ * inputs.  m == 0 clears dW and dbias, n == 0 dA.
+ */
+og_status og_gemm_nt_epi_grad(int64_t m, int64_t n, int64_t k, const void *dC, int64_t lddc,
+                              const void *A, int64_t lda, const void *W, int64_t ldw, int type,
+                              const void *P, int64_t ldp, int act, void *dA, int64_t ldda, void *dW,
+                              int64_t lddw, void *dbias, void *workspace, int64_t workspace_bytes);
+/* Bytes of its workspace, or a negative og_status.  Needs no device. */
+int64_t og_gemm_nt_epi_grad_workspace(int64_t m, int64_t n, int64_t k, int type);
 
 /*
  * The Euclidean norm over all elements of `count` tensors, as a model's

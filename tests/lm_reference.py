@@ -220,3 +220,106 @@ def logit_penalties(z, tokens, lengths, prompts, repetition, frequency, presence
     e = size * 2.0 ** -24 * 1.01 + 2.0 ** -148
     e = e + half_step(z.dtype) * (x.abs() + e) + torch.finfo(z.dtype).smallest_normal * torch.finfo(z.dtype).eps
     return x, e
+
+
+# -- gemm_nt_epi -------------------------------------------------------------
+
+def activation(x, act):
+    """act(x), act'(x) in 64 bits, with their limits at infinity."""
+    if act is None:
+        return x, torch.ones_like(x)
+    inf = torch.where(x.isnan(), x, torch.full_like(x, float("nan")))
+    flat = x.clamp(-300, 300)  # (both are their limits in fp32 from 120 on)
+    if act == "relu":
+        y, d = x.clamp(min=0), (x > 0).to(x.dtype)
+        return torch.where(x.isnan(), inf, y), torch.where(x.isnan(), inf, d)
+    if act == "gelu":
+        below = 0.5 * torch.erfc(-flat * 0.5 ** 0.5)
+        d = below + flat * torch.exp(-flat * flat / 2) / (2 * torch.pi) ** 0.5
+    elif act == "gelu_tanh":
+        c = 2 * (2 / torch.pi) ** 0.5
+        u = c * (flat + 0.044715 * flat ** 3)
+        below = torch.sigmoid(u)
+        d = below + flat * below * torch.sigmoid(-u) * c * (1 + 3 * 0.044715 * flat ** 2)
+    else:
+        below = torch.sigmoid(flat)
+        d = below + flat * below * torch.sigmoid(-flat)
+    y = torch.where(x > 300, x, flat * below)
+    return torch.where(x.isnan(), inf, y), d
+
+
+STEEP = 1.13  # no activation's slope is larger, nor (by a little) any second derivative's size
+
+
+def act_error(x, e, act):
+    """Of act(v) and act'(v) in fp32 for |v - x| <= e: the slope times e, and evaluation.  Every
+    value is a product of at most x and factors whose relative error is 2^-22 for each of a few
+    operations and, of the exponential, 2^-23 for each unit of its argument (at most x^2 / 2 or
+    1.6 (x + 0.045 x^3), where the value has not vanished: 110)."""
+    if act is None:
+        return e, torch.zeros_like(e)
+    y, d = activation(x, act)
+    if act == "relu":
+        return e, torch.where(x.abs() <= e, torch.ones_like(e), torch.zeros_like(e))
+    arg = (4 + torch.minimum(x.abs() * 2 + x * x, torch.full_like(x, 110.0))) * 2.0 ** -22
+    arg = arg.nan_to_num()
+    small = (y.abs() + d.abs()).clamp(max=2.0) + torch.exp(-x.abs().clamp(max=90) * 0.5)
+    return STEEP * e + arg * (y.abs() + 2.0 ** -120), STEEP * e + arg * small
+
+
+def product_error(a64, b64, dtype):
+    """Bound on the error of a @ b.T of two matrices of a type (in 64 bits here) by the tile product
+    or the few rows' kernel: sum_error and up to 16 parts' joining; fp32 to each row's 2^-38
+    besides."""
+    planes, k = 2 if dtype == torch.float32 else 1, a64.shape[1]
+    e = (a64.abs() @ b64.abs().t()) * (sum_error(k, planes) + 40 * ADD)
+    if planes == 2 and k:
+        ta, tb = a64.abs().amax(1, keepdim=True), b64.abs().amax(1, keepdim=True)
+        e = e + LAST * (ta * b64.abs().sum(1) + a64.abs().sum(1, keepdim=True) * tb.t())
+        e = e + 2.0 ** -148
+    return e
+
+
+def rounded(x, e, dtype):
+    """The bound after a rounding to dtype."""
+    info = torch.finfo(dtype)
+    return e + half_step(dtype) * (x.abs() + e) + info.smallest_normal * info.eps
+
+
+def gemm_epi(a, w, bias, act, residual):
+    """dict of exact values and bounds: pre, c."""
+    v = a.to(F64) @ w.to(F64).t()
+    e = product_error(a.to(F64), w.to(F64), a.dtype)
+    if bias is not None:
+        v = v + bias.to(F64)
+        e = e + 2.0 ** -24 * (v.abs() + e)
+    y, _ = activation(v, act)
+    ey, _ = act_error(v, e, act)
+    if residual is not None:
+        y = y + residual.to(F64)
+        ey = ey + 2.0 ** -24 * (y.abs() + ey)
+    return {"pre": v, "e_pre": rounded(v, e, a.dtype), "c": y, "e_c": rounded(y, ey, a.dtype)}
+
+
+def gemm_epi_grad(dc, a, w, pre, act):
+    """dict of exact values for this pre, and bounds: da, dw, dbias.  16-bit types round dP to the
+    type (its largest subnormal's half step, twice in fp16, which may hold halves)."""
+    dc64, a64, w64 = dc.to(F64), a.to(F64), w.to(F64)
+    dp, edp = dc64, torch.zeros_like(dc64)
+    if act is not None:
+        x = pre.to(F64)
+        _, d = activation(x, act)
+        _, ed = act_error(x, torch.zeros_like(x), act)
+        dp = dc64 * d
+        edp = dc64.abs() * ed + 2.0 ** -24 * (dp.abs() + dc64.abs() * ed) + 2.0 ** -149
+    held = edp
+    info = torch.finfo(dc.dtype)
+    if act is not None and dc.dtype != torch.float32:
+        held = edp + half_step(dc.dtype) * (dp.abs() + edp) + 2 * info.smallest_normal * info.eps
+    out = {"da": dp @ w64, "dw": dp.t() @ a64, "dbias": dp.sum(0)}
+    e_da = held @ w64.abs() + product_error(dp, w64.t(), dc.dtype) * 1.01
+    e_dw = held.t() @ a64.abs() + product_error(dp.t(), a64.t(), dc.dtype) * 1.01
+    e_db = edp.sum(0) + 22 * 2.0 ** -24 * (dp.abs() + edp).sum(0)
+    for name, e in (("da", e_da), ("dw", e_dw), ("dbias", e_db)):
+        out["e_" + name] = rounded(out[name], e, dc.dtype)
+    return out

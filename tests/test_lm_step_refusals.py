@@ -106,3 +106,78 @@ def test_valid_tensors_reach_the_device(L):
     assert _norm(L, _grads(dict(y=0, ldy=0))) == og.OG_ERR_DEVICE
     assert _clip(L, _grads(dict(x=8192, ldy=9))) == og.OG_ERR_DEVICE
     assert _clip(L, None, count=0) == og.OG_ERR_DEVICE  # the norm of nothing is written there
+
+
+def _epi(L, m=3, n=5, k=8, A=P, lda=8, W=P, ldw=8, type=0, bias=P, act=2, R=P, ldr=5, Pre=ODD, ldp=5, C=P, ldc=5, ws=P,
+         bytes=BIG):
+    return L.og_gemm_nt_epi(m, n, k, A, lda, W, ldw, type, bias, act, R, ldr, Pre, ldp, C, ldc, ws, bytes)
+
+
+def _epi_grad(L, m=3, n=5, k=8, dC=P, lddc=5, A=P, lda=8, W=P, ldw=8, type=0, Pre=P, ldp=5, act=2, dA=P, ldda=8, dW=P,
+              lddw=8, dbias=P, ws=P, bytes=BIG):
+    return L.og_gemm_nt_epi_grad(m, n, k, dC, lddc, A, lda, W, ldw, type, Pre, ldp, act, dA, ldda, dW, lddw, dbias, ws,
+                                 bytes)
+
+
+SHARED = [dict(type=3), dict(type=-1), dict(act=5), dict(act=-1), dict(m=-1), dict(n=-1), dict(k=-1), dict(lda=7),
+          dict(ldw=7), dict(ldp=4), dict(A=NULL), dict(W=NULL), dict(ws=ODD), dict(ws=NULL, m=500, n=500, k=500, lda=500,
+          ldw=500, ldr=500, ldp=500, ldc=500, lddc=500, ldda=500, lddw=500)]
+
+
+def _given(call, kw):
+    import inspect
+    return {k: v for k, v in kw.items() if k in inspect.signature(call).parameters}
+
+
+@pytest.mark.parametrize("kw", SHARED + [dict(ldr=4), dict(ldc=4), dict(C=NULL), dict(ldr=6), dict(Pre=P), dict(k=0, lda=0)])
+def test_epi_rejects_before_launch(L, kw):
+    assert _epi(L, **_given(_epi, kw)) == og.OG_ERR_INVALID_ARG
+    assert L.og_last_error()
+
+
+@pytest.mark.parametrize("kw", SHARED + [dict(lddc=4), dict(ldda=7), dict(lddw=7), dict(dC=NULL), dict(Pre=NULL)])
+def test_epi_grad_rejects_before_launch(L, kw):
+    assert _epi_grad(L, **_given(_epi_grad, kw)) == og.OG_ERR_INVALID_ARG
+    assert L.og_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(m=(1 << 24) + 1), dict(n=(1 << 20) + 1), dict(k=(1 << 20) + 1),
+                                dict(m=1 << 24, n=1 << 13), dict(n=1 << 20, k=1 << 17), dict(m=1 << 24, k=1 << 13)])
+@pytest.mark.parametrize("call", [_epi, _epi_grad])
+def test_epi_too_large(L, call, kw):
+    every = dict.fromkeys(("lda", "ldw", "ldr", "ldp", "ldc", "lddc", "ldda", "lddw"), 1 << 21)
+    assert call(L, **_given(call, {**every, **kw})) == og.OG_ERR_TOO_LARGE
+
+
+def test_epi_empty_and_valid(L):
+    assert _epi(L, m=0, A=NULL, C=NULL, ws=NULL, bytes=0) == og.OG_OK
+    assert _epi(L, n=0, W=NULL, C=NULL, ws=NULL, bytes=0) == og.OG_OK
+    assert _epi_grad(L, dA=NULL, dW=NULL, dbias=NULL) == og.OG_OK
+    assert _epi_grad(L, k=0, lda=1, ldw=1, ldda=1, lddw=1, dbias=NULL) == og.OG_OK
+    assert _epi_grad(L, m=0, dW=NULL, dbias=NULL) == og.OG_OK
+    _no_gpu()
+    for type in (0, 1, 2):
+        assert _epi(L, type=type) == og.OG_ERR_DEVICE
+        assert _epi(L, type=type, k=0, lda=1, ldw=1, A=NULL, W=NULL) == og.OG_ERR_DEVICE
+        assert _epi_grad(L, type=type) == og.OG_ERR_DEVICE
+        assert _epi_grad(L, type=type, Pre=NULL, ldp=0, act=0) == og.OG_ERR_DEVICE
+        # without dW, A is not wanted; without dA, W is not
+        assert _epi_grad(L, type=type, A=NULL, lda=0, dW=NULL, lddw=0) == og.OG_ERR_DEVICE
+        assert _epi_grad(L, type=type, W=NULL, ldw=0, dA=NULL, ldda=0) == og.OG_ERR_DEVICE
+        # an empty batch clears dW and dbias
+        assert _epi_grad(L, type=type, m=0, dC=NULL, A=NULL, W=NULL, Pre=NULL) == og.OG_ERR_DEVICE
+
+
+def test_epi_workspace(L):
+    for f in (L.og_gemm_nt_epi_workspace, L.og_gemm_nt_epi_grad_workspace):
+        assert f(3, 5, 8, 3) == og.OG_ERR_INVALID_ARG
+        assert f(-1, 5, 8, 0) == og.OG_ERR_INVALID_ARG
+        assert f(1 << 25, 5, 8, 0) == og.OG_ERR_TOO_LARGE
+    for type in (0, 1, 2):
+        m, n, k = 300, 200, 128
+        need = L.og_gemm_nt_epi_grad_workspace(m, n, k, type)
+        strides = dict(lddc=n, lda=k, ldw=k, ldp=n, ldda=k, lddw=k)
+        assert _epi_grad(L, m, n, k, type=type, bytes=need - 1, **strides) == og.OG_ERR_INVALID_ARG
+        need = L.og_gemm_nt_epi_workspace(m, n, k, type)
+        strides = dict(lda=k, ldw=k, ldr=n, ldp=n, ldc=n)
+        assert _epi(L, m, n, k, type=type, bytes=need - 1, **strides) == og.OG_ERR_INVALID_ARG
