@@ -62,6 +62,197 @@ __global__ __launch_bounds__(256) void planes_kernel(Side a, Side b, int cols, i
   }
 }
 
+// Few rows of A: bound by the bytes of W, which goes from memory to the matrix cores through
+// registers alone.  A block takes 16 NT rows of W and 16 MT rows of A; its W waves share k (their
+// sums meet in LDS, in wave order).  A lane's 16 bytes of a load are the 8 values its fragment
+// needs, so that one instruction reads 64 neighbouring bytes of 16 rows.  The loads of the next
+// chunk are in flight while one is multiplied.
+struct Rows {
+  int m, n, k;
+  const void *a, *w;
+  int64_t lda, ldw;
+  Finish f;
+};
+
+template <class T>
+struct Eight {
+  T v[8];
+};
+// Eight values of a row from k on, zero past its end.  FULL: it does not end here.
+template <class T, bool FULL>
+__device__ __forceinline__ Eight<T> load8(const T *row, int k, int K) {
+  Eight<T> t;
+  if (FULL || k + 8 <= K) {
+    __builtin_memcpy(&t, row + k, sizeof t);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t.v[e] = k + e < K ? row[k + e] : (T)0.0f;
+  }
+  return t;
+}
+
+// Fragments and their product: 16-bit values as they are; fp32 as three bf16 planes, cut, 24 bits
+// (h + m + l = the value; the products left out are 2^-24 of the whole and below), which need no
+// power of two.
+template <class T>
+struct Fragment {
+  s16x8 v;
+  Fragment() = default;
+  __device__ __forceinline__ explicit Fragment(const Eight<T> &x) { __builtin_memcpy(&v, &x, sizeof v); }
+  static __device__ __forceinline__ f32x4 product(const Fragment &x, const Fragment &w, f32x4 c) {
+    return mfma<T>(x.v, w.v, c);
+  }
+};
+template <>
+struct Fragment<float> {
+  s16x8 p[3];
+  Fragment() = default;
+  __device__ __forceinline__ explicit Fragment(const Eight<float> &x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // (a NaN is made quiet first: its highest mantissa bit then stays)
+      float r = __builtin_canonicalizef(x.v[e]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const uint32_t top = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
+        const float h = __builtin_bit_cast(float, top);
+        p[q][e] = (short)(top >> 16);
+        r = __builtin_isfinite(h) ? r - h : 0.0f;
+      }
+    }
+  }
+  static __device__ __forceinline__ f32x4 product(const Fragment &x, const Fragment &w, f32x4 c) {
+    constexpr int kX[6] = {2, 0, 1, 1, 0, 0}, kW[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c = mfma<__bf16>(x.p[kX[i]], w.p[kW[i]], c);
+    return c;
+  }
+};
+
+template <class T, int MT, int NT>
+struct Chunk {
+  static constexpr int kSteps = sizeof(T) == 4 ? 2 : 4, kDepth = 32 * kSteps;
+  Eight<T> w[NT][kSteps], x[MT][kSteps];
+  template <bool FULL>
+  __device__ __forceinline__ void load(const T *const (&a)[MT], const bool (&in)[MT], const T *const (&b)[NT], int k,
+                                       int K) {
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) w[u][j] = load8<T, FULL>(b[u], k + 32 * j, K);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+        if (in[t]) x[t][j] = load8<T, FULL>(a[t], k + 32 * j, K);
+  }
+};
+
+template <class T, int W, int MT, int NT>
+__global__ __launch_bounds__(W * 64) void rows_kernel(Rows p) {
+  using C = Chunk<T, MT, NT>;
+  __shared__ float sums[W][16 * MT][16 * NT + 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
+  const int chunks = (p.k + C::kDepth - 1) / C::kDepth;
+  const int c0 = (int)((int64_t)chunks * wave / W), c1 = (int)((int64_t)chunks * (wave + 1) / W);
+  const T *a[MT], *b[NT];
+  bool in[MT];
+  C next;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + i;
+    in[t] = m < p.m;
+    a[t] = static_cast<const T *>(p.a) + (int64_t)min(m, p.m - 1) * p.lda;
+#pragma unroll
+    for (int j = 0; j < C::kSteps; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) next.x[t][j].v[e] = (T)0.0f;  // what rows past m hold
+  }
+#pragma unroll
+  for (int u = 0; u < NT; ++u) b[u] = static_cast<const T *>(p.w) + (int64_t)min(n0 + 16 * u + i, p.n - 1) * p.ldw;
+  auto load = [&](int c) __attribute__((always_inline)) {
+    const int k = c * C::kDepth + 8 * g;
+    if ((c + 1) * C::kDepth <= p.k) next.template load<true>(a, in, b, k, p.k);
+    else next.template load<false>(a, in, b, k, p.k);
+  };
+  // acc[u][t][r]: row 16 u + i of W, row 16 t + 4 g + r of A
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[u][t] = f32x4{0, 0, 0, 0};
+  if (c0 < c1) load(c0);
+  for (int c = c0; c < c1; ++c) {
+    const C now = next;
+    if (c + 1 < c1) load(c + 1);
+#pragma unroll
+    for (int j = 0; j < C::kSteps; ++j) {
+      Fragment<T> w[NT];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) w[u] = Fragment<T>(now.w[u][j]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const Fragment<T> x(now.x[t][j]);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) acc[u][t] = Fragment<T>::product(x, w[u], acc[u][t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wave][16 * t + 4 * g + r][16 * u + i] = acc[u][t][r];
+  __syncthreads();
+  for (int o = threadIdx.x; o < MT * NT * 64; o += W * 64) {
+    const int row = o / (4 * NT), col = o % (4 * NT) * 4, m = m0 + row, n = n0 + col;
+    if (m >= p.m || n >= p.n) continue;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const f32x4 part = *reinterpret_cast<const f32x4 *>(&sums[w][row][col]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += part[e];
+    }
+    finish<T, false>(p.f, m, n, p.n - n, v);
+  }
+}
+
+template <class T, int W, int MT, int NT>
+void launch_rows(const Rows &p, hipStream_t s) {
+  hipLaunchKernelGGL((rows_kernel<T, W, MT, NT>),
+                     dim3((p.n + 16 * NT - 1) / (16 * NT), (p.m + 16 * MT - 1) / (16 * MT)), dim3(W * 64), 0, s, p);
+}
+
+// Whether a product runs on the rows kernel: up to 16 rows (fp32: 64, whose tile product needs
+// the planes of W made first), or where W read once for each 16 (32) rows is little.  us, rows
+// kernel and tile product, W rotating through memory: 16 rows of bf16 on 11008 x 4096 27.4 and 26.9,
+// on 4096 x 4096 10.7 and 12.3; 32 there 17.7 and 12.9; 64 on 1531 x 1000 5.1 and 8.6, 128 6.4 and 8.5.
+// fp32: 64 rows on 11008 x 4096 101 and 148, 128 186 and 153; 128 on 1531 x 1000 12.9 and 15.8.
+template <class T>
+bool few_rows(int64_t m, int64_t n, int64_t k) {
+  constexpr bool wide = sizeof(T) == 4;
+  return m <= (wide ? 64 : 16) || (wide ? (m + 31) / 32 * n * k <= (1 << 23) : (m + 15) / 16 * n * k <= (1 << 24));
+}
+
+// Tiles of a block: one of each up to 16 rows and for 16-bit types (11008 x 4096 bf16 by one row
+// 21.3 us, two tiles of W 24.5); two of A for more of fp32, and two of W where that leaves every
+// compute unit a block (4096 x 11008 by 64 rows 89 us with two, 124 with one; by 32, 128 blocks, 89
+// and 72).  Bound by the bytes of W: 90 MB of bf16 by one row at 4.2 TB/s, 180 MB of fp32 in 41 us at 4.4.
+template <class T>
+void run_rows(const Rows &p, hipStream_t s) {
+  if constexpr (sizeof(T) == 4) {
+    if (p.m > 16) {
+      const bool many = (int64_t)((p.n + 31) / 32) * ((p.m + 31) / 32) >= 256;
+      return many ? launch_rows<T, 4, 2, 2>(p, s) : launch_rows<T, 4, 2, 1>(p, s);
+    }
+  }
+  launch_rows<T, 8, 1, 1>(p, s);
+}
+
 struct Plan {
   int64_t kp;  // k padded
   int64_t tops_at, a_at, w_at, parts_at, total;
@@ -69,10 +260,11 @@ struct Plan {
 
 template <class T>
 Plan plan(int64_t m, int64_t n, int64_t k) {
-  Plan p;
+  Plan p{};
   Room r;
   constexpr int P = kPlanes<T>;
   p.kp = round_up(k, P == 2 ? 32 : 8);
+  if (few_rows<T>(m, n, k)) return Plan{};
   p.tops_at = r.take(P == 2 ? (round_up(m, 64) + round_up(n, 64)) * 4 : 0);
   p.a_at = r.take(P * m * p.kp * 2);
   p.w_at = r.take(P * n * p.kp * 2);
@@ -86,11 +278,11 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int type) {
 
 template <class T>
 void forward(const Call &c, const Plan &p, hipStream_t s) {
-  Finish f = c.f;
-  f.vec_b = whole(static_cast<const T *>(f.bias), 0);
-  f.vec_r = whole(static_cast<const T *>(f.residual), f.ldr);
-  f.vec_p = whole(static_cast<const T *>(f.pre), f.ldp);
-  f.vec_o = whole(static_cast<const T *>(f.out), f.ldo);
+  Finish f = set_accesses<T>(c.f);
+  if (few_rows<T>(c.m, c.n, c.k)) {
+    run_rows<T>(Rows{(int)c.m, (int)c.n, (int)c.k, c.a, c.w, c.lda, c.ldw, f}, s);
+    return;
+  }
   Args g{};
   g.M = (int)c.m;
   g.N = (int)c.n;
@@ -110,7 +302,7 @@ void forward(const Call &c, const Plan &p, hipStream_t s) {
     g.a = operand16(c.a, c.lda, c.m, c.k, p.kp, c.ws + p.a_at, s);
     g.b = operand16(c.w, c.ldw, c.n, c.k, p.kp, c.ws + p.w_at, s);
   }
-  run_product<T, false, false>(g, f, c.ws + p.parts_at, s);
+  run_product<T, false, false, false>(g, f, c.ws + p.parts_at, s);
 }
 
 }  // namespace og::epi::fwd
@@ -152,7 +344,7 @@ og_status og_gemm_nt_epi(int64_t m, int64_t n, int64_t k, const void *A, int64_t
     return fail(OG_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if ((st = check_device()) != OG_OK) return st;
   const Call c{m, n, k, A, W, lda, ldw,
-               Finish{nullptr, nullptr, 0, bias, act, residual, ldr, P, ldp, C, ldc, 0, 0, 0, 0},
+               Finish{nullptr, nullptr, 0, bias, act, residual, ldr, P, ldp, C, ldc, 0, 0, 0, 0, 0},
                static_cast<char *>(workspace)};
   if (type == OG_F32) forward<float>(c, p, current_stream());
   else if (type == OG_BF16) forward<__bf16>(c, p, current_stream());

@@ -19,50 +19,84 @@ using namespace og::tile;
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The logistic function s of x, and 1 - s, neither by a difference of near values.
-__device__ __forceinline__ void logistic(float x, float &s, float &rest) {
-  const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e), one = 1.0f / (1.0f + e), other = e * one;
-  s = x >= 0 ? one : other;
-  rest = x >= 0 ? other : one;
-}
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Phi(x), the normal distribution, accurate in its tail too.
-__device__ __forceinline__ float normal(float x) { return 0.5f * erfcf(-0.70710678118654752f * x); }
+// The logistic function of x: 1 / (1 + e), e = exp(-x).
+struct Logistic {
+  float e, s;
+  __device__ __forceinline__ explicit Logistic(float x) {
+    e = exp2_of(-kLog2e * x);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
+  }
+};
+
+// The normal distribution Phi and e = exp(-x^2 / 2).  The tail beyond |x| is e times a polynomial
+// of degree 9 in s = 1 / (1 + p |x|), fitted to exp(x^2 / 2) Phi(-|x|) for |x| up to 20 by least
+// squares of the relative error, reweighted until its largest values are even (2.6e-8): the tail
+// keeps its relative accuracy.
+struct Normal {
+  float e, phi;
+  __device__ __forceinline__ explicit Normal(float x) {
+    e = exp2_of(-0.5f * kLog2e * (x * x));
+    const float s = __builtin_amdgcn_rcpf(fmaf(0.26870057f, fabsf(x), 1.0f));
+    float q = 0.029144833f;
+    q = fmaf(q, s, -0.12963144f);
+    q = fmaf(q, s, 0.17909917f);
+    q = fmaf(q, s, -0.077821545f);
+    q = fmaf(q, s, 0.113234f);
+    q = fmaf(q, s, 0.06998415f);
+    q = fmaf(q, s, 0.101809844f);
+    q = fmaf(q, s, 0.10697627f);
+    q = fmaf(q, s, 0.10720471f);
+    const float tail = e * (q * s);
+    phi = x < 0 ? tail : 1.0f - tail;
+  }
+};
 
 constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kCube = 0.044715f;
 
 // act(x).  Far to the left, where the value is 0 in fp32, x times 0 would make an infinity NaN.
-__device__ __forceinline__ float act_of(float x, int act) {
-  float s, rest;
-  switch (act) {
-    case OG_ACT_RELU: return x > 0 ? x : x == x ? 0.0f : x;
-    case OG_ACT_GELU: return x < -20 ? -0.0f : x * normal(x);
-    case OG_ACT_GELU_TANH:
-      logistic(kTanh * x * (1.0f + kCube * x * x), s, rest);
-      return x < -20 ? -0.0f : x * s;
-    case OG_ACT_SILU: logistic(x, s, rest); return x < -120 ? -0.0f : x * s;
-    default: return x;
-  }
+template <int ACT>
+__device__ __forceinline__ float act_of(float x) {
+  if constexpr (ACT == OG_ACT_RELU) return x > 0 ? x : x == x ? 0.0f : x;
+  if constexpr (ACT == OG_ACT_GELU) return x < -20 ? -0.0f : x * Normal(x).phi;
+  if constexpr (ACT == OG_ACT_GELU_TANH)
+    return x < -20 ? -0.0f : x * Logistic(kTanh * x * fmaf(kCube, x * x, 1.0f)).s;
+  if constexpr (ACT == OG_ACT_SILU) return x < -120 ? -0.0f : x * Logistic(x).s;
+  return x;
 }
 
-// act'(x); 0 and 1 far to the left and the right.
-__device__ __forceinline__ float slope_of(float x, int act) {
-  float s, rest;
+// act'(x); 0 and 1 where it is in fp32, to the left and the right.
+template <int ACT>
+__device__ __forceinline__ float slope_of(float x) {
+  const float side = x > 0 ? 1.0f : 0.0f;
+  if constexpr (ACT == OG_ACT_RELU) return x == x ? side : x;
+  if constexpr (ACT == OG_ACT_GELU) {
+    const Normal n(x);
+    return fabsf(x) > 20 ? side : fmaf(x * 0.3989422804014327f, n.e, n.phi);
+  }
+  if constexpr (ACT == OG_ACT_GELU_TANH) {
+    const Logistic l(kTanh * x * fmaf(kCube, x * x, 1.0f));
+    // (e s is 1 - s without the difference)
+    return fabsf(x) > 10 ? side : l.s + x * l.s * (l.e * l.s) * fmaf(3.0f * kCube * kTanh, x * x, kTanh);
+  }
+  if constexpr (ACT == OG_ACT_SILU) {
+    const Logistic l(x);
+    return fabsf(x) > 80 ? side : fmaf(l.s * x, l.e * l.s, l.s);
+  }
+  return 1.0f;
+}
+
+// f(ACT) for act, outside the loops over values.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
-    case OG_ACT_RELU: return x > 0 ? 1.0f : x == x ? 0.0f : x;
-    case OG_ACT_GELU:
-      if (fabsf(x) > 20) return x > 0 ? 1.0f : 0.0f;
-      return normal(x) + x * 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * x * x);
-    case OG_ACT_GELU_TANH:
-      if (fabsf(x) > 20) return x > 0 ? 1.0f : 0.0f;
-      logistic(kTanh * x * (1.0f + kCube * x * x), s, rest);
-      return s + x * s * rest * kTanh * (1.0f + 3.0f * kCube * x * x);
-    case OG_ACT_SILU:
-      if (fabsf(x) > 120) return x > 0 ? 1.0f : 0.0f;
-      logistic(x, s, rest);
-      return s + s * x * rest;
-    default: return 1.0f;
+    case OG_ACT_RELU: f(std::integral_constant<int, OG_ACT_RELU>()); break;
+    case OG_ACT_GELU: f(std::integral_constant<int, OG_ACT_GELU>()); break;
+    case OG_ACT_GELU_TANH: f(std::integral_constant<int, OG_ACT_GELU_TANH>()); break;
+    case OG_ACT_SILU: f(std::integral_constant<int, OG_ACT_SILU>()); break;
+    default: f(std::integral_constant<int, OG_ACT_NONE>());
   }
 }
 
@@ -141,72 +175,163 @@ struct Finish {
   void *out;
   int64_t ldo;
   int vec_b, vec_r, vec_p, vec_o;  // four values are one access
+  int whole;                       // all of them are, and 256 rows apart is within 32 bits
 };
-
-// Four neighbouring sums of row m from column n on, `left` of them inside.
 template <class T>
-__device__ __forceinline__ void finish(const Finish &f, int64_t m, int n, int left, f32x4 v, int mpower) {
+Finish set_accesses(Finish f) {
+  f.vec_b = whole(static_cast<const T *>(f.bias), 0);
+  f.vec_r = whole(static_cast<const T *>(f.residual), f.ldr);
+  f.vec_p = whole(static_cast<const T *>(f.pre), f.ldp);
+  f.vec_o = whole(static_cast<const T *>(f.out), f.ldo);
+  const int64_t far = std::max({f.residual ? f.ldr : 0, f.pre ? f.ldp : 0, f.ldo});
+  f.whole = (f.vec_r || !f.residual) && (f.vec_p || !f.pre) && f.vec_o && far <= (1 << 21);
+  return f;
+}
+
+template <class T>
+__device__ __forceinline__ void scale(const Finish &f, f32x4 &v, int mpower, const int (&npower)[4]) {
   if constexpr (kPlanes<T> == 2) {
-    if (f.mtop) {
-      const f32x4 top = load4(f.ntop + n, left, true);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], -mpower - power_of(top[e]));
-    }
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], -mpower - npower[e]);
   } else {
     if (f.up) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], f.up);
     }
   }
-  if (f.bias) {
-    const f32x4 b = load4(static_cast<const T *>(f.bias) + n, left, f.vec_b);
+}
+
+// What belongs to four columns from n on, `left` of them inside, and to a row.
+template <class T, bool PLAIN>
+__device__ __forceinline__ void of_columns(const Finish &f, int n, int left, int (&npower)[4], f32x4 &bias) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += b[e];
+  for (int e = 0; e < 4; ++e) npower[e] = 0;
+  if constexpr (kPlanes<T> == 2) {
+    if (f.ntop) {
+      const f32x4 top = load4(f.ntop + n, left, true);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) npower[e] = power_of(top[e]);
+    }
   }
-  if (f.pre) store4(static_cast<T *>(f.pre) + m * f.ldp + n, v, left, f.vec_p);
-  if (f.act != OG_ACT_NONE) {
+  if (!PLAIN && f.bias) bias = load4(static_cast<const T *>(f.bias) + n, left, f.vec_b);
+}
+template <class T>
+__device__ __forceinline__ int of_row(const Finish &f, int m) {
+  if constexpr (kPlanes<T> == 2) return f.mtop ? power_of(f.mtop[m]) : 0;
+  return 0;
+}
+
+// All steps of four neighbouring sums of row m.
+template <class T, bool PLAIN>
+__device__ __forceinline__ void finish(const Finish &f, int64_t m, int n, int left, f32x4 v) {
+  int npower[4];
+  f32x4 bias = {0, 0, 0, 0};
+  of_columns<T, PLAIN>(f, n, left, npower, bias);
+  scale<T>(f, v, of_row<T>(f, (int)m), npower);
+  if constexpr (!PLAIN) {
+    v += bias;
+    if (f.pre) store4(static_cast<T *>(f.pre) + m * f.ldp + n, v, left, f.vec_p);
+    with_act(f.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = act_of(v[e], f.act);
-  }
-  if (f.residual) {
-    const f32x4 r = load4(static_cast<const T *>(f.residual) + m * f.ldr + n, left, f.vec_r);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += r[e];
+      for (int e = 0; e < 4; ++e) v[e] = act_of<act()>(v[e]);
+    });
+    if (f.residual) v += load4(static_cast<const T *>(f.residual) + m * f.ldr + n, left, f.vec_r);
   }
   store4(static_cast<T *>(f.out) + m * f.ldo + n, v, left, f.vec_o);
 }
 
-// The tile product's epilogue: finished, or (a product whose k is split) the part's sums.
+// The tile product's epilogue: finished, or (a product whose k is split) the part's sums.  PLAIN:
+// a gradient's, only scaled and stored.
 struct StoreArgs {
   Finish f;
   float *part;     // null: not split
   int64_t ld, step;  // of a row of a part, and from one part to the next
 };
-template <class T>
+template <class T, bool PLAIN>
 struct Store {
   using Args = StoreArgs;
   static constexpr bool kSymmetric = false;
+  // A block whose rows and columns are all the product's, all accesses whole: places as 32-bit
+  // offsets from the wave's first element, which is uniform.  Each four values go all the way
+  // before the next (fences): together their activations would need more registers than there
+  // are (4096 x 11008 x 4096 bf16, SiLU and P: epilogue @E0@ us a tile of 256 x 256 so, 36 with
+  // places of 64 bits, the activation chosen for each value and IEEE divisions).
+  template <class S, int ACT>
+  static __device__ __forceinline__ void inside(f32x4 (&acc)[S::FM][S::FN], const Place &t, const Finish &f) {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    const uint32_t row = t.lane & 15, col = 4 * (t.lane >> 4);
+    const int64_t m = t.m0, n = t.n0;
+    char *out = reinterpret_cast<char *>(static_cast<T *>(f.out) + m * f.ldo + n);
+    char *pre = PLAIN || !f.pre ? nullptr : reinterpret_cast<char *>(static_cast<T *>(f.pre) + m * f.ldp + n);
+    const char *residual =
+        PLAIN || !f.residual ? nullptr : reinterpret_cast<const char *>(static_cast<const T *>(f.residual) + m * f.ldr + n);
+    const uint32_t ldo = (uint32_t)f.ldo * sizeof(T), ldp = (uint32_t)f.ldp * sizeof(T), ldr = (uint32_t)f.ldr * sizeof(T);
+    f32x4 bias[S::FN];
+    int npower[S::FN][4];
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) {
+      bias[j] = f32x4{0, 0, 0, 0};
+      of_columns<T, PLAIN>(f, t.n0 + 16 * j + col, 4, npower[j], bias[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const uint32_t r = row + 16 * i;
+      const int mpower = of_row<T>(f, t.m0 + r);
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) {
+        const uint32_t c = (col + 16 * j) * sizeof(T);
+        f32x4 v = acc[i][j];
+        T4 h;
+        scale<T>(f, v, mpower, npower[j]);
+        if constexpr (!PLAIN) {
+          v += bias[j];
+          if (pre) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = (T)v[e];
+            *reinterpret_cast<T4 *>(pre + r * ldp + c) = h;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = act_of<ACT>(v[e]);
+          if (residual) {
+            h = *reinterpret_cast<const T4 *>(residual + r * ldr + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += (float)h[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = (T)v[e];
+        *reinterpret_cast<T4 *>(out + r * ldo + c) = h;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
   template <class S>
   static __device__ __forceinline__ void store(f32x4 (&acc)[S::FM][S::FN], const Place &t, const Args &e) {
     const int nc = t.n0 + 4 * (t.lane >> 4);
+    if (!e.part && e.f.whole && (t.tile_m + 1) * S::BM <= t.M && (t.tile_n + 1) * S::BN <= t.N) {
+      if constexpr (PLAIN) inside<S, OG_ACT_NONE>(acc, t, e.f);
+      else with_act(e.f.act, [&](auto act) __attribute__((always_inline)) { inside<S, act()>(acc, t, e.f); });
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const int m = t.m0 + 16 * i + (t.lane & 15);
       if (m >= t.M) continue;
-      const int mpower = kPlanes<T> == 2 && e.f.mtop ? power_of(e.f.mtop[m]) : 0;
+      float *to = e.part + t.batch * e.step + m * e.ld;
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const int n = nc + 16 * j;
         if (n >= t.N) continue;
-        if (e.part) *reinterpret_cast<f32x4 *>(e.part + t.batch * e.step + m * e.ld + n) = acc[i][j];
-        else finish<T>(e.f, m, n, t.N - n, acc[i][j], mpower);
+        if (e.part) *reinterpret_cast<f32x4 *>(to + n) = acc[i][j];
+        else finish<T, PLAIN>(e.f, m, n, t.N - n, acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
 };
 
 // Adds the parts of a split product in order and finishes.
-template <class T>
+template <class T, bool PLAIN>
 static __global__ __launch_bounds__(256) void join_kernel(int M, int N, int parts, const float *part, int64_t ld,
                                                    int64_t step, Finish f) {
   const int per = (N + 3) / 4;
@@ -219,7 +344,7 @@ static __global__ __launch_bounds__(256) void join_kernel(int M, int N, int part
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += w[e];
     }
-    finish<T>(f, m, n, N - n, v, kPlanes<T> == 2 && f.mtop ? power_of(f.mtop[m]) : 0);
+    finish<T, PLAIN>(f, m, n, N - n, v);
   }
 }
 
@@ -250,20 +375,20 @@ int64_t parts_bytes(int64_t M, int64_t N, int64_t K) {
   return p > 1 ? p * M * round_up(N, 4) * 4 : 0;
 }
 
-template <class T, bool TA, bool TB>
+template <class T, bool TA, bool TB, bool PLAIN>
 void run_product(Args g, const Finish &f, char *ws, hipStream_t s) {
   using E = Element<T>;
   const int parts = parts_of<T, TA && TB>(g.M, g.N, g.K);
   if (parts == 1) {
-    product<E, kPlanes<T>, TA, TB, Store<T>>(g, StoreArgs{f, nullptr, 0, 0}, 1, s);
+    product<E, kPlanes<T>, TA, TB, Store<T, PLAIN>>(g, StoreArgs{f, nullptr, 0, 0}, 1, s);
     return;
   }
   float *part = reinterpret_cast<float *>(ws);
   const int64_t ld = round_up(g.N, 4), step = g.M * ld;
   g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  product<E, kPlanes<T>, TA, TB, Store<T>>(g, StoreArgs{f, part, ld, step}, parts, s);
+  product<E, kPlanes<T>, TA, TB, Store<T, PLAIN>>(g, StoreArgs{f, part, ld, step}, parts, s);
   const int64_t quads = g.M * ((g.N + 3) / 4);
-  hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, s,
+  hipLaunchKernelGGL((join_kernel<T, PLAIN>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, s,
                      g.M, g.N, parts, part, ld, step, f);
 }
 

@@ -21,6 +21,7 @@
 namespace og::epi::grad {
 
 constexpr int kRows = 64, kCols = 256;  // of a block of a sweep: 4 waves, 4 columns a lane
+constexpr int kAtOnce = 4;              // rows of a wave whose loads are in flight together
 
 struct Matrix {
   const void *x;
@@ -38,16 +39,24 @@ struct Matrix {
   int blocks;             // of a launch
 };
 
-template <class T>
-__device__ __forceinline__ f32x4 value(const Matrix &a, int64_t i, int c) {
+// Four values of N rows from i on, 4 apart; zero past the matrix.  All loads come first.
+template <class T, int N>
+__device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, f32x4 (&v)[N]) {
   const int left = a.cols - c;
-  f32x4 v = load4(static_cast<const T *>(a.x) + i * a.ldx + c, left, a.vec_x);
-  if (a.pre) {
-    const f32x4 p = load4(static_cast<const T *>(a.pre) + i * a.ldp + c, left, a.vec_p);
+  f32x4 p[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = e < left ? v[e] * slope_of(p[e], a.act) : 0.0f;
+  for (int q = 0; q < N; ++q) {
+    const bool in = i + 4 * q < a.rows;
+    v[q] = load4(static_cast<const T *>(a.x) + (i + 4 * q) * a.ldx + c, in ? left : 0, a.vec_x);
+    if (a.pre) p[q] = load4(static_cast<const T *>(a.pre) + (i + 4 * q) * a.ldp + c, in ? left : 0, a.vec_p);
   }
-  return v;
+  if (!a.pre) return;
+  with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q][e] = e < left ? v[q][e] * slope_of<act()>(p[q][e]) : 0.0f;
+  });
 }
 
 // One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
@@ -68,41 +77,51 @@ __global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix
 #pragma unroll
       for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
-    for (int r = wave; r < kRows; r += 4) {
-      const int64_t i = i0 + r;
-      if (i >= a.rows) break;
-      const f32x4 v = value<T>(a, i, c);
-      if (a.out) {
-        const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
-        store_planes(a.out + i * a.width * 2, c, v, powers);
+    for (int r = wave; r < kRows; r += 4 * kAtOnce) {
+      f32x4 v[kAtOnce];
+      if (i0 + r >= a.rows) break;
+      values<T>(a, i0 + r, c, v);
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int64_t i = i0 + r + 4 * q;
+        if (i >= a.rows) break;
+        if (a.out) {
+          const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
+          store_planes(a.out + i * a.width * 2, c, v[q], powers);
+        }
+        if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v[q], cpower);
       }
-      if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v, cpower);
     }
   } else {
     f32x4 sum = {0, 0, 0, 0}, top = {0, 0, 0, 0};
-    for (int r = wave; r < kRows; r += 4) {
-      const int64_t i = i0 + r;
-      if (i >= a.rows) break;
-      const f32x4 v = c < a.width ? value<T>(a, i, c) : f32x4{0, 0, 0, 0};
-      f32x4 size;
+    for (int r = wave; r < kRows; r += 4 * kAtOnce) {
+      f32x4 v[kAtOnce];
+      if (i0 + r >= a.rows) break;
+      values<T>(a, i0 + r, c, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum[e] += v[e];
-        size[e] = __builtin_isfinite(v[e]) ? fabsf(v[e]) : 0.0f;
-        top[e] = fmaxf(top[e], size[e]);
-      }
-      if constexpr (kPlanes<T> == 2) {
-        if (a.rtop) {
-          const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
-          if (lane == 0 && most > 0) atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
-        }
-      } else if (a.out && c < a.width) {
-        f32x4 h = v;
-        if (a.halve) {
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int64_t i = i0 + r + 4 * q;
+        if (i >= a.rows) break;
+        f32x4 size;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] *= 0.5f;
+        for (int e = 0; e < 4; ++e) {
+          sum[e] += v[q][e];
+          size[e] = __builtin_isfinite(v[q][e]) ? fabsf(v[q][e]) : 0.0f;
+          top[e] = fmaxf(top[e], size[e]);
         }
-        store4(reinterpret_cast<T *>(a.out) + i * a.width + c, h, a.width - c, true);
+        if constexpr (kPlanes<T> == 2) {
+          if (a.rtop) {
+            const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
+            if (lane == 0 && most > 0)
+              atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
+          }
+        } else if (a.out && c < a.width) {
+          if (a.halve) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[q][e] *= 0.5f;
+          }
+          store4(reinterpret_cast<T *>(a.out) + i * a.width + c, v[q], a.width - c, true);
+        }
       }
     }
     if (!a.sums && !a.ctop) return;
@@ -188,8 +207,15 @@ int sweep_blocks(const Matrix &a) {
   return (int)((int64_t)((a.rows + kRows - 1) / kRows) * ((a.width + kCols - 1) / kCols));
 }
 
-Finish output(void *out, int64_t ld, int vec, const float *mtop, const float *ntop, int up) {
-  return Finish{mtop, ntop, up, nullptr, OG_ACT_NONE, nullptr, 0, nullptr, 0, out, ld, 0, 0, 0, vec};
+template <class T>
+Finish output(void *out, int64_t ld, const float *mtop, const float *ntop, int up) {
+  Finish f{};
+  f.mtop = mtop;
+  f.ntop = ntop;
+  f.up = up;
+  f.out = out;
+  f.ldo = ld;
+  return set_accesses<T>(f);
 }
 
 template <class T>
@@ -272,13 +298,11 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   Args g{};
   if (c.da && m > 0 && k > 0) {
     g.a = rows, g.b = W, g.M = m, g.N = k, g.K = n;
-    run_product<T, false, true>(
-        g, output(c.da, c.ldda, whole(static_cast<T *>(c.da), c.ldda), rtop, wtop, up), c.ws + p.parts_at, s);
+    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop, up), c.ws + p.parts_at, s);
   }
   if (c.dw && n > 0 && k > 0) {
     g.a = cols, g.b = A, g.M = n, g.N = k, g.K = m;
-    run_product<T, true, true>(
-        g, output(c.dw, c.lddw, whole(static_cast<T *>(c.dw), c.lddw), ctop, atop, up), c.ws + p.parts_at, s);
+    run_product<T, true, true, true>(g, output<T>(c.dw, c.lddw, ctop, atop, up), c.ws + p.parts_at, s);
   }
 }
 

@@ -120,8 +120,9 @@ def _epi_grad(L, m=3, n=5, k=8, dC=P, lddc=5, A=P, lda=8, W=P, ldw=8, type=0, Pr
 
 
 SHARED = [dict(type=3), dict(type=-1), dict(act=5), dict(act=-1), dict(m=-1), dict(n=-1), dict(k=-1), dict(lda=7),
-          dict(ldw=7), dict(ldp=4), dict(A=NULL), dict(W=NULL), dict(ws=ODD), dict(ws=NULL, m=500, n=500, k=500, lda=500,
-          ldw=500, ldr=500, ldp=500, ldc=500, lddc=500, ldda=500, lddw=500)]
+          dict(ldw=7), dict(ldp=4), dict(A=NULL), dict(W=NULL), dict(ws=ODD),
+          dict(ws=NULL, m=900, n=900, k=900, **dict.fromkeys(("lda", "ldw", "ldr", "ldp", "ldc", "lddc", "ldda", "lddw"),
+                                                             900))]
 
 
 def _given(call, kw):
@@ -174,7 +175,7 @@ def test_epi_workspace(L):
         assert f(-1, 5, 8, 0) == og.OG_ERR_INVALID_ARG
         assert f(1 << 25, 5, 8, 0) == og.OG_ERR_TOO_LARGE
     for type in (0, 1, 2):
-        m, n, k = 300, 200, 128
+        m, n, k = 1300, 800, 512
         need = L.og_gemm_nt_epi_grad_workspace(m, n, k, type)
         strides = dict(lddc=n, lda=k, ldw=k, ldp=n, ldda=k, lddw=k)
         assert _epi_grad(L, m, n, k, type=type, bytes=need - 1, **strides) == og.OG_ERR_INVALID_ARG
