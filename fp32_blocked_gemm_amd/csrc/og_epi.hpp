@@ -407,10 +407,18 @@ struct Room {
   }
 };
 
+// The largest of the wave's (non-negative) values, in every lane.
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+#define OG_ROR(N)                                                                                  \
+  v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v),      \
+                                                                  0x120 + N, 0xf, 0xf, true)))
+  OG_ROR(8);
+  OG_ROR(4);
+  OG_ROR(2);
+  OG_ROR(1);
+#undef OG_ROR
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // Rows of 16-bit values, zero from cols to ld (a multiple of 8).

@@ -20,8 +20,9 @@
 
 namespace og::epi::grad {
 
-constexpr int kRows = 64, kCols = 256;  // of a block of a sweep: 4 waves, 4 columns a lane
-constexpr int kAtOnce = 4;              // rows of a wave whose loads are in flight together
+// A block of a sweep: 16 waves, 4 columns a lane, 4 rows a wave whose loads are in flight
+// together (4 waves of 16 rows in turn: @SW@).
+constexpr int kWaves = 16, kAtOnce = 4, kRows = kWaves * kAtOnce, kCols = 256;
 
 struct Matrix {
   const void *x;
@@ -39,16 +40,16 @@ struct Matrix {
   int blocks;             // of a launch
 };
 
-// Four values of N rows from i on, 4 apart; zero past the matrix.  All loads come first.
+// Four values of N rows from i on, kWaves apart; zero past the matrix.  All loads come first.
 template <class T, int N>
 __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, f32x4 (&v)[N]) {
   const int left = a.cols - c;
   f32x4 p[N];
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    const bool in = i + 4 * q < a.rows;
-    v[q] = load4(static_cast<const T *>(a.x) + (i + 4 * q) * a.ldx + c, in ? left : 0, a.vec_x);
-    if (a.pre) p[q] = load4(static_cast<const T *>(a.pre) + (i + 4 * q) * a.ldp + c, in ? left : 0, a.vec_p);
+    const bool in = i + kWaves * q < a.rows;
+    v[q] = load4(static_cast<const T *>(a.x) + (i + kWaves * q) * a.ldx + c, in ? left : 0, a.vec_x);
+    if (a.pre) p[q] = load4(static_cast<const T *>(a.pre) + (i + kWaves * q) * a.ldp + c, in ? left : 0, a.vec_p);
   }
   if (!a.pre) return;
   with_act(a.act, [&](auto act) __attribute__((always_inline)) {
@@ -62,8 +63,8 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, f32x4 
 // One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
 // and largest magnitudes.
 template <class T, bool LAYOUT>
-__global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
-  __shared__ f32x4 of_waves[2][4][64];
+__global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
+  __shared__ f32x4 of_waves[2][kWaves][64];
   int block = blockIdx.x;
   const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
   block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
@@ -77,13 +78,12 @@ __global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix
 #pragma unroll
       for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
-    for (int r = wave; r < kRows; r += 4 * kAtOnce) {
+    {
       f32x4 v[kAtOnce];
-      if (i0 + r >= a.rows) break;
-      values<T>(a, i0 + r, c, v);
+      values<T>(a, i0 + wave, c, v);
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
-        const int64_t i = i0 + r + 4 * q;
+        const int64_t i = i0 + wave + kWaves * q;
         if (i >= a.rows) break;
         if (a.out) {
           const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
@@ -94,13 +94,12 @@ __global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix
     }
   } else {
     f32x4 sum = {0, 0, 0, 0}, top = {0, 0, 0, 0};
-    for (int r = wave; r < kRows; r += 4 * kAtOnce) {
+    {
       f32x4 v[kAtOnce];
-      if (i0 + r >= a.rows) break;
-      values<T>(a, i0 + r, c, v);
+      values<T>(a, i0 + wave, c, v);
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
-        const int64_t i = i0 + r + 4 * q;
+        const int64_t i = i0 + wave + kWaves * q;
         if (i >= a.rows) break;
         f32x4 size;
 #pragma unroll
@@ -130,7 +129,7 @@ __global__ __launch_bounds__(256) void sweep_kernel(Matrix m0, Matrix m1, Matrix
     __syncthreads();
     if (wave || c >= a.width) return;
 #pragma unroll
-    for (int w = 1; w < 4; ++w)
+    for (int w = 1; w < kWaves; ++w)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sum[e] += of_waves[0][w][lane][e];
@@ -270,9 +269,9 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     const int blocks = dp.blocks + ma.blocks + mw.blocks;
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
                        tops, total);
-    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(256), 0, s, dp, ma, mw);
+    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
     if (blocks > 0 && (c.da || c.dw))
-      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(256), 0, s, dp, ma, mw);
+      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
     rows = Operand{at(p.p_at), 2 * p.np, 0};
     cols = Operand{at(p.pc_at), 2 * p.np, 0};
     A = Operand{at(p.a_at), 2 * p.kp, 0};
@@ -286,7 +285,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     if (dp.out || dp.sums) {
       dp.blocks = sweep_blocks(dp);
       if (dp.blocks > 0)
-        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(256), 0, s, dp, Matrix{}, Matrix{});
+        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
     }
     rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s);
