@@ -20,9 +20,14 @@
 
 namespace og::epi::grad {
 
-// A block of a sweep: 16 waves, 4 columns a lane, 4 rows a wave whose loads are in flight
-// together (4 waves of 16 rows in turn: @SW@).
-constexpr int kWaves = 16, kAtOnce = 4, kRows = kWaves * kAtOnce, kCols = 256;
+// A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
+// (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
+// dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).
+constexpr int kWaves = 8, kRows = 4 * kWaves;
+template <class T>
+constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
+template <class T>
+constexpr int kCols = 64 * kPer<T>;  // of a block
 
 struct Matrix {
   const void *x;
@@ -40,23 +45,36 @@ struct Matrix {
   int blocks;             // of a launch
 };
 
-// Four values of N rows from i on, kWaves apart; zero past the matrix.  All loads come first.
-template <class T, int N>
-__device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, f32x4 (&v)[N]) {
-  const int left = a.cols - c;
-  f32x4 p[N];
+// A lane's columns as fp32.
+template <class T>
+struct Lane {
+  f32x4 v[kPer<T> / 4];
+};
+template <class T>
+__device__ __forceinline__ void load_lane(const T *p, int left, bool vec, Lane<T> &lane) {
+  if (vec && left >= kPer<T>) {
+    typedef T V __attribute__((ext_vector_type(kPer<T>)));
+    const V w = *reinterpret_cast<const V *>(p);
 #pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const bool in = i + kWaves * q < a.rows;
-    v[q] = load4(static_cast<const T *>(a.x) + (i + kWaves * q) * a.ldx + c, in ? left : 0, a.vec_x);
-    if (a.pre) p[q] = load4(static_cast<const T *>(a.pre) + (i + kWaves * q) * a.ldp + c, in ? left : 0, a.vec_p);
+    for (int e = 0; e < kPer<T>; ++e) lane.v[e / 4][e % 4] = (float)w[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPer<T>; ++e) lane.v[e / 4][e % 4] = e < left ? (float)p[e] : 0.0f;
   }
+}
+
+// A lane's values of row i, zero past the matrix.
+template <class T>
+__device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, Lane<T> &v) {
+  const int left = a.cols - c;
+  load_lane<T>(static_cast<const T *>(a.x) + i * a.ldx + c, left, a.vec_x, v);
   if (!a.pre) return;
+  Lane<T> p;
+  load_lane<T>(static_cast<const T *>(a.pre) + i * a.ldp + c, left, a.vec_p, p);
   with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < N; ++q)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[q][e] = e < left ? v[q][e] * slope_of<act()>(p[q][e]) : 0.0f;
+    for (int e = 0; e < kPer<T>; ++e)
+      v.v[e / 4][e % 4] = e < left ? v.v[e / 4][e % 4] * slope_of<act()>(p.v[e / 4][e % 4]) : 0.0f;
   });
 }
 
@@ -64,13 +82,15 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, f32x4 
 // and largest magnitudes.
 template <class T, bool LAYOUT>
 __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
-  __shared__ f32x4 of_waves[2][kWaves][64];
+  constexpr int H = kPer<T> / 4;
+  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves][64];
   int block = blockIdx.x;
   const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
   block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
-  const int across = (a.width + kCols - 1) / kCols, rb = block / across;
+  const int across = (a.width + kCols<T> - 1) / kCols<T>, rb = block / across;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (block - rb * across) * kCols + 4 * lane, i0 = rb * kRows;
+  const int c = (block - rb * across) * kCols<T> + kPer<T> * lane;
+  const int64_t i0 = (int64_t)rb * kRows + wave, end = min((int64_t)(rb + 1) * kRows, (int64_t)a.rows);
   if constexpr (LAYOUT) {
     if (c >= a.width) return;
     int cpower[4] = {0, 0, 0, 0};
@@ -78,68 +98,69 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
 #pragma unroll
       for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
-    {
-      f32x4 v[kAtOnce];
-      values<T>(a, i0 + wave, c, v);
-#pragma unroll
-      for (int q = 0; q < kAtOnce; ++q) {
-        const int64_t i = i0 + wave + kWaves * q;
-        if (i >= a.rows) break;
-        if (a.out) {
-          const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
-          store_planes(a.out + i * a.width * 2, c, v[q], powers);
-        }
-        if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v[q], cpower);
+    for (int64_t i = i0; i < end; i += kWaves) {
+      Lane<T> v;
+      values<T>(a, i, c, v);
+      if (a.out) {
+        const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
+        store_planes(a.out + i * a.width * 2, c, v.v[0], powers);
       }
+      if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v.v[0], cpower);
     }
   } else {
-    f32x4 sum = {0, 0, 0, 0}, top = {0, 0, 0, 0};
-    {
-      f32x4 v[kAtOnce];
-      values<T>(a, i0 + wave, c, v);
+    f32x4 sum[H], top[H];
 #pragma unroll
-      for (int q = 0; q < kAtOnce; ++q) {
-        const int64_t i = i0 + wave + kWaves * q;
-        if (i >= a.rows) break;
+    for (int h = 0; h < H; ++h) sum[h] = top[h] = f32x4{0, 0, 0, 0};
+    for (int64_t i = i0; i < end; i += kWaves) {
+      Lane<T> v;
+      values<T>(a, i, c, v);
+#pragma unroll
+      for (int h = 0; h < H; ++h) sum[h] += v.v[h];
+      if constexpr (kPlanes<T> == 2) {
         f32x4 size;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sum[e] += v[q][e];
-          size[e] = __builtin_isfinite(v[q][e]) ? fabsf(v[q][e]) : 0.0f;
-          top[e] = fmaxf(top[e], size[e]);
+          const float x = v.v[0][e];
+          size[e] = __builtin_isfinite(x) ? fabsf(x) : 0.0f;
+          top[0][e] = fmaxf(top[0][e], size[e]);
         }
-        if constexpr (kPlanes<T> == 2) {
-          if (a.rtop) {
-            const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
-            if (lane == 0 && most > 0)
-              atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
-          }
-        } else if (a.out && c < a.width) {
-          if (a.halve) {
+        if (a.rtop) {
+          const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
+          if (lane == 0 && most > 0)
+            atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
+        }
+      } else if (a.out && c < a.width) {
+        typedef T V __attribute__((ext_vector_type(kPer<T>)));
+        V w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[q][e] *= 0.5f;
-          }
-          store4(reinterpret_cast<T *>(a.out) + i * a.width + c, v[q], a.width - c, true);
-        }
+        for (int e = 0; e < kPer<T>; ++e) w[e] = (T)(a.halve ? 0.5f * v.v[e / 4][e % 4] : v.v[e / 4][e % 4]);
+        *reinterpret_cast<V *>(reinterpret_cast<T *>(a.out) + i * a.width + c) = w;
       }
     }
     if (!a.sums && !a.ctop) return;
-    of_waves[0][wave][lane] = sum;
-    of_waves[1][wave][lane] = top;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      of_waves[h][wave][lane] = sum[h];
+      if (kPlanes<T> == 2) of_waves[H + h][wave][lane] = top[h];
+    }
     __syncthreads();
     if (wave || c >= a.width) return;
+    for (int w = 1; w < kWaves; ++w) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w)
+      for (int h = 0; h < H; ++h) sum[h] += of_waves[h][w][lane];
+      if constexpr (kPlanes<T> == 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum[e] += of_waves[0][w][lane][e];
-        top[e] = fmaxf(top[e], of_waves[1][w][lane][e]);
+        for (int e = 0; e < 4; ++e) top[0][e] = fmaxf(top[0][e], of_waves[H][w][lane][e]);
       }
-    if (a.sums) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c) = sum;
-    if (a.ctop) {
+    }
+    if (a.sums) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c + 4 * h) = sum[h];
+    }
+    if (kPlanes<T> == 2 && a.ctop) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float most = top[e];  // (a bit cast of a vector's element takes the first one's bits)
+        const float most = top[0][e];  // (a bit cast of a vector's element takes the first one's bits)
         if (c + e < a.cols && most > 0)
           atomicMax(reinterpret_cast<uint32_t *>(a.ctop + c + e), __builtin_bit_cast(uint32_t, most));
       }
@@ -202,8 +223,14 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int type) {
   return type == OG_F32 ? plan<float>(m, n, k) : type == OG_BF16 ? plan<__bf16>(m, n, k) : plan<_Float16>(m, n, k);
 }
 
+template <class T>
 int sweep_blocks(const Matrix &a) {
-  return (int)((int64_t)((a.rows + kRows - 1) / kRows) * ((a.width + kCols - 1) / kCols));
+  return (int)((int64_t)((a.rows + kRows - 1) / kRows) * ((a.width + kCols<T> - 1) / kCols<T>));
+}
+// Whether a lane's columns are one aligned load.
+template <class T>
+int lanes_whole(const void *p, int64_t ld) {
+  return ld % kPer<T> == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
 template <class T>
@@ -232,8 +259,8 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   dp.rows = m;
   dp.cols = n;
   dp.width = (int)p.np;
-  dp.vec_x = whole(static_cast<const T *>(c.dc), c.lddc);
-  dp.vec_p = whole(static_cast<const T *>(c.pre), c.ldp);
+  dp.vec_x = lanes_whole<T>(c.dc, c.lddc);
+  dp.vec_p = lanes_whole<T>(c.pre, c.ldp);
   dp.sums = c.dbias ? reinterpret_cast<float *>(c.ws + p.sums_at) : nullptr;
   Operand rows, cols, A, W;  // dP by rows and by columns, A, W
   const float *rtop = nullptr, *ctop = nullptr, *atop = nullptr, *wtop = nullptr;
@@ -249,7 +276,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       a.rows = (int)count;
       a.cols = k;
       a.width = (int)p.kp;
-      a.vec_x = whole(static_cast<const T *>(x), ld);
+      a.vec_x = lanes_whole<T>(x, ld);
       a.ctop = top;
       a.out_c = out;
       return a;
@@ -265,7 +292,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       dp.out_c = at(p.pc_at);
       ma = of(c.a, c.lda, m, ta, at(p.a_at));
     }
-    for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks(*x);
+    for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks<T>(*x);
     const int blocks = dp.blocks + ma.blocks + mw.blocks;
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
                        tops, total);
@@ -283,7 +310,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     up = dp.halve;
     dp.out = place || !(c.da || c.dw) ? nullptr : at(p.p_at);
     if (dp.out || dp.sums) {
-      dp.blocks = sweep_blocks(dp);
+      dp.blocks = sweep_blocks<T>(dp);
       if (dp.blocks > 0)
         hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
     }
