@@ -215,11 +215,12 @@ def _ld(t) -> int:
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if cols > 1 and one != 1:
         raise ValueError("columns must be contiguous (stride(1) == 1)")
     if rows <= 1 or cols == 0:
         return max(1, cols)
-    return t.stride(0)
+    return ld
 
 
 def _check_f32_cuda(*ts):
@@ -344,24 +345,24 @@ def _type(t, allowed=(F32, BF16)) -> int:
 
 
 def _one_device(*ts):
-    dev = ts[0].device
+    at = ts[0].get_device()
     for t in ts:
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors")
-        if t.device != dev:
+        if t.get_device() != at:
             raise ValueError("tensors must be on one device")
-    return dev
+    return ts[0].device
 
 
 def _run(dev, call, *args):
     """Calls the library on the current stream of `dev` (which it makes the current device
     where it is not)."""
     torch = _torch()
-    if torch.cuda.current_device() != dev.index:
+    index = dev.index
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(dev):
             return _run(dev, call, *args)
-    L = lib()
-    L.og_set_stream(torch._C._cuda_getCurrentRawStream(dev.index))
+    lib().og_set_stream(torch._C._cuda_getCurrentRawStream(index))
     status = call(*args)
     if status != OG_OK:
         _check(status)
@@ -454,7 +455,7 @@ def newton_schulz(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out=No
 
 
 def _vector(t, n, dtype, what):
-    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous tensor of {n} {dtype} values")
 
 
@@ -544,7 +545,7 @@ def _product_shapes(A, B):
 
 
 def _matrix(t, rows, cols, dtype, what):
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or t.dtype != dtype:
+    if t.shape != (rows, cols) or t.dtype != dtype:
         raise ValueError(f"{what} must be [{rows}, {cols}] of {dtype}")
 
 
@@ -640,26 +641,31 @@ def _run_of(t):
 def _grads(grads, out):
     """The table of og_grad_norm's tensors, and their device."""
     torch = _torch()
-    code = _type(grads[0], (F32, BF16, F16))
+    _type(grads[0], (F32, BF16, F16))
     dev = _one_device(grads[0])
-    table = array.array("q")
+    at, code_of, table = dev.index, _TYPES.get, []
     for x, y in zip(grads, grads if out is None else out):
-        code = _TYPES.get(x.dtype)
+        dtype = x.dtype
+        code = code_of(dtype)
         if code is None:
             _type(x, (F32, BF16, F16))
-        if x.device != dev or y.device != dev:
+        if x.get_device() != at or (y is not x and y.get_device() != at):
             raise ValueError("tensors must be on one device")
-        if y is x or y.stride() == x.stride() or (x.is_contiguous() and y.is_contiguous()):
+        if y is not x and (not y.is_same_size(x) or y.dtype != dtype):
+            raise ValueError("an output must have its gradient's shape and type")
+        if x.is_contiguous() and (y is x or y.is_contiguous()):
+            n = x.numel()
+            table += (x.data_ptr(), y.data_ptr(), 1, n, n, n, code)
+            continue
+        if y is x or y.stride() == x.stride():
             rows, cols, ldx = _run_of(x)
             ldy = ldx
-        elif x.dim() == 2 and y.dim() == 2:
+        elif x.dim() == 2:
             rows, cols, ldx, ldy = *x.shape, _ld(x), _ld(y)
         else:
             raise ValueError("an output must have its gradient's layout")
-        if y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("an output must have its gradient's shape and type")
-        table.extend((x.data_ptr(), y.data_ptr(), rows, cols, ldx, ldy, code))
-    return table, dev
+        table += (x.data_ptr(), y.data_ptr(), rows, cols, ldx, ldy, code)
+    return array.array("q", table), dev
 
 
 def grad_norm(grads, workspace=None):
@@ -731,10 +737,12 @@ def logit_penalties(logits, tokens=None, lengths=None, prompt_lengths=None, repe
     for what, x, dtype in (("lengths", lengths, torch.int64), ("prompt_lengths", prompt_lengths, torch.int64),
                            ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
                            ("presence", presence, torch.float32)):
-        if x is not None:
-            _vector(x, n, dtype, what)
-            given.append(x)
-        vectors.append(None if x is None else x.data_ptr())
+        if x is None:
+            vectors.append(None)
+            continue
+        _vector(x, n, dtype, what)
+        given.append(x)
+        vectors.append(x.data_ptr())
     rows = []
     for what, x, dtype, cols in (("bias", bias, torch.float32, v), ("mask", mask, torch.int32, (v + 31) // 32)):
         if x is None:

@@ -23,9 +23,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr int kLoads = 4;       // of a thread, in flight together
 constexpr int kBlocks = 1024;   // and partial sums
 constexpr int kTensors = 64;    // of a launch: the arguments are at most 4 KB
-constexpr int kChunk = 16384;   // bytes
+constexpr int kChunk = 16 * kThreads * kLoads;   // bytes
 
 struct Tensor {
   const void *x;
@@ -79,11 +80,11 @@ __device__ __forceinline__ double squares(const Tensor &t, int c) {
   double sum[4] = {0, 0, 0, 0};
   if ((t.type & kWhole) && end - from == V::kPer) {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(x + from) + threadIdx.x;
-    u32x4 w[4];
+    u32x4 w[kLoads];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = p[q * kThreads];
+    for (int q = 0; q < kLoads; ++q) w[q] = p[q * kThreads];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kLoads; ++q) {
       float v[V::kOne];
       V::load(w[q], v);
 #pragma unroll
@@ -117,11 +118,11 @@ __device__ __forceinline__ void scaled(const Tensor &t, int c, Factor by) {
   if ((t.type & kWhole) && end - from == V::kPer) {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(x + from) + threadIdx.x;
     u32x4 *to = reinterpret_cast<u32x4 *>(y + from) + threadIdx.x;
-    u32x4 w[4];
+    u32x4 w[kLoads];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = p[q * kThreads];
+    for (int q = 0; q < kLoads; ++q) w[q] = p[q * kThreads];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kLoads; ++q) {
       float v[V::kOne];
       V::load(w[q], v);
 #pragma unroll

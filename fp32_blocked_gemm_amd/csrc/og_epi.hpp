@@ -348,12 +348,71 @@ static __global__ __launch_bounds__(256) void join_kernel(int M, int N, int part
   }
 }
 
-// Parts of k: as many as take the least time by the tiles' measured stages, where the parts'
-// sums cost a launch and their bytes, written and read.
+// A tile and what it costs (as og_tile.hpp's Choice): nanoseconds of a stage alone, as one of 256
+// blocks and as a share, and of a round of blocks besides its stages (start and epilogue).
+template <class S_, int ALONE, int ONE, int SHARE, int ROUND>
+struct Cost {
+  using S = S_;
+  static double time(bool, int64_t M, int64_t N, int64_t K, int64_t batch) {
+    const int64_t n = (M + S::BM - 1) / S::BM * ((N + S::BN - 1) / S::BN) * batch;
+    const double stages = (double)((K + depth(S::P) - 1) / depth(S::P));
+    if (n <= 256) return stages * (ALONE + (ONE - ALONE) * (n / 256.0)) + ROUND;
+    return (double)((n + 255) / 256) * stages * SHARE + (double)((n + 256 * S::BLOCKS - 1) / (256 * S::BLOCKS)) * ROUND;
+  }
+};
+
+// The tiles by planes and by whether both operands are transposed (dW).  Beside og_tile.hpp's squares
+// are oblong ones, which fill the compute units where squares leave a part of a round (512 x 11008
+// x 4096 fp32: 174 tiles of 192 x 192 168 us, 232 of 128 x 192 122).  Times measured on stages of k 1024
+// to 3072; of 1800 seeded products the listed tiles' predicted time is 1.01 times that of the best of 15
+// shapes in the mean.
+template <class E, int P, bool TT>
+struct EpiTiles {
+  using type = Choices<Cost<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 1010, 1505, 1462, 15000>,
+                       Cost<Shape<E, 1, 192, 256, 2, 4, 2, 1>, 753, 1140, 1160, 11000>,
+                       Cost<Shape<E, 1, 192, 192, 2, 4, 3, 1>, 620, 898, 887, 9500>,
+                       Cost<Shape<E, 1, 128, 192, 2, 4, 3, 1>, 455, 650, 720, 7500>,
+                       Cost<Shape<E, 1, 128, 128, 2, 2, 2, 2>, 386, 780, 442, 7000>,
+                       Cost<Shape<E, 1, 128, 64, 4, 2, 4, 1>, 253, 348, 337, 6000>,
+                       Cost<Shape<E, 1, 64, 64, 2, 2, 4, 2>, 187, 252, 193, 5000>>;
+};
+template <class E>
+struct EpiTiles<E, 1, true> {
+  using type = Choices<Cost<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 999, 1569, 1540, 13000>,
+                       Cost<Shape<E, 1, 192, 256, 2, 4, 2, 1>, 845, 1196, 1202, 11000>,
+                       Cost<Shape<E, 1, 192, 192, 2, 4, 3, 1>, 702, 982, 1072, 9000>,
+                       Cost<Shape<E, 1, 128, 192, 2, 4, 3, 1>, 549, 693, 831, 7000>,
+                       Cost<Shape<E, 1, 128, 128, 2, 2, 2, 2>, 471, 879, 466, 8000>,
+                       Cost<Shape<E, 1, 128, 64, 4, 2, 4, 1>, 290, 372, 343, 6000>,
+                       Cost<Shape<E, 1, 64, 64, 2, 2, 4, 2>, 262, 276, 180, 5000>>;
+};
+template <class E>
+struct EpiTiles<E, 2, false> {
+  using type = Choices<Cost<Shape<E, 2, 256, 256, 2, 4, 2, 1>, 1412, 2400, 2050, 16000>,
+                       Cost<Shape<E, 2, 192, 256, 2, 4, 2, 1>, 1090, 1600, 1600, 11500>,
+                       Cost<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 861, 1223, 1213, 11000>,
+                       Cost<Shape<E, 2, 128, 192, 2, 4, 3, 1>, 610, 861, 856, 9500>,
+                       Cost<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 410, 727, 598, 8000>,
+                       Cost<Shape<E, 2, 128, 64, 4, 2, 4, 1>, 343, 404, 402, 5500>,
+                       Cost<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 214, 273, 206, 6000>>;
+};
+template <class E>
+struct EpiTiles<E, 2, true> {
+  // (256 x 256 needs a register more than there are)
+  using type = Choices<Cost<Shape<E, 2, 192, 256, 2, 4, 2, 1>, 1171, 1604, 1625, 12000>,
+                       Cost<Shape<E, 2, 192, 192, 2, 4, 3, 1>, 980, 1327, 1294, 11000>,
+                       Cost<Shape<E, 2, 128, 192, 2, 4, 3, 1>, 721, 954, 990, 9000>,
+                       Cost<Shape<E, 2, 128, 128, 2, 4, 2, 2>, 474, 728, 613, 8000>,
+                       Cost<Shape<E, 2, 128, 64, 4, 2, 4, 1>, 375, 477, 461, 6000>,
+                       Cost<Shape<E, 2, 64, 64, 2, 2, 4, 2>, 271, 327, 220, 6000>>;
+};
+
+// Parts of k: as many as take the least time, where the parts' sums cost a launch and their
+// bytes, written and read.
 constexpr int kMostParts = 16;
 template <class T, bool TT>
 int parts_of(int64_t M, int64_t N, int64_t K) {
-  using C = typename Tiles<Element<T>, kPlanes<T>, TT>::type;
+  using C = typename EpiTiles<Element<T>, kPlanes<T>, TT>::type;
   double best = std::numeric_limits<double>::infinity();
   int parts = 1;
   for (int p = 1; p <= kMostParts && (p == 1 || K / p >= 256); p += p < 4 ? 1 : p) {
@@ -377,19 +436,20 @@ int64_t parts_bytes(int64_t M, int64_t N, int64_t K) {
 
 template <class T, bool TA, bool TB, bool PLAIN>
 void run_product(Args g, const Finish &f, char *ws, hipStream_t s) {
-  using E = Element<T>;
+  using C = typename EpiTiles<Element<T>, kPlanes<T>, TA && TB>::type;
   const int parts = parts_of<T, TA && TB>(g.M, g.N, g.K);
-  if (parts == 1) {
-    product<E, kPlanes<T>, TA, TB, Store<T, PLAIN>>(g, StoreArgs{f, nullptr, 0, 0}, 1, s);
-    return;
+  StoreArgs e{f, nullptr, 0, 0};
+  if (parts > 1) {
+    e.part = reinterpret_cast<float *>(ws);
+    e.ld = round_up(g.N, 4);
+    e.step = g.M * e.ld;
+    g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
   }
-  float *part = reinterpret_cast<float *>(ws);
-  const int64_t ld = round_up(g.N, 4), step = g.M * ld;
-  g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
-  product<E, kPlanes<T>, TA, TB, Store<T, PLAIN>>(g, StoreArgs{f, part, ld, step}, parts, s);
+  product_of<TA, TB, Store<T, PLAIN>>(C(), least(C(), false, g, parts), g, e, parts, s);
+  if (parts == 1) return;
   const int64_t quads = g.M * ((g.N + 3) / 4);
-  hipLaunchKernelGGL((join_kernel<T, PLAIN>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, s,
-                     g.M, g.N, parts, part, ld, step, f);
+  hipLaunchKernelGGL((join_kernel<T, PLAIN>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0,
+                     s, g.M, g.N, parts, e.part, e.ld, e.step, f);
 }
 
 // Whether the tile product can read a 16-bit matrix where it lies.

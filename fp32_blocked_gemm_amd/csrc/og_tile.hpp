@@ -327,8 +327,9 @@ __global__ __launch_bounds__(S::NW * 64, S::kWavesPerSimd) void tile_kernel(Args
   // NST ahead: kRate a row, from right after the barrier on.
   constexpr int kAhead = P == 1 ? 2 : 1;
   constexpr int kPer = SA::kLoads + SB::kLoads;
-  constexpr int kRate = P == 1 ? kPer / 4 : (kPer + FM / 2 - 1) / (FM / 2);
+  constexpr int kRate = P == 1 ? (kPer < 4 ? 1 : kPer / 4) : (kPer + FM / 2 - 1) / (FM / 2);
   constexpr int kEarly = kPer < kRate * kAhead ? kPer : kRate * kAhead;
+  static_assert(kEarly + (P == 1 ? FM : FM - 1) * kRate >= kPer, "a stage's loads are all issued");
   auto issue = [&](int j) __attribute__((always_inline)) {
     if (j < SA::kLoads) sa.issue(j, to, rsa, left);
     else sb.issue(j - SA::kLoads, to + SA::kBytes, rsb, left);
