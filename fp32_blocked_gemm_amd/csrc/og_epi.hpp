@@ -481,6 +481,61 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 
+template <class T>
+struct Eight {
+  T v[8];
+};
+// Eight values of a row from k on, zero past its end.  FULL: it does not end here.
+template <class T, bool FULL>
+__device__ __forceinline__ Eight<T> load8(const T *row, int k, int K) {
+  Eight<T> t;
+  if (FULL || k + 8 <= K) {
+    __builtin_memcpy(&t, row + k, sizeof t);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t.v[e] = k + e < K ? row[k + e] : (T)0.0f;
+  }
+  return t;
+}
+
+// Fragments and their product: 16-bit values as they are; fp32 as three bf16 planes, cut, 24 bits
+// (h + m + l = the value; the products left out are 2^-24 of the whole and below), which need no
+// power of two.
+template <class T>
+struct Fragment {
+  s16x8 v;
+  Fragment() = default;
+  __device__ __forceinline__ explicit Fragment(const Eight<T> &x) { __builtin_memcpy(&v, &x, sizeof v); }
+  static __device__ __forceinline__ f32x4 product(const Fragment &x, const Fragment &w, f32x4 c) {
+    return mfma<T>(x.v, w.v, c);
+  }
+};
+template <>
+struct Fragment<float> {
+  s16x8 p[3];
+  Fragment() = default;
+  __device__ __forceinline__ explicit Fragment(const Eight<float> &x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // (a NaN is made quiet first: its highest mantissa bit then stays)
+      float r = __builtin_canonicalizef(x.v[e]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const uint32_t top = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
+        const float h = __builtin_bit_cast(float, top);
+        p[q][e] = (short)(top >> 16);
+        r = __builtin_isfinite(h) ? r - h : 0.0f;
+      }
+    }
+  }
+  static __device__ __forceinline__ f32x4 product(const Fragment &x, const Fragment &w, f32x4 c) {
+    constexpr int kX[6] = {2, 0, 1, 1, 0, 0}, kW[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c = mfma<__bf16>(x.p[kX[i]], w.p[kW[i]], c);
+    return c;
+  }
+};
+
 // Rows of 16-bit values, zero from cols to ld (a multiple of 8).
 static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int64_t ldx, int rows, int cols, uint16_t *out,
                                                    int ld) {

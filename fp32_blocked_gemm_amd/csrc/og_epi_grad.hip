@@ -23,7 +23,7 @@ namespace og::epi::grad {
 // A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
 // (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
 // dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).
-constexpr int kWaves = 8, kRows = 4 * kWaves;
+constexpr int kWaves = 8, kRows = 4 * kWaves;  // (rows of a block: Matrix::rows_per)
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
 template <class T>
@@ -42,6 +42,9 @@ struct Matrix {
   uint16_t *out_c;        // fp32: planes by the column's power
   float *rtop, *ctop;     // fp32: largest magnitudes (null: not wanted)
   float *sums;            // column sums of the block's rows, [row block][width] (null: not wanted)
+  int rows_per;           // rows of a block
+  float *plain;           // fp32 of few rows: the values (null: not wanted)
+  void *bias;             // a single row block: the column sums' own place (null: sums)
   int blocks;             // of a launch
 };
 
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
   const int across = (a.width + kCols<T> - 1) / kCols<T>, rb = block / across;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = (block - rb * across) * kCols<T> + kPer<T> * lane;
-  const int64_t i0 = (int64_t)rb * kRows + wave, end = min((int64_t)(rb + 1) * kRows, (int64_t)a.rows);
+  const int64_t i0 = (int64_t)rb * a.rows_per + wave, end = min((int64_t)(rb + 1) * a.rows_per, (int64_t)a.rows);
   if constexpr (LAYOUT) {
     if (c >= a.width) return;
     int cpower[4] = {0, 0, 0, 0};
@@ -117,6 +120,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
 #pragma unroll
       for (int h = 0; h < H; ++h) sum[h] += v.v[h];
       if constexpr (kPlanes<T> == 2) {
+        if (a.plain && c < a.width) *reinterpret_cast<f32x4 *>(a.plain + i * a.width + c) = v.v[0];
         f32x4 size;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
         *reinterpret_cast<V *>(reinterpret_cast<T *>(a.out) + i * a.width + c) = w;
       }
     }
-    if (!a.sums && !a.ctop) return;
+    if (!a.sums && !a.ctop && !a.bias) return;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       of_waves[h][wave][lane] = sum[h];
@@ -156,6 +160,10 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
     if (a.sums) {
 #pragma unroll
       for (int h = 0; h < H; ++h) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c + 4 * h) = sum[h];
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) store4(static_cast<T *>(a.bias) + c + 4 * h, sum[h], a.cols - c - 4 * h, false);
     }
     if (kPlanes<T> == 2 && a.ctop) {
 #pragma unroll
@@ -187,6 +195,140 @@ __global__ __launch_bounds__(1024) void bias_kernel(const float *sums, int block
   out[c] = (T)(float)sum;
 }
 
+// Few fp32 rows of dC and A (up to kFew): bound by the bytes of W, read, and of dW, written.  Both
+// products run from memory through registers as three bf16 planes, 24 bits, so that nothing of W is
+// scanned and laid out first (4096 x 4096, one row: 55 us in all, 100 by the tile products; 16-bit
+// types, whose W lies ready for those, gain nothing).  dP lies in fp32: the sweep's, or dC.
+constexpr int kFew = 32;
+template <class T>
+constexpr bool few_rows(int64_t m) {
+  return kPlanes<T> == 2 && m <= kFew;
+}
+
+struct FewRows {
+  int m, n, k;
+  const float *dp, *a, *w;
+  int64_t lddp, lda, ldw;
+  int vec;         // four columns of a row of W are one access
+  int steps;       // of 32 rows of W: of a part
+  Finish f;
+  float *part;     // dA in parts; null: whole
+  int64_t ld, step;
+};
+
+// dA: a block takes 64 columns of W and 16 MT rows of dP, its four waves share the part's rows of W.
+// A lane reads four columns of eight rows, 256 neighbouring bytes a row and instruction; its
+// column 4 i + e is the fragment e's column i, so that four fragments' sums are four neighbours.
+// (4096 x 4096: 20 us, 3.3 TB/s.)
+template <int MT>
+__global__ __launch_bounds__(256) void few_da_kernel(FewRows p) {
+  __shared__ __align__(16) float sums[4][16 * MT][68];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int c = blockIdx.x * 64 + 4 * i;
+  const int s0 = blockIdx.y * p.steps, s1 = min(s0 + p.steps, (p.n + 31) / 32);
+  f32x4 acc[4][MT];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[e][t] = f32x4{0, 0, 0, 0};
+  f32x4 next[8];
+  auto load = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int j = 32 * s + 8 * g + r;
+      next[r] = load4(p.w + (int64_t)j * p.ldw + c, j < p.n ? p.k - c : 0, p.vec);
+    }
+  };
+  if (s0 + wave < s1) load(s0 + wave);
+  for (int s = s0 + wave; s < s1; s += 4) {
+    f32x4 now[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) now[r] = next[r];
+    Eight<float> x[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int m = 16 * t + i;
+      x[t] = load8<float, false>(p.dp + (int64_t)min(m, p.m - 1) * p.lddp, 32 * s + 8 * g, m < p.m ? p.n : 0);
+    }
+    if (s + 4 < s1) load(s + 4);
+    Fragment<float> d[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) d[t] = Fragment<float>(x[t]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      Eight<float> column;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) column.v[r] = now[r][e];
+      const Fragment<float> w(column);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[e][t] = Fragment<float>::product(w, d[t], acc[e][t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<f32x4 *>(&sums[wave][16 * t + i][16 * g + 4 * r]) =
+          f32x4{acc[0][t][r], acc[1][t][r], acc[2][t][r], acc[3][t][r]};
+  __syncthreads();
+  for (int o = threadIdx.x; o < MT * 256; o += 256) {
+    const int m = o / 16, col = o % 16 * 4, n = blockIdx.x * 64 + col;
+    if (m >= p.m || n >= p.k) continue;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4 *>(&sums[w][m][col]);
+    if (p.part) *reinterpret_cast<f32x4 *>(p.part + blockIdx.y * p.step + m * p.ld + n) = v;
+    else finish<float, true>(p.f, m, n, p.k - n, v);
+  }
+}
+
+// dW: a wave takes 64 columns, whose fragments of A stay in registers, and kTall rows, 16 at a time;
+// one instruction sums over all rows of dP and A.  A lane's four sums are neighbours in a row.
+constexpr int kTall = 64;
+__global__ __launch_bounds__(256) void few_dw_kernel(FewRows p) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, m = 8 * (lane >> 4);
+  const int c0 = (blockIdx.x * 4 + wave) * 64;
+  if (c0 >= p.k) return;
+  auto eight = [&](const float *x, int64_t ld, int at, int cols) __attribute__((always_inline)) {
+    Eight<float> v;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v.v[r] = m + r < p.m && at < cols ? x[(int64_t)(m + r) * ld + at] : 0.0f;
+    return v;
+  };
+  const int first = blockIdx.y * kTall, last = min(first + kTall, p.n);
+  Eight<float> next = eight(p.dp, p.lddp, first + i, p.n);
+  Fragment<float> a[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = Fragment<float>(eight(p.a, p.lda, c0 + 16 * e + i, p.k));
+  for (int j0 = first; j0 < last; j0 += 16) {
+    const Fragment<float> d(next);
+    if (j0 + 16 < last) next = eight(p.dp, p.lddp, j0 + 16 + i, p.n);
+    f32x4 acc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = Fragment<float>::product(a[e], d, f32x4{0, 0, 0, 0});
+    if (j0 + i >= p.n) continue;
+    float *to = static_cast<float *>(p.f.out) + (int64_t)(j0 + i) * p.f.ldo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = c0 + 16 * e + 4 * (lane >> 4);
+      if (c < p.k) store4(to + c, acc[e], p.k - c, p.f.vec_o);
+    }
+  }
+}
+
+// Parts of dA's sums: blocks for two a compute unit, each wave of a part with at least four steps.
+struct FewParts {
+  int parts, steps;
+};
+FewParts few_parts(int64_t n, int64_t k) {
+  const int64_t blocks = std::max<int64_t>(1, (k + 63) / 64), steps = (n + 31) / 32;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({512 / blocks, steps / 16, kMostParts}));
+  const int64_t per = std::max<int64_t>(1, (steps + want - 1) / want);
+  return FewParts{(int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per};
+}
+
 struct Call {
   int64_t m, n, k;
   const void *dc, *a, *w, *pre;
@@ -204,11 +346,18 @@ struct Plan {
 
 template <class T>
 Plan plan(int64_t m, int64_t n, int64_t k) {
-  Plan p;
+  Plan p{};
   Room r;
   constexpr int P = kPlanes<T>;
   p.np = round_up(n, P == 2 ? 32 : 8);
   p.kp = round_up(k, P == 2 ? 32 : 8);
+  if (few_rows<T>(m)) {
+    p.p_at = r.take(m * p.np * 4);
+    const int parts = few_parts(n, k).parts;
+    p.parts_at = r.take(parts > 1 ? parts * m * round_up(k, 4) * 4 : 0);
+    p.total = r.at;
+    return p;
+  }
   p.tops_at = r.take(P == 2 ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
   p.p_at = r.take(P * m * p.np * 2);
   p.pc_at = r.take(P == 2 ? P * m * p.np * 2 : 0);
@@ -225,7 +374,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int type) {
 
 template <class T>
 int sweep_blocks(const Matrix &a) {
-  return (int)((int64_t)((a.rows + kRows - 1) / kRows) * ((a.width + kCols<T> - 1) / kCols<T>));
+  return (int)((int64_t)((a.rows + a.rows_per - 1) / a.rows_per) * ((a.width + kCols<T> - 1) / kCols<T>));
 }
 // Whether a lane's columns are one aligned load.
 template <class T>
@@ -244,13 +393,67 @@ Finish output(void *out, int64_t ld, const float *mtop, const float *ntop, int u
   return set_accesses<T>(f);
 }
 
+void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
+  const int m = (int)c.m, n = (int)c.n, k = (int)c.k;
+  const bool place = c.act == OG_ACT_NONE;  // dC is dP
+  Matrix a{};
+  a.x = c.dc;
+  a.ldx = c.lddc;
+  a.pre = place ? nullptr : c.pre;
+  a.ldp = c.ldp;
+  a.act = c.act;
+  a.rows = m;
+  a.cols = n;
+  a.width = (int)p.np;
+  a.rows_per = kFew;
+  a.vec_x = lanes_whole<float>(c.dc, c.lddc);
+  a.vec_p = lanes_whole<float>(c.pre, c.ldp);
+  a.bias = c.dbias;
+  if (!place && (c.da || c.dw)) a.plain = reinterpret_cast<float *>(c.ws + p.p_at);
+  a.blocks = (a.width + kCols<float> - 1) / kCols<float>;  // (m 0 clears dbias)
+  if (a.blocks > 0 && (a.bias || a.plain)) {
+    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves), 0, s, a, Matrix{}, Matrix{});
+  }
+  FewRows q{};
+  q.m = m, q.n = n, q.k = k;
+  q.dp = place ? static_cast<const float *>(c.dc) : a.plain;
+  q.lddp = place ? c.lddc : p.np;
+  q.a = static_cast<const float *>(c.a), q.w = static_cast<const float *>(c.w);
+  q.lda = c.lda, q.ldw = c.ldw;
+  if (c.da) {
+    const FewParts parts = few_parts(n, k);
+    q.f = output<float>(c.da, c.ldda, nullptr, nullptr, 0);
+    q.vec = whole(q.w, q.ldw);
+    q.steps = parts.steps;
+    if (parts.parts > 1) {
+      q.part = reinterpret_cast<float *>(c.ws + p.parts_at);
+      q.ld = round_up(k, 4);
+      q.step = m * q.ld;
+    }
+    const dim3 grid((k + 63) / 64, parts.parts);
+    if (m <= 16) hipLaunchKernelGGL(few_da_kernel<1>, grid, dim3(256), 0, s, q);
+    else hipLaunchKernelGGL(few_da_kernel<2>, grid, dim3(256), 0, s, q);
+    if (q.part) {
+      const int64_t quads = (int64_t)m * ((k + 3) / 4);
+      hipLaunchKernelGGL((join_kernel<float, true>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
+                         dim3(256), 0, s, m, k, parts.parts, q.part, q.ld, q.step, q.f);
+    }
+  }
+  if (c.dw) {
+    q.f = output<float>(c.dw, c.lddw, nullptr, nullptr, 0);
+    hipLaunchKernelGGL(few_dw_kernel, dim3((k + 255) / 256, (n + kTall - 1) / kTall), dim3(256), 0, s, q);
+  }
+}
+
 template <class T>
 void gradient(const Call &c, const Plan &p, hipStream_t s) {
+  if (few_rows<T>(c.m)) return few_gradient(c, p, s);
   constexpr int P = kPlanes<T>;
   const int m = (int)c.m, n = (int)c.n, k = (int)c.k;
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
   Matrix dp{};
+  dp.rows_per = kRows;
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
@@ -271,6 +474,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     const int64_t total = tw + round_up(k, 64) - tops;
     auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
       Matrix a{};
+      a.rows_per = kRows;
       a.x = x;
       a.ldx = ld;
       a.rows = (int)count;
@@ -282,6 +486,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       return a;
     };
     Matrix ma{}, mw{};
+    ma.rows_per = mw.rows_per = kRows;
     if (c.da) {
       dp.rtop = r;
       dp.out = at(p.p_at);
