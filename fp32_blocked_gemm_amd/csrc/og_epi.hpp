@@ -427,29 +427,32 @@ int parts_of(int64_t M, int64_t N, int64_t K) {
   return parts;
 }
 
-// Bytes of a product's parts.
+// Bytes of a product's parts.  (fold: see run_product)
 template <class T, bool TT>
-int64_t parts_bytes(int64_t M, int64_t N, int64_t K) {
-  const int p = parts_of<T, TT>(M, N, K);
-  return p > 1 ? p * M * round_up(N, 4) * 4 : 0;
+int64_t parts_bytes(int64_t M, int64_t N, int64_t K, int fold = 1) {
+  const int p = parts_of<T, TT>(fold * M, N, K);
+  return p * fold > 1 ? p * fold * M * round_up(N, 4) * 4 : 0;
 }
 
+// The product, its k in parts where that is faster.  fold 2: the rows of A come twice, as a matrix
+// and its remainder below it (g.M rows in all), whose sums are added like parts.
 template <class T, bool TA, bool TB, bool PLAIN>
-void run_product(Args g, const Finish &f, char *ws, hipStream_t s) {
+void run_product(Args g, const Finish &f, char *ws, hipStream_t s, int fold = 1) {
   using C = typename EpiTiles<Element<T>, kPlanes<T>, TA && TB>::type;
   const int parts = parts_of<T, TA && TB>(g.M, g.N, g.K);
   StoreArgs e{f, nullptr, 0, 0};
-  if (parts > 1) {
+  if (parts * fold > 1) {
     e.part = reinterpret_cast<float *>(ws);
     e.ld = round_up(g.N, 4);
     e.step = g.M * e.ld;
-    g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
   }
+  if (parts > 1) g.k_split = (int)round_up((g.K + parts - 1) / parts, 64);
   product_of<TA, TB, Store<T, PLAIN>>(C(), least(C(), false, g, parts), g, e, parts, s);
-  if (parts == 1) return;
-  const int64_t quads = g.M * ((g.N + 3) / 4);
+  if (!e.part) return;
+  const int rows = g.M / fold;
+  const int64_t quads = (int64_t)rows * ((g.N + 3) / 4);
   hipLaunchKernelGGL((join_kernel<T, PLAIN>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0,
-                     s, g.M, g.N, parts, e.part, e.ld, e.step, f);
+                     s, rows, g.N, parts * fold, e.part, e.ld, rows * e.ld, f);
 }
 
 // Whether the tile product can read a 16-bit matrix where it lies.
@@ -536,9 +539,9 @@ struct Fragment<float> {
   }
 };
 
-// Rows of 16-bit values, zero from cols to ld (a multiple of 8).
-static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int64_t ldx, int rows, int cols, uint16_t *out,
-                                                   int ld) {
+// Rows of 16-bit values, zero from cols to ld (a multiple of 8); `times` copies one below the other.
+static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int64_t ldx, int rows, int cols,
+                                                          uint16_t *out, int ld, int times) {
   const int per = ld / 8;
   const int64_t total = (int64_t)rows * per;
   for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
@@ -547,17 +550,18 @@ static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int
     s16x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? (short)x[i * ldx + c + e] : (short)0;
-    *reinterpret_cast<s16x8 *>(out + i * ld + c) = v;
+    for (int t = 0; t < times; ++t) *reinterpret_cast<s16x8 *>(out + (i + (int64_t)t * rows) * ld + c) = v;
   }
 }
 
-// A 16-bit matrix as an operand.
-inline Operand operand16(const void *x, int64_t ld, int64_t rows, int64_t cols, int64_t padded, char *ws, hipStream_t s) {
-  if (rows == 0 || cols == 0 || readable(x, cols, ld)) return Operand{static_cast<const uint16_t *>(x), ld, 0};
+// A 16-bit matrix as an operand, its rows `times` over.
+inline Operand operand16(const void *x, int64_t ld, int64_t rows, int64_t cols, int64_t padded, char *ws, hipStream_t s,
+                         int times = 1) {
+  if (rows == 0 || cols == 0 || (times == 1 && readable(x, cols, ld))) return Operand{static_cast<const uint16_t *>(x), ld, 0};
   uint16_t *to = reinterpret_cast<uint16_t *>(ws);
   const int64_t granules = rows * (padded / 8);
   hipLaunchKernelGGL(copy_kernel, dim3((unsigned)std::min<int64_t>((granules + 255) / 256, 8192)), dim3(256), 0, s,
-                     static_cast<const uint16_t *>(x), ld, (int)rows, (int)cols, to, (int)padded);
+                     static_cast<const uint16_t *>(x), ld, (int)rows, (int)cols, to, (int)padded, times);
   return Operand{to, padded, 0};
 }
 

@@ -7,9 +7,13 @@
 // (the transposing reads).
 //
 // 16-bit types: dP is rounded to the type once (where an activation changes it;
-// else dC is read where it lies), the sums dbias from it before that.  fp16
-// holds half of dP where the slope may pass 1, so that none that dC holds
-// overflows.
+// else dC is read where it lies), the sums dbias from it before that.  That
+// rounding and P's make errors of dA and dW 1.45 times those of a plain form in fp32
+// throughout, whose result is rounded once (0.0024 and 0.0017 in bf16).  Up to 128
+// rows, where single outputs hang on few roundings and the bytes of W bound the
+// time, what a smooth activation's dP leaves to its rounding is kept as a second matrix below the
+// first (A comes twice for it): 1.05 times.  fp16 holds half of dP where the
+// slope may pass 1, so that none that dC holds overflows.
 //
 // fp32: two fp16 planes.  A product's powers of two belong to the indices that
 // it does not sum over, so that every row and column of a gradient keeps the bits
@@ -22,8 +26,13 @@ namespace og::epi::grad {
 
 // A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
 // (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
-// dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).
-constexpr int kWaves = 8, kRows = 4 * kWaves;  // (rows of a block: Matrix::rows_per)
+// dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).  fp32 takes
+// more rows a block for fewer atomics on a column's maximum (4096 x 1536 x 384, all of the gradient:
+// 128 rows 100 us, 64 104, 32 107, 97 without the atomics).
+template <class T>
+constexpr int kWaves = kPlanes<T> == 2 ? 16 : 8;
+template <class T>
+constexpr int kRows = kPlanes<T> == 2 ? 128 : 32;
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
 template <class T>
@@ -40,6 +49,7 @@ struct Matrix {
   int halve;              // fp16: the output is half the value
   uint16_t *out;          // 16-bit types: the values (null: not wanted); fp32: planes by the row's power
   uint16_t *out_c;        // fp32: planes by the column's power
+  uint16_t *rest;         // 16-bit types: what the rounding of out leaves (null: not wanted)
   float *rtop, *ctop;     // fp32: largest magnitudes (null: not wanted)
   float *sums;            // column sums of the block's rows, [row block][width] (null: not wanted)
   int rows_per;           // rows of a block
@@ -84,9 +94,9 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, Lane<T
 // One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
 // and largest magnitudes.
 template <class T, bool LAYOUT>
-__global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
+__global__ __launch_bounds__(64 * kWaves<T>) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
   constexpr int H = kPer<T> / 4;
-  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves][64];
+  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves<T>][64];
   int block = blockIdx.x;
   const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
   block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
@@ -101,7 +111,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
 #pragma unroll
       for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
-    for (int64_t i = i0; i < end; i += kWaves) {
+    for (int64_t i = i0; i < end; i += kWaves<T>) {
       Lane<T> v;
       values<T>(a, i, c, v);
       if (a.out) {
@@ -114,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
     f32x4 sum[H], top[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) sum[h] = top[h] = f32x4{0, 0, 0, 0};
-    for (int64_t i = i0; i < end; i += kWaves) {
+    for (int64_t i = i0; i < end; i += kWaves<T>) {
       Lane<T> v;
       values<T>(a, i, c, v);
 #pragma unroll
@@ -139,6 +149,15 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
 #pragma unroll
         for (int e = 0; e < kPer<T>; ++e) w[e] = (T)(a.halve ? 0.5f * v.v[e / 4][e % 4] : v.v[e / 4][e % 4]);
         *reinterpret_cast<V *>(reinterpret_cast<T *>(a.out) + i * a.width + c) = w;
+        if (a.rest) {
+          V r;
+#pragma unroll
+          for (int e = 0; e < kPer<T>; ++e) {
+            const float whole = a.halve ? 0.5f * v.v[e / 4][e % 4] : v.v[e / 4][e % 4], held = (float)w[e];
+            r[e] = (T)(__builtin_isfinite(held) ? whole - held : 0.0f);
+          }
+          *reinterpret_cast<V *>(reinterpret_cast<T *>(a.rest) + i * a.width + c) = r;
+        }
       }
     }
     if (!a.sums && !a.ctop && !a.bias) return;
@@ -149,7 +168,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
     }
     __syncthreads();
     if (wave || c >= a.width) return;
-    for (int w = 1; w < kWaves; ++w) {
+    for (int w = 1; w < kWaves<T>; ++w) {
 #pragma unroll
       for (int h = 0; h < H; ++h) sum[h] += of_waves[h][w][lane];
       if constexpr (kPlanes<T> == 2) {
@@ -329,6 +348,9 @@ FewParts few_parts(int64_t n, int64_t k) {
   return FewParts{(int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per};
 }
 
+// 16-bit types: rows up to which dP is held with its remainder.
+constexpr int kTwice = 128;
+
 struct Call {
   int64_t m, n, k;
   const void *dc, *a, *w, *pre;
@@ -359,12 +381,14 @@ Plan plan(int64_t m, int64_t n, int64_t k) {
     return p;
   }
   p.tops_at = r.take(P == 2 ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
-  p.p_at = r.take(P * m * p.np * 2);
+  const int fold = P == 1 && m <= kTwice ? 2 : 1;  // (whatever the activation)
+  p.p_at = r.take(fold * P * m * p.np * 2);
   p.pc_at = r.take(P == 2 ? P * m * p.np * 2 : 0);
-  p.a_at = r.take(P * m * p.kp * 2);
+  p.a_at = r.take(fold * P * m * p.kp * 2);
   p.w_at = r.take(P * n * p.kp * 2);
-  p.sums_at = r.take((m + kRows - 1) / kRows * p.np * 4);
-  p.parts_at = r.take(std::max(parts_bytes<T, false>(m, k, n), parts_bytes<T, true>(n, k, m)));
+  p.sums_at = r.take((m + kRows<T> - 1) / kRows<T> * p.np * 4);
+  p.parts_at = r.take(std::max({parts_bytes<T, false>(m, k, n), parts_bytes<T, false>(m, k, n, fold),
+                                parts_bytes<T, true>(n, k, m), parts_bytes<T, true>(n, k, fold * m)}));
   p.total = r.at;
   return p;
 }
@@ -412,7 +436,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
   if (!place && (c.da || c.dw)) a.plain = reinterpret_cast<float *>(c.ws + p.p_at);
   a.blocks = (a.width + kCols<float> - 1) / kCols<float>;  // (m 0 clears dbias)
   if (a.blocks > 0 && (a.bias || a.plain)) {
-    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves), 0, s, a, Matrix{}, Matrix{});
+    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves<float>), 0, s, a, Matrix{}, Matrix{});
   }
   FewRows q{};
   q.m = m, q.n = n, q.k = k;
@@ -453,7 +477,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
   Matrix dp{};
-  dp.rows_per = kRows;
+  dp.rows_per = kRows<T>;
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
@@ -467,14 +491,14 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   dp.sums = c.dbias ? reinterpret_cast<float *>(c.ws + p.sums_at) : nullptr;
   Operand rows, cols, A, W;  // dP by rows and by columns, A, W
   const float *rtop = nullptr, *ctop = nullptr, *atop = nullptr, *wtop = nullptr;
-  int up = 0;
+  int up = 0, fold = 1;
   if constexpr (P == 2) {
     float *tops = reinterpret_cast<float *>(c.ws + p.tops_at);
     float *r = tops, *t = r + round_up(m, 64), *ta = t + round_up(n, 64), *tw = ta + round_up(k, 64);
     const int64_t total = tw + round_up(k, 64) - tops;
     auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
       Matrix a{};
-      a.rows_per = kRows;
+      a.rows_per = kRows<T>;
       a.x = x;
       a.ldx = ld;
       a.rows = (int)count;
@@ -486,7 +510,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       return a;
     };
     Matrix ma{}, mw{};
-    ma.rows_per = mw.rows_per = kRows;
+    ma.rows_per = mw.rows_per = kRows<T>;
     if (c.da) {
       dp.rtop = r;
       dp.out = at(p.p_at);
@@ -501,9 +525,9 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     const int blocks = dp.blocks + ma.blocks + mw.blocks;
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
                        tops, total);
-    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
+    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves<T>), 0, s, dp, ma, mw);
     if (blocks > 0 && (c.da || c.dw))
-      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
+      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves<T>), 0, s, dp, ma, mw);
     rows = Operand{at(p.p_at), 2 * p.np, 0};
     cols = Operand{at(p.pc_at), 2 * p.np, 0};
     A = Operand{at(p.a_at), 2 * p.kp, 0};
@@ -514,25 +538,33 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     if constexpr (std::is_same_v<T, _Float16>) dp.halve = c.act > OG_ACT_RELU;
     up = dp.halve;
     dp.out = place || !(c.da || c.dw) ? nullptr : at(p.p_at);
-    if (dp.out || dp.sums) {
-      dp.blocks = sweep_blocks<T>(dp);
+    if (m > 0 && m <= kTwice && c.act > OG_ACT_RELU) {
+      fold = 2;
+      if (dp.out) dp.rest = dp.out + m * p.np;
+    }
+    if (m <= kRows<T>) {  // one row block has all of a column's sum
+      dp.bias = c.dbias;
+      dp.sums = nullptr;
+    }
+    if (dp.out || dp.sums || dp.bias) {
+      dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias ? (dp.width + kCols<T> - 1) / kCols<T> : 0);  // (m 0 clears dbias)
       if (dp.blocks > 0)
-        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
+        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves<T>), 0, s, dp, Matrix{}, Matrix{});
     }
     rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
-    if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s);
+    if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
     if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
   }
-  if (c.dbias)
-    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + kRows - 1) / kRows, n,
+  if (dp.sums)
+    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + kRows<T> - 1) / kRows<T>, n,
                        dp.width, static_cast<T *>(c.dbias));
   Args g{};
   if (c.da && m > 0 && k > 0) {
-    g.a = rows, g.b = W, g.M = m, g.N = k, g.K = n;
-    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop, up), c.ws + p.parts_at, s);
+    g.a = rows, g.b = W, g.M = fold * m, g.N = k, g.K = n;
+    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop, up), c.ws + p.parts_at, s, fold);
   }
   if (c.dw && n > 0 && k > 0) {
-    g.a = cols, g.b = A, g.M = n, g.N = k, g.K = m;
+    g.a = cols, g.b = A, g.M = n, g.N = k, g.K = fold * m;
     run_product<T, true, true, true>(g, output<T>(c.dw, c.lddw, ctop, atop, up), c.ws + p.parts_at, s);
   }
 }

@@ -303,7 +303,8 @@ def gemm_epi(a, w, bias, act, residual):
 
 def gemm_epi_grad(dc, a, w, pre, act):
     """dict of exact values for this pre, and bounds: da, dw, dbias.  16-bit types round dP to the
-    type (its largest subnormal's half step, twice in fp16, which may hold halves)."""
+    type (its largest subnormal's half step, twice in fp16, which may hold halves); up to 128 rows
+    with a second matrix of what that leaves, whose own rounding is half a step of half a step."""
     dc64, a64, w64 = dc.to(F64), a.to(F64), w.to(F64)
     dp, edp = dc64, torch.zeros_like(dc64)
     if act is not None:
@@ -315,7 +316,8 @@ def gemm_epi_grad(dc, a, w, pre, act):
     held = edp
     info = torch.finfo(dc.dtype)
     if act is not None and dc.dtype != torch.float32:
-        held = edp + half_step(dc.dtype) * (dp.abs() + edp) + 2 * info.smallest_normal * info.eps
+        step = half_step(dc.dtype) ** (2 if len(dc) <= 128 else 1)
+        held = edp + step * (dp.abs() + edp) + 2 * info.smallest_normal * info.eps
     out = {"da": dp @ w64, "dw": dp.t() @ a64, "dbias": dp.sum(0)}
     e_da = held @ w64.abs() + product_error(dp, w64.t(), dc.dtype) * 1.01
     e_dw = held.t() @ a64.abs() + product_error(dp.t(), a64.t(), dc.dtype) * 1.01
