@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -78,21 +79,18 @@ def build(verbose: bool = False) -> str:
              for u in range(1, N_UNITS + 1)]
     cmds = [[HIPCC, *FLAGS, *([] if src in OPERATORS else VGPR_FORM), *inc, *defs, "-c", src, "-o",
              obj] for src, defs, obj in jobs]
-    pending, running, msgs, failed = list(cmds), [], [], []
-    limit = _jobs()
-    while pending or running:
-        while pending and len(running) < limit:
-            cmd = pending.pop(0)
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            running.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                  stderr=subprocess.STDOUT, text=True)))
-        cmd, proc = running.pop(0)
-        out, _ = proc.communicate()
-        lines = [l for l in out.splitlines() if NOISE not in l]
-        msgs += lines
-        if proc.returncode != 0:
-            failed.append(cmd[-1])
+    msgs, failed = [], []
+
+    def compile_one(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return cmd, subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+    with ThreadPoolExecutor(_jobs()) as pool:
+        for cmd, res in pool.map(compile_one, cmds):
+            msgs += [l for l in res.stdout.splitlines() if NOISE not in l]
+            if res.returncode != 0:
+                failed.append(cmd[-1])
     if failed:
         raise RuntimeError(f"hipcc failed for {failed}:\n" + "\n".join(msgs))
     link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *[obj for *_, obj in jobs],

@@ -111,7 +111,8 @@ __global__ __launch_bounds__(W * 64) void rows_kernel(Rows p) {
   __shared__ float sums[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
+  const int across = (p.n + 16 * NT - 1) / (16 * NT), below = blockIdx.x / across;
+  const int n0 = (blockIdx.x - below * across) * 16 * NT, m0 = below * 16 * MT;
   const int chunks = (p.k + C::kDepth - 1) / C::kDepth;
   const int c0 = (int)((int64_t)chunks * wave / W), c1 = (int)((int64_t)chunks * (wave + 1) / W);
   const T *a[MT], *b[NT];
@@ -180,8 +181,9 @@ __global__ __launch_bounds__(W * 64) void rows_kernel(Rows p) {
 
 template <class T, int W, int MT, int NT>
 void launch_rows(const Rows &p, hipStream_t s) {
-  hipLaunchKernelGGL((rows_kernel<T, W, MT, NT>),
-                     dim3((p.n + 16 * NT - 1) / (16 * NT), (p.m + 16 * MT - 1) / (16 * MT)), dim3(W * 64), 0, s, p);
+  // (one axis: a second would end at 65535 blocks)
+  const unsigned across = (p.n + 16 * NT - 1) / (16 * NT), below = (p.m + 16 * MT - 1) / (16 * MT);
+  hipLaunchKernelGGL((rows_kernel<T, W, MT, NT>), dim3(across * below), dim3(W * 64), 0, s, p);
 }
 
 // Whether a product runs on the rows kernel: up to 16 rows (fp32: 64, whose tile product needs
@@ -192,7 +194,8 @@ void launch_rows(const Rows &p, hipStream_t s) {
 template <class T>
 bool few_rows(int64_t m, int64_t n, int64_t k) {
   constexpr bool wide = sizeof(T) == 4;
-  return m <= (wide ? 64 : 16) || (wide ? (m + 31) / 32 * n * k <= (1 << 23) : (m + 15) / 16 * n * k <= (1 << 24));
+  const int64_t weights = n * std::max<int64_t>(k, 1);
+  return m <= (wide ? 64 : 16) || (wide ? (m + 31) / 32 * weights <= (1 << 23) : (m + 15) / 16 * weights <= (1 << 24));
 }
 
 // Tiles of a block: one of each up to 16 rows and for 16-bit types (11008 x 4096 bf16 by one row
@@ -249,7 +252,7 @@ void forward(const Call &c, const Plan &p, hipStream_t s) {
     uint16_t *a = reinterpret_cast<uint16_t *>(c.ws + p.a_at), *w = reinterpret_cast<uint16_t *>(c.ws + p.w_at);
     const int64_t rows = c.m + c.n;
     const Side sa{c.a, c.lda, (int)c.m, a, mtop}, sw{c.w, c.ldw, (int)c.n, w, ntop};
-    const bool wide = c.k > 256 * kHeld;
+    const bool wide = c.k > 256 * kHeld && rows <= (1 << 22);  // (a launch has fewer than 2^32 threads)
     hipLaunchKernelGGL(wide ? planes_kernel<4> : planes_kernel<1>, dim3((unsigned)(wide ? rows : (rows + 3) / 4)),
                        dim3(256), 0, s, sa, sw, (int)c.k, (int)p.kp, whole(static_cast<const float *>(c.a), c.lda),
                        whole(static_cast<const float *>(c.w), c.ldw));

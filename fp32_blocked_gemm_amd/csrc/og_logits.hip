@@ -91,7 +91,7 @@ struct Steps {
 // VEC: eight neighbouring logits a thread (rows of z, o and bias are aligned to vectors of eight); else single ones, a block's width apart.
 template <class T, bool VEC>
 __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
-  extern __shared__ uint32_t counts[];
+  extern __shared__ __align__(32) uint32_t counts[];
   const int64_t row = blockIdx.y;
   const int v0 = blockIdx.x * p.segment, size = min(p.segment, p.v - v0);
   const int tid = threadIdx.x;

@@ -433,8 +433,8 @@ int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int t
  * more (where the product is not small) each row of A and W is held as two fp16
  * planes times a power of two of its own: 22 bits of each value, down to 2^-38 of
  * the row's largest.  An fp32 row
- * that holds an infinity or NaN makes the sums it enters NaN; 16-bit ones follow the
- * formula.  act of -infinity is -0 (OG_ACT_NONE: itself; OG_ACT_RELU: +0), of NaN NaN.
+ * that holds an infinity or NaN makes the sums it enters NaN or infinite; 16-bit ones
+ * follow the formula.  act of -infinity is -0 (OG_ACT_NONE: itself; OG_ACT_RELU: +0), of NaN NaN.
  * The residual may be C itself with the same stride; P must not be C, and neither may
  * overlap an input otherwise.  The gaps of P and C are not written.
  * Requirements: m, n, k >= 0; lda, ldw >= max(1, k); ldc (and ldr, ldp where given)

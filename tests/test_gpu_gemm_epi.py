@@ -271,3 +271,33 @@ def test_refused_by_the_binding():
             og.gemm_nt_epi_grad(dc, A, B, **kw)
     with pytest.raises(ValueError):
         og.gemm_nt_epi_grad(dc[:3], A, B)
+
+
+@pytest.mark.parametrize("dtype", EVERY)
+@pytest.mark.parametrize("m,n,k", [(1100000, 1, 1), (1100000, 2, 0), (90000, 3, 5), (2, 70000, 3)])
+def test_many_rows(m, n, k, dtype):
+    """More row blocks than a launch's second axis has."""
+    c, dc = make(m, n, k, dtype)
+    say(f"gemm_nt_epi {m}x{n}x{k} {dtype}")
+    out, pre = og.gemm_nt_epi(**c, act="relu", need_pre=True)
+    check_forward(c, "relu", out, pre)
+    check_grad(c, dc, pre, "relu", og.gemm_nt_epi_grad(dc, c["A"], c["B"], pre=pre, act="relu"))
+
+
+def test_outputs_past_32_bits():
+    """C, P and dC of more than 4 GiB: the last rows, and the gradient that they enter."""
+    th = torch()
+    m, n, k = 66000, 33024, 64
+    gen = th.Generator(device="cuda").manual_seed(0)
+    A = th.randn((m, k), generator=gen, device="cuda").bfloat16()
+    B = (0.1 * th.randn((n, k), generator=gen, device="cuda")).bfloat16()
+    say(f"gemm_nt_epi {m}x{n}x{k}")
+    out, pre = og.gemm_nt_epi(A, B, act="silu", need_pre=True)
+    e = ref.gemm_epi(A[-70:], B, None, "silu", None)
+    inside(out[-70:], e["c"], e["e_c"])
+    inside(pre[-70:], e["pre"], e["e_pre"])
+    dA = og.gemm_nt_epi_grad(out, A, B, pre=pre, act="silu", need=(True, False, False))[0]
+    # (of more than 128 rows: dP is rounded to the type once)
+    wide = th.cat([out[-70:], out[-70:]]), th.cat([A[-70:], A[-70:]]), th.cat([pre[-70:], pre[-70:]])
+    e = ref.gemm_epi_grad(wide[0], wide[1], B, wide[2], "silu")
+    inside(dA[-70:], e["da"][:70], e["e_da"][:70])

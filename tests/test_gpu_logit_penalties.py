@@ -158,3 +158,13 @@ def test_refused_by_the_binding():
             og.logit_penalties(**{**c, **kw})
     shared = {**c, "bias": c["bias"][:1].expand(3, 100)}
     assert th.equal(og.logit_penalties(**shared), og.logit_penalties(**{**c, "bias": c["bias"][:1]}))
+
+
+def test_more_rows_than_a_launch_has():
+    th = torch()
+    n, v = 70000, 5
+    c = make(n, v, 3, "float32", STEPS, seed=9)
+    got = og.logit_penalties(**c)
+    for rows in (slice(0, 40), slice(65500, 65570), slice(n - 40, n)):
+        part = {k: x[rows] for k, x in c.items()}
+        check(part, got[rows])
