@@ -1,7 +1,8 @@
 """Python binding of libog: exact and fast fp32 matrix product and NCHW
-convolution, and three operators around a language model's N x K weights (the
-product with 4-bit weights, the linear cross entropy with its gradient, the
-Newton-Schulz update) on MI355X (gfx950).
+convolution, and operators around a language model's N x K weights (the
+product with 4-bit weights, the product with an epilogue and its gradient, the
+linear cross entropy with its gradient, the gradients' norm and clipping, the
+Newton-Schulz update, the penalties on logits) on MI355X (gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libog.so`` behind the C ABI of ``include/og.h``.  Torch supplies
@@ -345,12 +346,11 @@ def _type(t, allowed=(F32, BF16)) -> int:
 
 
 def _one_device(*ts):
-    at = ts[0].get_device()
+    at = ts[0].get_device()  # (-1: not on a GPU)
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if t.get_device() != at:
-            raise ValueError("tensors must be on one device")
+        i = t.get_device()
+        if i != at or i < 0:
+            raise ValueError("tensors must be CUDA tensors" if min(i, at) < 0 else "tensors must be on one device")
     return ts[0].device
 
 

@@ -254,8 +254,10 @@ struct Store {
   // A block whose rows and columns are all the product's, all accesses whole: places as 32-bit
   // offsets from the wave's first element, which is uniform.  Each four values go all the way
   // before the next (fences): together their activations would need more registers than there
-  // are.  (4096 x 11008 x 4096 bf16, SiLU and P: 381 us, 318 without either; 496 with places of 64
-  // bits, the activation chosen for each value and IEEE divisions.)
+  // are.  (4096 x 11008 x 4096 bf16, calls back to back: 298 us without activation and P, 298 with
+  // SiLU, 342 with SiLU and P, whose 90 MB more leave the compute units all at once at the end of a
+  // round of tiles.  With places of 64 bits, the activation chosen for each value and IEEE
+  // divisions the last took 110 us more.)
   template <class S, int ACT>
   static __device__ __forceinline__ void inside(f32x4 (&acc)[S::FM][S::FN], const Place &t, const Finish &f) {
     typedef T T4 __attribute__((ext_vector_type(4)));
@@ -364,8 +366,8 @@ struct Cost {
 // The tiles by planes and by whether both operands are transposed (dW).  Beside og_tile.hpp's squares
 // are oblong ones, which fill the compute units where squares leave a part of a round (512 x 11008
 // x 4096 fp32: 174 tiles of 192 x 192 168 us, 232 of 128 x 192 122).  Times measured on stages of k 1024
-// to 3072; of 1800 seeded products the listed tiles' predicted time is 1.01 times that of the best of 15
-// shapes in the mean.
+// to 3072.  (144 seeded products of 65 to 11008 rows and columns, 24 of each kind: the chosen tile and
+// parts take 1.01 to 1.05 times the fastest listed ones' time in the mean, at most 1.20.)
 template <class E, int P, bool TT>
 struct EpiTiles {
   using type = Choices<Cost<Shape<E, 1, 256, 256, 2, 4, 2, 1>, 1010, 1505, 1462, 15000>,
@@ -408,7 +410,7 @@ struct EpiTiles<E, 2, true> {
 };
 
 // Parts of k: as many as take the least time, where the parts' sums cost a launch and their
-// bytes, written and read.
+// bytes, written and read (at 6.5 TB/s: mostly in the caches).
 constexpr int kMostParts = 16;
 template <class T, bool TT>
 int parts_of(int64_t M, int64_t N, int64_t K) {
@@ -421,7 +423,7 @@ int parts_of(int64_t M, int64_t N, int64_t K) {
     g.N = (int)N;
     g.K = (int)K;
     g.k_split = p > 1 ? (int)round_up((K + p - 1) / p, 64) : 0;
-    const double t = least(C(), false, g, p) + (p > 1 ? 4000 + 8.0 * p * M * N / 4000 : 0);
+    const double t = least(C(), false, g, p) + (p > 1 ? 3500 + 8.0 * p * M * N / 6500 : 0);
     if (t < best) best = t, parts = p;
   }
   return parts;

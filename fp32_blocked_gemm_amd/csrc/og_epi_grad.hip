@@ -27,12 +27,13 @@ namespace og::epi::grad {
 // A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
 // (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
 // dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).  fp32 takes
-// more rows a block for fewer atomics on a column's maximum (4096 x 1536 x 384, all of the gradient:
-// 128 rows 100 us, 64 104, 32 107, 97 without the atomics).
+// more rows a block where there are many, for fewer atomics on a column's maximum (all of the gradient,
+// 4096 x 1536 x 384: 32 rows 108 us, 64 104, without the atomics 97; 300 x 1001 x 3001: 68 and 78).
+constexpr int kWaves = 8, kRows = 32;
 template <class T>
-constexpr int kWaves = kPlanes<T> == 2 ? 16 : 8;
-template <class T>
-constexpr int kRows = kPlanes<T> == 2 ? 128 : 32;
+int rows_per(int64_t rows) {
+  return kPlanes<T> == 2 && rows >= 2048 ? 2 * kRows : kRows;
+}
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
 template <class T>
@@ -94,9 +95,9 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, Lane<T
 // One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
 // and largest magnitudes.
 template <class T, bool LAYOUT>
-__global__ __launch_bounds__(64 * kWaves<T>) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
+__global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
   constexpr int H = kPer<T> / 4;
-  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves<T>][64];
+  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves][64];
   int block = blockIdx.x;
   const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
   block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(64 * kWaves<T>) void sweep_kernel(Matrix m0, Matrix
 #pragma unroll
       for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
-    for (int64_t i = i0; i < end; i += kWaves<T>) {
+    for (int64_t i = i0; i < end; i += kWaves) {
       Lane<T> v;
       values<T>(a, i, c, v);
       if (a.out) {
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(64 * kWaves<T>) void sweep_kernel(Matrix m0, Matrix
     f32x4 sum[H], top[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) sum[h] = top[h] = f32x4{0, 0, 0, 0};
-    for (int64_t i = i0; i < end; i += kWaves<T>) {
+    for (int64_t i = i0; i < end; i += kWaves) {
       Lane<T> v;
       values<T>(a, i, c, v);
 #pragma unroll
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * kWaves<T>) void sweep_kernel(Matrix m0, Matrix
     }
     __syncthreads();
     if (wave || c >= a.width) return;
-    for (int w = 1; w < kWaves<T>; ++w) {
+    for (int w = 1; w < kWaves; ++w) {
 #pragma unroll
       for (int h = 0; h < H; ++h) sum[h] += of_waves[h][w][lane];
       if constexpr (kPlanes<T> == 2) {
@@ -216,8 +217,9 @@ __global__ __launch_bounds__(1024) void bias_kernel(const float *sums, int block
 
 // Few fp32 rows of dC and A (up to kFew): bound by the bytes of W, read, and of dW, written.  Both
 // products run from memory through registers as three bf16 planes, 24 bits, so that nothing of W is
-// scanned and laid out first (4096 x 4096, one row: 55 us in all, 100 by the tile products; 16-bit
-// types, whose W lies ready for those, gain nothing).  dP lies in fp32: the sweep's, or dC.
+// scanned and laid out first (forward and gradient of one row on 4096 x 4096 61 us, 103 with the tile
+// products; 16-bit types, whose W lies ready for those, gain nothing).  dP lies in fp32: the
+// sweep's, or dC.
 constexpr int kFew = 32;
 template <class T>
 constexpr bool few_rows(int64_t m) {
@@ -386,7 +388,7 @@ Plan plan(int64_t m, int64_t n, int64_t k) {
   p.pc_at = r.take(P == 2 ? P * m * p.np * 2 : 0);
   p.a_at = r.take(fold * P * m * p.kp * 2);
   p.w_at = r.take(P * n * p.kp * 2);
-  p.sums_at = r.take((m + kRows<T> - 1) / kRows<T> * p.np * 4);
+  p.sums_at = r.take((m + kRows - 1) / kRows * p.np * 4);
   p.parts_at = r.take(std::max({parts_bytes<T, false>(m, k, n), parts_bytes<T, false>(m, k, n, fold),
                                 parts_bytes<T, true>(n, k, m), parts_bytes<T, true>(n, k, fold * m)}));
   p.total = r.at;
@@ -436,7 +438,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
   if (!place && (c.da || c.dw)) a.plain = reinterpret_cast<float *>(c.ws + p.p_at);
   a.blocks = (a.width + kCols<float> - 1) / kCols<float>;  // (m 0 clears dbias)
   if (a.blocks > 0 && (a.bias || a.plain)) {
-    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves<float>), 0, s, a, Matrix{}, Matrix{});
+    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves), 0, s, a, Matrix{}, Matrix{});
   }
   FewRows q{};
   q.m = m, q.n = n, q.k = k;
@@ -477,7 +479,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
   Matrix dp{};
-  dp.rows_per = kRows<T>;
+  dp.rows_per = rows_per<T>(m);
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
@@ -498,7 +500,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     const int64_t total = tw + round_up(k, 64) - tops;
     auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
       Matrix a{};
-      a.rows_per = kRows<T>;
+      a.rows_per = rows_per<T>(count);
       a.x = x;
       a.ldx = ld;
       a.rows = (int)count;
@@ -510,7 +512,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       return a;
     };
     Matrix ma{}, mw{};
-    ma.rows_per = mw.rows_per = kRows<T>;
+    ma.rows_per = mw.rows_per = kRows;
     if (c.da) {
       dp.rtop = r;
       dp.out = at(p.p_at);
@@ -525,9 +527,9 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     const int blocks = dp.blocks + ma.blocks + mw.blocks;
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
                        tops, total);
-    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves<T>), 0, s, dp, ma, mw);
+    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
     if (blocks > 0 && (c.da || c.dw))
-      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves<T>), 0, s, dp, ma, mw);
+      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
     rows = Operand{at(p.p_at), 2 * p.np, 0};
     cols = Operand{at(p.pc_at), 2 * p.np, 0};
     A = Operand{at(p.a_at), 2 * p.kp, 0};
@@ -542,21 +544,21 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       fold = 2;
       if (dp.out) dp.rest = dp.out + m * p.np;
     }
-    if (m <= kRows<T>) {  // one row block has all of a column's sum
+    if (m <= kRows) {  // one row block has all of a column's sum
       dp.bias = c.dbias;
       dp.sums = nullptr;
     }
     if (dp.out || dp.sums || dp.bias) {
       dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias ? (dp.width + kCols<T> - 1) / kCols<T> : 0);  // (m 0 clears dbias)
       if (dp.blocks > 0)
-        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves<T>), 0, s, dp, Matrix{}, Matrix{});
+        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
     }
     rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
     if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
   }
   if (dp.sums)
-    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + kRows<T> - 1) / kRows<T>, n,
+    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + dp.rows_per - 1) / dp.rows_per, n,
                        dp.width, static_cast<T *>(c.dbias));
   Args g{};
   if (c.da && m > 0 && k > 0) {

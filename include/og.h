@@ -462,7 +462,7 @@ int64_t og_gemm_nt_epi_workspace(int64_t m, int64_t n, int64_t k, int type);
  * the type for dA and dW (up to 128 rows with its remainder, rounded too), not for dbias.  fp32: each row of dP and column of W (for
  * dA), each column of dP and of A (for dW) is held as two fp16 planes by a power
  * of two of its own, as above; up to 32 rows take 24 bits.  dbias is summed in fp32
- * by 32 rows (128 of fp32) and in 64 bits over those.
+ * by 32 or 64 rows and in 64 bits over those.
  * Requirements as above, with a workspace of og_gemm_nt_epi_grad_workspace(m, n, k, type)
  * bytes; W is read for dA only, A for dW only.  The outputs must not overlap the
  * inputs.  m == 0 clears dW and dbias, n == 0 dA.
