@@ -628,14 +628,24 @@ def gemm_nt_epi_grad(dC, A, B, pre=None, act=None, need=(True, True, True), dA=N
     return tuple(outs)
 
 
+def _dense(t) -> bool:
+    """Whether the elements follow one another in memory, in whatever order of dimensions."""
+    n = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
 def _run_of(t):
     """(rows, cols, row stride) of a tensor as runs of elements: one run where its elements
     follow one another in memory."""
-    if t.is_contiguous() or (t.dim() == 2 and t.t().is_contiguous()):
+    if t.is_contiguous() or _dense(t):
         return 1, t.numel(), t.numel()
     if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) >= t.shape[1]:
         return t.shape[0], t.shape[1], t.stride(0)
-    raise ValueError("a gradient must be contiguous, or 2-D with contiguous rows or columns")
+    raise ValueError("a gradient must be dense, or 2-D with contiguous rows")
 
 
 def _grads(grads, out):
@@ -670,8 +680,8 @@ def _grads(grads, out):
 
 def grad_norm(grads, workspace=None):
     """The Euclidean norm over all elements of the tensors `grads` (og_grad_norm), a tensor of
-    one float32.  Types float32, bfloat16 and float16, mixed as they come; contiguous tensors
-    or 2-D ones with contiguous rows or columns."""
+    one float32.  Types float32, bfloat16 and float16, mixed as they come; dense tensors, in
+    any order of their dimensions, or 2-D ones with contiguous rows."""
     return _grad_norm(list(grads), None, None, 0.0, workspace)
 
 

@@ -108,7 +108,7 @@ struct Chunk {
 template <class T, int W, int MT, int NT>
 __global__ __launch_bounds__(W * 64) void rows_kernel(Rows p) {
   using C = Chunk<T, MT, NT>;
-  __shared__ float sums[W][16 * MT][16 * NT + 4];
+  __shared__ __align__(16) float sums[W][16 * MT][16 * NT + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int across = (p.n + 16 * NT - 1) / (16 * NT), below = blockIdx.x / across;

@@ -429,10 +429,10 @@ int64_t og_linear_cross_entropy_workspace(int64_t n, int64_t v, int64_t d, int t
  *
  * act is OG_ACT_NONE to OG_ACT_SILU; it takes the fp32 v, not the rounded P, which
  * is there for og_gemm_nt_epi_grad.  P and C are rounded to the type once.
- * 16-bit tensors are multiplied as they are; of up to 64 fp32 rows 24 bits are, of
- * more (where the product is not small) each row of A and W is held as two fp16
- * planes times a power of two of its own: 22 bits of each value, down to 2^-38 of
- * the row's largest.  An fp32 row
+ * 16-bit tensors are multiplied as they are; of up to 64 fp32 rows 24 bits are (of
+ * values above 2^-102), of more (where the product is not small) each row of A and W is
+ * held as two fp16 planes times a power of two of its own: 22 bits of each value,
+ * down to 2^-38 of the row's largest.  An fp32 row
  * that holds an infinity or NaN makes the sums it enters NaN or infinite; 16-bit ones
  * follow the formula.  act of -infinity is -0 (OG_ACT_NONE: itself; OG_ACT_RELU: +0), of NaN NaN.
  * The residual may be C itself with the same stride; P must not be C, and neither may

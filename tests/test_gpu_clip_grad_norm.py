@@ -101,6 +101,25 @@ def test_strides(dtype):
     check([was[:, :200], was[:, 100:300]], out, norm, 3.0, 1e-6)
 
 
+@pytest.mark.parametrize("dtype", EVERY)
+def test_dense_in_any_order(dtype):
+    """Convolution weights with the channels last, permuted tensors, single elements of any stride;
+    a slice of one is refused and nothing is written."""
+    th = torch()
+    flat = tensors([(24 * 5 * 3 * 3,)], (dtype,))[0]
+    views = [flat.view(24, 3, 3, 5).permute(0, 3, 1, 2), tensors([(7, 6, 5)], (dtype,))[0].permute(2, 0, 1),
+             tensors([(9, 4)], (dtype,))[0][3:4, 1:2], tensors([(9, 4)], (dtype,))[0][:, 2:3]]
+    was = [v.clone() for v in views]
+    out = [th.empty_like(v) for v in views]
+    assert out[0].stride() == views[0].stride()
+    check(was, out, og.clip_grad_norm(views, 0.7, out=out), 0.7, 1e-6)
+    check(was, views, og.clip_grad_norm(views, 0.7), 0.7, 1e-6)
+    kept = flat.clone()
+    with pytest.raises(ValueError):
+        og.clip_grad_norm([views[0][:, :4]], 0.1)
+    assert th.equal(flat, kept)
+
+
 @pytest.mark.parametrize("scale", [1e30, 1e-30, 3e-39])
 def test_range(scale):
     """Squares outside fp32's range, subnormal values."""
