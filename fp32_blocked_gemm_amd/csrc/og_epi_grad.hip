@@ -55,7 +55,7 @@ struct Matrix {
   float *sums;            // column sums of the block's rows, [row block][width] (null: not wanted)
   int rows_per;           // rows of a block
   float *plain;           // fp32 of few rows: the values (null: not wanted)
-  void *bias;             // a single row block: the column sums' own place (null: sums)
+  void *bias;             // where the column sums go in the end; without sums, of a single row block, at once
   int blocks;             // of a launch
 };
 
@@ -92,13 +92,34 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, Lane<T
   });
 }
 
-// One sweep over up to three matrices.  LAYOUT: the planes (fp32); else the values, their sums
-// and largest magnitudes.
+// dbias from the row blocks' sums: 64 columns a block, the row blocks by its waves in turn, in a
+// fixed order in 64 bits.
+template <class T, int WAVES>
+__device__ __forceinline__ void bias_columns(const Matrix &a, int block, double (&of)[WAVES][64]) {
+  const int c = block * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  const int blocks = (a.rows + a.rows_per - 1) / a.rows_per;
+  double sum = 0;
+  if (c < a.cols)
+    for (int b = w; b < blocks; b += WAVES) sum += (double)a.sums[(int64_t)b * a.width + c];
+  of[w][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (w || c >= a.cols) return;
+  for (int k = 1; k < WAVES; ++k) sum += of[k][threadIdx.x];
+  static_cast<T *>(a.bias)[c] = (T)(float)sum;
+}
+
+// One sweep over up to three matrices.  LAYOUT: the planes (fp32), and in blocks behind all others
+// dbias from m0's sums; else the values, their sums and largest magnitudes.
 template <class T, bool LAYOUT>
 __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
   constexpr int H = kPer<T> / 4;
   __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves][64];
   int block = blockIdx.x;
+  if constexpr (LAYOUT) {
+    const int all = m0.blocks + m1.blocks + m2.blocks;
+    if (block >= all)
+      return bias_columns<T, kWaves>(m0, block - all, *reinterpret_cast<double(*)[kWaves][64]>(of_waves));
+  }
   const Matrix &a = block < m0.blocks ? m0 : block < m0.blocks + m1.blocks ? m1 : m2;
   block -= block < m0.blocks ? 0 : block < m0.blocks + m1.blocks ? m0.blocks : m0.blocks + m1.blocks;
   const int across = (a.width + kCols<T> - 1) / kCols<T>, rb = block / across;
@@ -181,7 +202,7 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
 #pragma unroll
       for (int h = 0; h < H; ++h) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c + 4 * h) = sum[h];
     }
-    if (a.bias) {
+    if (a.bias && !a.sums) {
 #pragma unroll
       for (int h = 0; h < H; ++h) store4(static_cast<T *>(a.bias) + c + 4 * h, sum[h], a.cols - c - 4 * h, false);
     }
@@ -200,19 +221,10 @@ __global__ __launch_bounds__(256) void clear_kernel(float *p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
-// dbias from the row blocks' sums: 64 columns a block, 16 threads each, in a fixed order in 64 bits.
 template <class T>
-__global__ __launch_bounds__(1024) void bias_kernel(const float *sums, int blocks, int cols, int width, T *out) {
+__global__ __launch_bounds__(1024) void bias_kernel(Matrix a) {
   __shared__ double of[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
-  double sum = 0;
-  if (c < cols)
-    for (int b = w; b < blocks; b += 16) sum += (double)sums[(int64_t)b * width + c];
-  of[w][threadIdx.x & 63] = sum;
-  __syncthreads();
-  if (w || c >= cols) return;
-  for (int k = 1; k < 16; ++k) sum += of[k][threadIdx.x];
-  out[c] = (T)(float)sum;
+  bias_columns<T, 16>(a, blockIdx.x, of);
 }
 
 // Few fp32 rows of dC and A (up to kFew): bound by the bytes of W, read, and of dW, written.  Both
@@ -490,6 +502,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   dp.width = (int)p.np;
   dp.vec_x = lanes_whole<T>(c.dc, c.lddc);
   dp.vec_p = lanes_whole<T>(c.pre, c.ldp);
+  dp.bias = c.dbias;
   dp.sums = c.dbias ? reinterpret_cast<float *>(c.ws + p.sums_at) : nullptr;
   Operand rows, cols, A, W;  // dP by rows and by columns, A, W
   const float *rtop = nullptr, *ctop = nullptr, *atop = nullptr, *wtop = nullptr;
@@ -528,8 +541,11 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
                        tops, total);
     if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
-    if (blocks > 0 && (c.da || c.dw))
-      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
+    if (blocks > 0 && (c.da || c.dw)) {
+      const int behind = dp.sums ? (n + 63) / 64 : 0;
+      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks + behind), dim3(64 * kWaves), 0, s, dp, ma, mw);
+      dp.sums = nullptr;  // (done)
+    }
     rows = Operand{at(p.p_at), 2 * p.np, 0};
     cols = Operand{at(p.pc_at), 2 * p.np, 0};
     A = Operand{at(p.a_at), 2 * p.kp, 0};
@@ -544,12 +560,10 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       fold = 2;
       if (dp.out) dp.rest = dp.out + m * p.np;
     }
-    if (m <= kRows) {  // one row block has all of a column's sum
-      dp.bias = c.dbias;
-      dp.sums = nullptr;
-    }
-    if (dp.out || dp.sums || dp.bias) {
-      dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias ? (dp.width + kCols<T> - 1) / kCols<T> : 0);  // (m 0 clears dbias)
+    if (m <= kRows) dp.sums = nullptr;  // one row block has all of a column's sum
+    if (dp.out || dp.bias) {
+      // (m 0 clears dbias)
+      dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias && !dp.sums ? (dp.width + kCols<T> - 1) / kCols<T> : 0);
       if (dp.blocks > 0)
         hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
     }
@@ -557,9 +571,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
     if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
     if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
   }
-  if (dp.sums)
-    hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp.sums, (m + dp.rows_per - 1) / dp.rows_per, n,
-                       dp.width, static_cast<T *>(c.dbias));
+  if (dp.sums) hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp);
   Args g{};
   if (c.da && m > 0 && k > 0) {
     g.a = rows, g.b = W, g.M = fold * m, g.N = k, g.K = n;
