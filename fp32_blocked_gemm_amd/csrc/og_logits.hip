@@ -140,9 +140,11 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
           now[e] = (T)steps((float)now[e], c[e], bias ? add[e] : 0.0f, allowed & (1u << e));
         *reinterpret_cast<T8 *>(o + i) = now;
       } else {
-        for (int k = i; k < size; ++k)
-          o[k] = (T)steps((float)z[k], p.tokens ? counts[k] : 0, bias ? bias[k] : 0.0f,
-                          mask ? mask[k >> 5] >> (k & 31) & 1 : 1);
+        for (int k = i; k < size; ++k) {
+          const uint32_t c = p.tokens ? counts[k] : 0;
+          if (!all && !c) continue;
+          o[k] = (T)steps((float)z[k], c, bias ? bias[k] : 0.0f, mask ? mask[k >> 5] >> (k & 31) & 1 : 1);
+        }
       }
     }
   } else {

@@ -168,3 +168,20 @@ def test_more_rows_than_a_launch_has():
     for rows in (slice(0, 40), slice(65500, 65570), slice(n - 40, n)):
         part = {k: x[rows] for k, x in c.items()}
         check(part, got[rows])
+
+
+@pytest.mark.parametrize("width", [1032, 1028, 1027])
+def test_in_place_leaves_other_logits_alone(width):
+    """Without bias and mask only the row's tokens are written: any bits of the others stay, of a
+    NaN too."""
+    th = torch()
+    z = th.full((2, 1032), 0x7FA12345, dtype=th.int32, device="cuda").view(th.float32)
+    view = z[:, :width]
+    tokens = th.tensor([[3, width - 1, 3], [700, 0, -1]], device="cuda")
+    for i in range(2):
+        view[i, tokens[i][tokens[i] >= 0]] = 2.0
+    before = z.view(th.int32).clone()
+    og.logit_penalties(view, tokens, frequency=th.ones(2, device="cuda"), out=view)
+    changed = (z.view(th.int32) != before).nonzero().tolist()
+    assert changed == [[0, 3], [0, width - 1], [1, 0], [1, 700]]
+    assert view[0, 3] == 0 and view[0, width - 1] == 1 and view[1, 0] == view[1, 700] == 1
