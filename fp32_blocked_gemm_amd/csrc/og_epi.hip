@@ -306,7 +306,7 @@ og_status og_gemm_nt_epi(int64_t m, int64_t n, int64_t k, const void *A, int64_t
     return fail(OG_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if ((st = check_device()) != OG_OK) return st;
   const Call c{m, n, k, A, W, lda, ldw,
-               Finish{nullptr, nullptr, 0, bias, act, residual, ldr, P, ldp, C, ldc, 0, 0, 0, 0, 0},
+               Finish{nullptr, nullptr, bias, act, residual, ldr, P, ldp, C, ldc, 0, 0, 0, 0, 0},
                static_cast<char *>(workspace)};
   if (type == OG_F32) forward<float>(c, p, current_stream());
   else if (type == OG_BF16) forward<__bf16>(c, p, current_stream());

@@ -161,11 +161,10 @@ __device__ __forceinline__ void store_planes(uint16_t *out, int c, f32x4 v, cons
 }
 
 // What becomes of a finished sum at (m, n):
-//   v = sum 2^(up - the powers of its row and column) + bias[n];  P = v;  C = act(v) + residual
+//   v = sum 2^-(the powers of its row and column) + bias[n];  P = v;  C = act(v) + residual
 // (out is C of a forward product, dA or dW of the gradient's).
 struct Finish {
-  const float *mtop, *ntop;  // fp32: the largest magnitudes that give the powers; else null
-  int up;
+  const float *mtop, *ntop;  // operands held by powers of two: the magnitudes that give them; else null
   const void *bias;
   int act;
   const void *residual;
@@ -188,15 +187,17 @@ Finish set_accesses(Finish f) {
   return f;
 }
 
-template <class T>
+// Whether the operands of a product may be held by powers of two: fp32 ones, and fp16 ones of the
+// gradient (PLAIN).
+template <class T, bool PLAIN>
+constexpr bool kPowers = kPlanes<T> == 2 || (PLAIN && std::is_same_v<T, _Float16>);
+
+template <class T, bool PLAIN>
 __device__ __forceinline__ void scale(const Finish &f, f32x4 &v, int mpower, const int (&npower)[4]) {
-  if constexpr (kPlanes<T> == 2) {
+  if constexpr (kPowers<T, PLAIN>) {
+    if (kPlanes<T> == 2 || f.mtop) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], -mpower - npower[e]);
-  } else {
-    if (f.up) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], f.up);
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], -mpower - npower[e]);
     }
   }
 }
@@ -206,7 +207,7 @@ template <class T, bool PLAIN>
 __device__ __forceinline__ void of_columns(const Finish &f, int n, int left, int (&npower)[4], f32x4 &bias) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) npower[e] = 0;
-  if constexpr (kPlanes<T> == 2) {
+  if constexpr (kPowers<T, PLAIN>) {
     if (f.ntop) {
       const f32x4 top = load4(f.ntop + n, left, true);
 #pragma unroll
@@ -215,9 +216,9 @@ __device__ __forceinline__ void of_columns(const Finish &f, int n, int left, int
   }
   if (!PLAIN && f.bias) bias = load4(static_cast<const T *>(f.bias) + n, left, f.vec_b);
 }
-template <class T>
+template <class T, bool PLAIN>
 __device__ __forceinline__ int of_row(const Finish &f, int m) {
-  if constexpr (kPlanes<T> == 2) return f.mtop ? power_of(f.mtop[m]) : 0;
+  if constexpr (kPowers<T, PLAIN>) return f.mtop ? power_of(f.mtop[m]) : 0;
   return 0;
 }
 
@@ -227,7 +228,7 @@ __device__ __forceinline__ void finish(const Finish &f, int64_t m, int n, int le
   int npower[4];
   f32x4 bias = {0, 0, 0, 0};
   of_columns<T, PLAIN>(f, n, left, npower, bias);
-  scale<T>(f, v, of_row<T>(f, (int)m), npower);
+  scale<T, PLAIN>(f, v, of_row<T, PLAIN>(f, (int)m), npower);
   if constexpr (!PLAIN) {
     v += bias;
     if (f.pre) store4(static_cast<T *>(f.pre) + m * f.ldp + n, v, left, f.vec_p);
@@ -278,13 +279,13 @@ struct Store {
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
       const uint32_t r = row + 16 * i;
-      const int mpower = of_row<T>(f, t.m0 + r);
+      const int mpower = of_row<T, PLAIN>(f, t.m0 + r);
 #pragma unroll
       for (int j = 0; j < S::FN; ++j) {
         const uint32_t c = (col + 16 * j) * sizeof(T);
         f32x4 v = acc[i][j];
         T4 h;
-        scale<T>(f, v, mpower, npower[j]);
+        scale<T, PLAIN>(f, v, mpower, npower[j]);
         if constexpr (!PLAIN) {
           v += bias[j];
           if (pre) {

@@ -12,8 +12,15 @@
 // throughout, whose result is rounded once (0.0024 and 0.0017 in bf16).  Up to 128
 // rows, where single outputs hang on few roundings and the bytes of W bound the
 // time, what a smooth activation's dP leaves to its rounding is kept as a second matrix below the
-// first (A comes twice for it): 1.05 times.  fp16 holds half of dP where the
-// slope may pass 1, so that none that dC holds overflows.
+// first (A comes twice for it): 1.05 times.  For more rows of bf16 that was measured and is left out: the
+// gradient of 4096 x 11008 x 4096 takes 644 us, with the remainder 1335, with dP, W and A in fp16 by powers
+// of two 816; of 1000 x 4096 x 4096 100, 171 and 136.
+//
+// fp16 holds a smooth activation's dP by powers of two, as below, so that neither
+// small values become subnormal nor large ones, times a slope above 1, infinite (256 x
+// 512 x 256 with dC of 1e-5: errors of dW 5.6e-3 with dP as it is, 3.1e-4 so, 2.4e-4 of the result's
+// rounding); W and A are as they lie.  The largest magnitudes cost a sweep: 4096 x 11008 x 4096 663 and
+// 804 us, 200 x 4096 x 4096 50 and 68.
 //
 // fp32: two fp16 planes.  A product's powers of two belong to the indices that
 // it does not sum over, so that every row and column of a gradient keeps the bits
@@ -26,13 +33,12 @@ namespace og::epi::grad {
 
 // A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
 // (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
-// dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).  fp32 takes
-// more rows a block where there are many, for fewer atomics on a column's maximum (all of the gradient,
+// dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).  Maxima take
+// more rows a block where there are many, for fewer atomics on a column's (all of the gradient,
 // 4096 x 1536 x 384: 32 rows 108 us, 64 104, without the atomics 97; 300 x 1001 x 3001: 68 and 78).
 constexpr int kWaves = 8, kRows = 32;
-template <class T>
-int rows_per(int64_t rows) {
-  return kPlanes<T> == 2 && rows >= 2048 ? 2 * kRows : kRows;
+int rows_per(int64_t rows, bool held) {
+  return held && rows >= 2048 ? 2 * kRows : kRows;
 }
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
@@ -47,11 +53,10 @@ struct Matrix {
   int act;
   int rows, cols, width;  // width: padded columns of the outputs
   int vec_x, vec_p;
-  int halve;              // fp16: the output is half the value
-  uint16_t *out;          // 16-bit types: the values (null: not wanted); fp32: planes by the row's power
-  uint16_t *out_c;        // fp32: planes by the column's power
-  uint16_t *rest;         // 16-bit types: what the rounding of out leaves (null: not wanted)
-  float *rtop, *ctop;     // fp32: largest magnitudes (null: not wanted)
+  uint16_t *out;          // null: not wanted; else the values or (LAYOUT) what the row's power makes of them in fp16
+  uint16_t *out_c;        // LAYOUT: by the column's power (null: not wanted)
+  int twice;              // 16-bit types: below each output the same size again, what its rounding leaves
+  float *rtop, *ctop;     // largest magnitudes (null: not wanted)
   float *sums;            // column sums of the block's rows, [row block][width] (null: not wanted)
   int rows_per;           // rows of a block
   float *plain;           // fp32 of few rows: the values (null: not wanted)
@@ -92,6 +97,37 @@ __device__ __forceinline__ void values(const Matrix &a, int64_t i, int c, Lane<T
   });
 }
 
+// A lane's values rounded to a 16-bit type, and (rest not null) what that leaves of the finite ones, rounded too.
+template <class T>
+__device__ __forceinline__ void store_rounded(T *to, T *rest, const float (&v)[8]) {
+  typedef T V __attribute__((ext_vector_type(8)));
+  V w;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = (T)v[e];
+  *reinterpret_cast<V *>(to) = w;
+  if (rest) {
+    V r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = (T)(__builtin_isfinite((float)w[e]) ? v[e] - (float)w[e] : 0.0f);
+    *reinterpret_cast<V *>(rest) = r;
+  }
+}
+
+// Row i's columns from c on times 2^e: fp32 as two fp16 planes, fp16 as it is.
+template <class T>
+__device__ __forceinline__ void store_scaled(const Matrix &a, uint16_t *out, int64_t i, int c, const Lane<T> &v,
+                                             const int (&e)[kPer<T>]) {
+  if constexpr (kPlanes<T> == 2) {
+    store_planes(out + i * a.width * 2, c, v.v[0], e);
+  } else {
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = __builtin_ldexpf(v.v[q / 4][q % 4], e[q]);
+    _Float16 *to = reinterpret_cast<_Float16 *>(out) + i * a.width + c;
+    store_rounded(to, a.twice ? to + (int64_t)a.rows * a.width : nullptr, x);
+  }
+}
+
 // dbias from the row blocks' sums: 64 columns a block, the row blocks by its waves in turn, in a
 // fixed order in 64 bits.
 template <class T, int WAVES>
@@ -108,12 +144,12 @@ __device__ __forceinline__ void bias_columns(const Matrix &a, int block, double 
   static_cast<T *>(a.bias)[c] = (T)(float)sum;
 }
 
-// One sweep over up to three matrices.  LAYOUT: the planes (fp32), and in blocks behind all others
-// dbias from m0's sums; else the values, their sums and largest magnitudes.
-template <class T, bool LAYOUT>
+// One sweep over up to three matrices.  LAYOUT: the operands by powers of two, and in blocks behind all
+// others dbias from m0's sums; else the values and their sums, or (TOPS) their largest magnitudes and sums.
+template <class T, bool LAYOUT, bool TOPS>
 __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1, Matrix m2) {
   constexpr int H = kPer<T> / 4;
-  __shared__ f32x4 of_waves[LAYOUT ? 1 : 2 * H][kWaves][64];
+  __shared__ f32x4 of_waves[LAYOUT ? 1 : TOPS ? 2 * H : H][kWaves][64];
   int block = blockIdx.x;
   if constexpr (LAYOUT) {
     const int all = m0.blocks + m1.blocks + m2.blocks;
@@ -128,19 +164,22 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
   const int64_t i0 = (int64_t)rb * a.rows_per + wave, end = min((int64_t)(rb + 1) * a.rows_per, (int64_t)a.rows);
   if constexpr (LAYOUT) {
     if (c >= a.width) return;
-    int cpower[4] = {0, 0, 0, 0};
+    int cpower[kPer<T>] = {};
     if (a.out_c) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
+      for (int e = 0; e < kPer<T>; ++e) cpower[e] = c + e < a.cols ? power_of(a.ctop[c + e]) : 0;
     }
     for (int64_t i = i0; i < end; i += kWaves) {
       Lane<T> v;
       values<T>(a, i, c, v);
       if (a.out) {
-        const int p = power_of(a.rtop[i]), powers[4] = {p, p, p, p};
-        store_planes(a.out + i * a.width * 2, c, v.v[0], powers);
+        const int p = power_of(a.rtop[i]);
+        int powers[kPer<T>];
+#pragma unroll
+        for (int e = 0; e < kPer<T>; ++e) powers[e] = p;
+        store_scaled<T>(a, a.out, i, c, v, powers);
       }
-      if (a.out_c) store_planes(a.out_c + i * a.width * 2, c, v.v[0], cpower);
+      if (a.out_c) store_scaled<T>(a, a.out_c, i, c, v, cpower);
     }
   } else {
     f32x4 sum[H], top[H];
@@ -153,66 +192,53 @@ __global__ __launch_bounds__(64 * kWaves) void sweep_kernel(Matrix m0, Matrix m1
       for (int h = 0; h < H; ++h) sum[h] += v.v[h];
       if constexpr (kPlanes<T> == 2) {
         if (a.plain && c < a.width) *reinterpret_cast<f32x4 *>(a.plain + i * a.width + c) = v.v[0];
-        f32x4 size;
+      }
+      if constexpr (TOPS) {
+        float most = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = v.v[0][e];
-          size[e] = __builtin_isfinite(x) ? fabsf(x) : 0.0f;
-          top[0][e] = fmaxf(top[0][e], size[e]);
+        for (int e = 0; e < kPer<T>; ++e) {
+          const float x = v.v[e / 4][e % 4], size = __builtin_isfinite(x) ? fabsf(x) : 0.0f;
+          top[e / 4][e % 4] = fmaxf(top[e / 4][e % 4], size);
+          most = fmaxf(most, size);
         }
         if (a.rtop) {
-          const float most = wave_max(fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3])));
+          most = wave_max(most);
           if (lane == 0 && most > 0)
             atomicMax(reinterpret_cast<uint32_t *>(a.rtop + i), __builtin_bit_cast(uint32_t, most));
         }
       } else if (a.out && c < a.width) {
-        typedef T V __attribute__((ext_vector_type(kPer<T>)));
-        V w;
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < kPer<T>; ++e) w[e] = (T)(a.halve ? 0.5f * v.v[e / 4][e % 4] : v.v[e / 4][e % 4]);
-        *reinterpret_cast<V *>(reinterpret_cast<T *>(a.out) + i * a.width + c) = w;
-        if (a.rest) {
-          V r;
-#pragma unroll
-          for (int e = 0; e < kPer<T>; ++e) {
-            const float whole = a.halve ? 0.5f * v.v[e / 4][e % 4] : v.v[e / 4][e % 4], held = (float)w[e];
-            r[e] = (T)(__builtin_isfinite(held) ? whole - held : 0.0f);
-          }
-          *reinterpret_cast<V *>(reinterpret_cast<T *>(a.rest) + i * a.width + c) = r;
-        }
+        for (int e = 0; e < 8; ++e) x[e] = v.v[e / 4][e % 4];
+        T *to = reinterpret_cast<T *>(a.out) + i * a.width + c;
+        store_rounded(to, a.twice ? to + (int64_t)a.rows * a.width : nullptr, x);
       }
     }
     if (!a.sums && !a.ctop && !a.bias) return;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       of_waves[h][wave][lane] = sum[h];
-      if (kPlanes<T> == 2) of_waves[H + h][wave][lane] = top[h];
+      if (TOPS) of_waves[H + h][wave][lane] = top[h];
     }
     __syncthreads();
-    if (wave || c >= a.width) return;
-    for (int w = 1; w < kWaves; ++w) {
+    // a column a thread, the waves in turn
+    const int q = threadIdx.x, column = (block - rb * across) * kCols<T> + q;
+    if (q >= kCols<T> || column >= a.width) return;
+    auto held = [&](int w, int what) __attribute__((always_inline)) {
+      return of_waves[what * H + q % kPer<T> / 4][w][q / kPer<T>][q % 4];
+    };
+    float total = held(0, 0);
 #pragma unroll
-      for (int h = 0; h < H; ++h) sum[h] += of_waves[h][w][lane];
-      if constexpr (kPlanes<T> == 2) {
+    for (int w = 1; w < kWaves; ++w) total += held(w, 0);
+    if (a.sums) a.sums[(int64_t)rb * a.width + column] = total;
+    if (column >= a.cols) return;
+    if (a.bias && !a.sums) static_cast<T *>(a.bias)[column] = (T)total;
+    if constexpr (TOPS) {
+      if (!a.ctop) return;
+      float most = held(0, 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[0][e] = fmaxf(top[0][e], of_waves[H][w][lane][e]);
-      }
-    }
-    if (a.sums) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) *reinterpret_cast<f32x4 *>(a.sums + (int64_t)rb * a.width + c + 4 * h) = sum[h];
-    }
-    if (a.bias && !a.sums) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) store4(static_cast<T *>(a.bias) + c + 4 * h, sum[h], a.cols - c - 4 * h, false);
-    }
-    if (kPlanes<T> == 2 && a.ctop) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float most = top[0][e];  // (a bit cast of a vector's element takes the first one's bits)
-        if (c + e < a.cols && most > 0)
-          atomicMax(reinterpret_cast<uint32_t *>(a.ctop + c + e), __builtin_bit_cast(uint32_t, most));
-      }
+      for (int w = 1; w < kWaves; ++w) most = fmaxf(most, held(w, 1));
+      if (most > 0) atomicMax(reinterpret_cast<uint32_t *>(a.ctop + column), __builtin_bit_cast(uint32_t, most));
     }
   }
 }
@@ -394,10 +420,11 @@ Plan plan(int64_t m, int64_t n, int64_t k) {
     p.total = r.at;
     return p;
   }
-  p.tops_at = r.take(P == 2 ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
-  const int fold = P == 1 && m <= kTwice ? 2 : 1;  // (whatever the activation)
+  // (whatever the activation)
+  const int fold = P == 1 && m <= kTwice ? 2 : 1;
+  p.tops_at = r.take(kPowers<T, true> ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
   p.p_at = r.take(fold * P * m * p.np * 2);
-  p.pc_at = r.take(P == 2 ? P * m * p.np * 2 : 0);
+  p.pc_at = r.take(kPowers<T, true> ? fold * P * m * p.np * 2 : 0);
   p.a_at = r.take(fold * P * m * p.kp * 2);
   p.w_at = r.take(P * n * p.kp * 2);
   p.sums_at = r.take((m + kRows - 1) / kRows * p.np * 4);
@@ -421,11 +448,10 @@ int lanes_whole(const void *p, int64_t ld) {
 }
 
 template <class T>
-Finish output(void *out, int64_t ld, const float *mtop, const float *ntop, int up) {
+Finish output(void *out, int64_t ld, const float *mtop, const float *ntop) {
   Finish f{};
   f.mtop = mtop;
   f.ntop = ntop;
-  f.up = up;
   f.out = out;
   f.ldo = ld;
   return set_accesses<T>(f);
@@ -450,7 +476,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
   if (!place && (c.da || c.dw)) a.plain = reinterpret_cast<float *>(c.ws + p.p_at);
   a.blocks = (a.width + kCols<float> - 1) / kCols<float>;  // (m 0 clears dbias)
   if (a.blocks > 0 && (a.bias || a.plain)) {
-    hipLaunchKernelGGL((sweep_kernel<float, false>), dim3(a.blocks), dim3(64 * kWaves), 0, s, a, Matrix{}, Matrix{});
+    hipLaunchKernelGGL((sweep_kernel<float, false, true>), dim3(a.blocks), dim3(64 * kWaves), 0, s, a, Matrix{}, Matrix{});
   }
   FewRows q{};
   q.m = m, q.n = n, q.k = k;
@@ -460,7 +486,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
   q.lda = c.lda, q.ldw = c.ldw;
   if (c.da) {
     const FewParts parts = few_parts(n, k);
-    q.f = output<float>(c.da, c.ldda, nullptr, nullptr, 0);
+    q.f = output<float>(c.da, c.ldda, nullptr, nullptr);
     q.vec = whole(q.w, q.ldw);
     q.steps = parts.steps;
     if (parts.parts > 1) {
@@ -478,7 +504,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
     }
   }
   if (c.dw) {
-    q.f = output<float>(c.dw, c.lddw, nullptr, nullptr, 0);
+    q.f = output<float>(c.dw, c.lddw, nullptr, nullptr);
     hipLaunchKernelGGL(few_dw_kernel, dim3((k + 255) / 256, (n + kTall - 1) / kTall), dim3(256), 0, s, q);
   }
 }
@@ -490,8 +516,11 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   const int m = (int)c.m, n = (int)c.n, k = (int)c.k;
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
+  const bool rounds = P == 1 && m > 0 && c.act > OG_ACT_RELU;  // dP has more bits than the type
+  const int fold = rounds && m <= kTwice ? 2 : 1;
+  const bool held = P == 2 || (kPowers<T, true> && rounds);  // dP (fp32: A and W too) by powers of two
   Matrix dp{};
-  dp.rows_per = rows_per<T>(m);
+  dp.rows_per = rows_per(m, held);
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
@@ -506,68 +535,72 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   dp.sums = c.dbias ? reinterpret_cast<float *>(c.ws + p.sums_at) : nullptr;
   Operand rows, cols, A, W;  // dP by rows and by columns, A, W
   const float *rtop = nullptr, *ctop = nullptr, *atop = nullptr, *wtop = nullptr;
-  int up = 0, fold = 1;
-  if constexpr (P == 2) {
-    float *tops = reinterpret_cast<float *>(c.ws + p.tops_at);
-    float *r = tops, *t = r + round_up(m, 64), *ta = t + round_up(n, 64), *tw = ta + round_up(k, 64);
-    const int64_t total = tw + round_up(k, 64) - tops;
-    auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
-      Matrix a{};
-      a.rows_per = rows_per<T>(count);
-      a.x = x;
-      a.ldx = ld;
-      a.rows = (int)count;
-      a.cols = k;
-      a.width = (int)p.kp;
-      a.vec_x = lanes_whole<T>(x, ld);
-      a.ctop = top;
-      a.out_c = out;
-      return a;
-    };
-    Matrix ma{}, mw{};
-    ma.rows_per = mw.rows_per = kRows;
-    if (c.da) {
-      dp.rtop = r;
-      dp.out = at(p.p_at);
-      mw = of(c.w, c.ldw, n, tw, at(p.w_at));
+  dp.twice = fold == 2;
+  if (P == 1 && m <= kRows) dp.sums = nullptr;  // one row block has all of a column's sum
+  if constexpr (kPowers<T, true>) {
+    if (held) {
+      float *tops = reinterpret_cast<float *>(c.ws + p.tops_at);
+      float *r = tops, *t = r + round_up(m, 64), *ta = t + round_up(n, 64), *tw = ta + round_up(k, 64);
+      const int64_t total = tw + round_up(k, 64) - tops;
+      auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
+        Matrix a{};
+        a.rows_per = rows_per(count, true);
+        a.x = x;
+        a.ldx = ld;
+        a.rows = (int)count;
+        a.cols = k;
+        a.width = (int)p.kp;
+        a.vec_x = lanes_whole<T>(x, ld);
+        a.ctop = top;
+        a.out_c = out;
+        return a;
+      };
+      Matrix ma{}, mw{};
+      ma.rows_per = mw.rows_per = kRows;
+      if (c.da) {
+        dp.rtop = r;
+        dp.out = at(p.p_at);
+        if (P == 2) mw = of(c.w, c.ldw, n, tw, at(p.w_at));
+      }
+      if (c.dw) {
+        dp.ctop = t;
+        dp.out_c = at(p.pc_at);
+        if (P == 2) ma = of(c.a, c.lda, m, ta, at(p.a_at));
+      }
+      for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks<T>(*x);
+      const int blocks = dp.blocks + ma.blocks + mw.blocks;
+      hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
+                         tops, total);
+      if (blocks > 0)
+        hipLaunchKernelGGL((sweep_kernel<T, false, true>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
+      if (blocks > 0 && (c.da || c.dw)) {
+        const int behind = dp.sums ? (n + 63) / 64 : 0;
+        hipLaunchKernelGGL((sweep_kernel<T, true, true>), dim3(blocks + behind), dim3(64 * kWaves), 0, s, dp, ma, mw);
+        dp.sums = nullptr;  // (done)
+      }
+      rows = Operand{at(p.p_at), P * p.np, 0};
+      cols = Operand{at(p.pc_at), P * p.np, 0};
+      rtop = r, ctop = t;
+      if (P == 2) {
+        A = Operand{at(p.a_at), P * p.kp, 0};
+        W = Operand{at(p.w_at), P * p.kp, 0};
+        atop = ta, wtop = tw;
+      }
     }
-    if (c.dw) {
-      dp.ctop = t;
-      dp.out_c = at(p.pc_at);
-      ma = of(c.a, c.lda, m, ta, at(p.a_at));
+  }
+  if constexpr (P == 1) {
+    if (!held) {
+      const bool place = same && readable(c.dc, n, c.lddc);
+      dp.out = place || !(c.da || c.dw) ? nullptr : at(p.p_at);
+      if (dp.out || dp.bias) {
+        // (m 0 clears dbias)
+        dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias && !dp.sums ? (dp.width + kCols<T> - 1) / kCols<T> : 0);
+        if (dp.blocks > 0)
+          hipLaunchKernelGGL((sweep_kernel<T, false, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{},
+                             Matrix{});
+      }
+      rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     }
-    for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks<T>(*x);
-    const int blocks = dp.blocks + ma.blocks + mw.blocks;
-    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)std::min<int64_t>((total + 255) / 256, 1024)), dim3(256), 0, s,
-                       tops, total);
-    if (blocks > 0) hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(blocks), dim3(64 * kWaves), 0, s, dp, ma, mw);
-    if (blocks > 0 && (c.da || c.dw)) {
-      const int behind = dp.sums ? (n + 63) / 64 : 0;
-      hipLaunchKernelGGL((sweep_kernel<T, true>), dim3(blocks + behind), dim3(64 * kWaves), 0, s, dp, ma, mw);
-      dp.sums = nullptr;  // (done)
-    }
-    rows = Operand{at(p.p_at), 2 * p.np, 0};
-    cols = Operand{at(p.pc_at), 2 * p.np, 0};
-    A = Operand{at(p.a_at), 2 * p.kp, 0};
-    W = Operand{at(p.w_at), 2 * p.kp, 0};
-    rtop = r, ctop = t, atop = ta, wtop = tw;
-  } else {
-    const bool place = same && readable(c.dc, n, c.lddc);
-    if constexpr (std::is_same_v<T, _Float16>) dp.halve = c.act > OG_ACT_RELU;
-    up = dp.halve;
-    dp.out = place || !(c.da || c.dw) ? nullptr : at(p.p_at);
-    if (m > 0 && m <= kTwice && c.act > OG_ACT_RELU) {
-      fold = 2;
-      if (dp.out) dp.rest = dp.out + m * p.np;
-    }
-    if (m <= kRows) dp.sums = nullptr;  // one row block has all of a column's sum
-    if (dp.out || dp.bias) {
-      // (m 0 clears dbias)
-      dp.blocks = std::max(sweep_blocks<T>(dp), dp.bias && !dp.sums ? (dp.width + kCols<T> - 1) / kCols<T> : 0);
-      if (dp.blocks > 0)
-        hipLaunchKernelGGL((sweep_kernel<T, false>), dim3(dp.blocks), dim3(64 * kWaves), 0, s, dp, Matrix{}, Matrix{});
-    }
-    rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
     if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
   }
@@ -575,11 +608,11 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   Args g{};
   if (c.da && m > 0 && k > 0) {
     g.a = rows, g.b = W, g.M = fold * m, g.N = k, g.K = n;
-    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop, up), c.ws + p.parts_at, s, fold);
+    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop), c.ws + p.parts_at, s, fold);
   }
   if (c.dw && n > 0 && k > 0) {
     g.a = cols, g.b = A, g.M = n, g.N = k, g.K = fold * m;
-    run_product<T, true, true, true>(g, output<T>(c.dw, c.lddw, ctop, atop, up), c.ws + p.parts_at, s);
+    run_product<T, true, true, true>(g, output<T>(c.dw, c.lddw, ctop, atop), c.ws + p.parts_at, s);
   }
 }
 
