@@ -104,13 +104,13 @@ __device__ __forceinline__ double squares(const Tensor &t, int c) {
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-// The factor, m 2^e with 24 bits of m in [1, 2): it may be far below fp32's range, and 1
-// leaves subnormal values as they are.
+// The factor, m 2^e with 24 bits of m in [1/2, 1], e at most 0: it may be far below fp32's range,
+// a product with m cannot leave it, and 1 (m 1) leaves subnormal values as they are.
 struct Factor {
   float m;
   int e;
   __device__ __forceinline__ explicit Factor(double f)
-      : m(2.0f * (float)__builtin_amdgcn_frexp_mant(f)), e(__builtin_amdgcn_frexp_exp(f) - 1) {}
+      : m(f == 1.0 ? 1.0f : (float)__builtin_amdgcn_frexp_mant(f)), e(f == 1.0 ? 0 : __builtin_amdgcn_frexp_exp(f)) {}
   __device__ __forceinline__ float operator()(float x) const { return __builtin_ldexpf(x * m, e); }
 };
 

@@ -505,9 +505,10 @@ og_status og_grad_norm(int64_t count, const og_grad *grads, float *norm, void *w
  *
  * for each tensor, the factor computed in 64 bits and rounded to 24 (of any
  * size), the product rounded to fp32 and to the tensor's type.  Where the factor is 1, y = x
- * bit for bit and tensors in place are not written.  A norm that is infinite
- * makes finite elements 0 and infinite ones NaN, one that is NaN makes all of
- * them NaN (the caller sees it in `norm`).
+ * bit for bit and tensors in place are not written.  An infinite element
+ * makes finite ones 0 and infinite ones NaN, one that is NaN makes all of
+ * them NaN (the caller sees it in `norm`).  The factor takes the norm as summed, in 64 bits:
+ * finite elements whose norm is past fp32's range give an infinite `norm` and are scaled to max_norm.
  * Requirements besides: max_norm and eps finite, >= 0; y non-null and ldy >=
  * cols as for x; no two tensors begin at one y, and no y overlaps another
  * tensor's x or y.
