@@ -261,8 +261,8 @@ void forward(const Call &c, const Plan &p, hipStream_t s) {
     g.a = Operand{a, 2 * p.kp, 0};
     g.b = Operand{w, 2 * p.kp, 0};
   } else {
-    g.a = operand16(c.a, c.lda, c.m, c.k, p.kp, c.ws + p.a_at, s);
-    g.b = operand16(c.w, c.ldw, c.n, c.k, p.kp, c.ws + p.w_at, s);
+    g.a = operand16<T>(c.a, c.lda, c.m, c.k, p.kp, c.ws + p.a_at, s);
+    g.b = operand16<T>(c.w, c.ldw, c.n, c.k, p.kp, c.ws + p.w_at, s);
   }
   run_product<T, false, false, false>(g, f, c.ws + p.parts_at, s);
 }

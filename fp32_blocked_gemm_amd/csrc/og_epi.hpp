@@ -333,19 +333,29 @@ struct Store {
   }
 };
 
-// Adds the parts of a split product in order and finishes.
-template <class T, bool PLAIN>
+// Adds the parts of a split product in order and finishes.  FOLD 2: every part is followed by that of
+// the remainder, which counts where the matrix's own sum is finite (an infinity of the other operand
+// times a remainder of 0, or of the other sign, would make it NaN).
+template <class T, bool PLAIN, int FOLD>
 static __global__ __launch_bounds__(256) void join_kernel(int M, int N, int parts, const float *part, int64_t ld,
                                                    int64_t step, Finish f) {
   const int per = (N + 3) / 4;
   const int64_t total = (int64_t)M * per;
   for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
     const int m = (int)(at / per), n = (int)(at - (int64_t)m * per) * 4;
-    f32x4 v = {0, 0, 0, 0};
+    f32x4 v = {0, 0, 0, 0}, own = {0, 0, 0, 0};
     for (int p = 0; p < parts; ++p) {
-      const f32x4 w = *reinterpret_cast<const f32x4 *>(part + p * step + m * ld + n);
+      const float *at = part + p * (FOLD * step) + m * ld + n;
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(at);
+      v += w;
+      if constexpr (FOLD == 2) {
+        own += w;
+        v += *reinterpret_cast<const f32x4 *>(at + step);
+      }
+    }
+    if constexpr (FOLD == 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += w[e];
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_isfinite(own[e]) ? v[e] : own[e];
     }
     finish<T, PLAIN>(f, m, n, N - n, v);
   }
@@ -437,6 +447,10 @@ int64_t parts_bytes(int64_t M, int64_t N, int64_t K, int fold = 1) {
   return p * fold > 1 ? p * fold * M * round_up(N, 4) * 4 : 0;
 }
 
+// The most matrices below one another that a product's operand has: 16-bit gradients' may be two.
+template <class T, bool PLAIN>
+constexpr int kFold = PLAIN && kPlanes<T> == 1 ? 2 : 1;
+
 // The product, its k in parts where that is faster.  fold 2: the rows of A come twice, as a matrix
 // and its remainder below it (g.M rows in all), whose sums are added like parts.
 template <class T, bool TA, bool TB, bool PLAIN>
@@ -454,8 +468,9 @@ void run_product(Args g, const Finish &f, char *ws, hipStream_t s, int fold = 1)
   if (!e.part) return;
   const int rows = g.M / fold;
   const int64_t quads = (int64_t)rows * ((g.N + 3) / 4);
-  hipLaunchKernelGGL((join_kernel<T, PLAIN>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0,
-                     s, rows, g.N, parts * fold, e.part, e.ld, rows * e.ld, f);
+  const auto join = fold == 1 ? join_kernel<T, PLAIN, 1> : join_kernel<T, PLAIN, kFold<T, PLAIN>>;
+  hipLaunchKernelGGL(join, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, s, rows, g.N, parts,
+                     e.part, e.ld, rows * e.ld, f);
 }
 
 // Whether the tile product can read a 16-bit matrix where it lies.
@@ -542,9 +557,10 @@ struct Fragment<float> {
   }
 };
 
-// Rows of 16-bit values, zero from cols to ld (a multiple of 8); `times` copies one below the other.
+// Rows of 16-bit values, zero from cols to ld (a multiple of 8); times 2: below them once more, with 0
+// for what is not finite (bits of the exponent all set) -- a remainder's product has no more to say there.
 static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int64_t ldx, int rows, int cols,
-                                                          uint16_t *out, int ld, int times) {
+                                                          uint16_t *out, int ld, int times, int exponent) {
   const int per = ld / 8;
   const int64_t total = (int64_t)rows * per;
   for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
@@ -553,18 +569,25 @@ static __global__ __launch_bounds__(256) void copy_kernel(const uint16_t *x, int
     s16x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? (short)x[i * ldx + c + e] : (short)0;
-    for (int t = 0; t < times; ++t) *reinterpret_cast<s16x8 *>(out + (i + (int64_t)t * rows) * ld + c) = v;
+    *reinterpret_cast<s16x8 *>(out + i * ld + c) = v;
+    if (times == 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] & exponent) == exponent ? (short)0 : v[e];
+      *reinterpret_cast<s16x8 *>(out + (i + rows) * ld + c) = v;
+    }
   }
 }
 
-// A 16-bit matrix as an operand, its rows `times` over.
-inline Operand operand16(const void *x, int64_t ld, int64_t rows, int64_t cols, int64_t padded, char *ws, hipStream_t s,
+// A 16-bit matrix as an operand, its rows `times` over (see copy_kernel).
+template <class T>
+Operand operand16(const void *x, int64_t ld, int64_t rows, int64_t cols, int64_t padded, char *ws, hipStream_t s,
                          int times = 1) {
   if (rows == 0 || cols == 0 || (times == 1 && readable(x, cols, ld))) return Operand{static_cast<const uint16_t *>(x), ld, 0};
   uint16_t *to = reinterpret_cast<uint16_t *>(ws);
   const int64_t granules = rows * (padded / 8);
   hipLaunchKernelGGL(copy_kernel, dim3((unsigned)std::min<int64_t>((granules + 255) / 256, 8192)), dim3(256), 0, s,
-                     static_cast<const uint16_t *>(x), ld, (int)rows, (int)cols, to, (int)padded, times);
+                     static_cast<const uint16_t *>(x), ld, (int)rows, (int)cols, to, (int)padded, times,
+                     std::is_same_v<T, __bf16> ? 0x7F80 : 0x7C00);
   return Operand{to, padded, 0};
 }
 

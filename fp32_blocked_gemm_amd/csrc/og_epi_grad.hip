@@ -12,7 +12,8 @@
 // throughout, whose result is rounded once (0.0024 and 0.0017 in bf16).  Up to 128
 // rows, where single outputs hang on few roundings and the bytes of W bound the
 // time, what a smooth activation's dP leaves to its rounding is kept as a second matrix below the
-// first (A comes twice for it): 1.05 times.  For more rows of bf16 that was measured and is left out: the
+// first (A comes twice for it): 1.05 times; where W or A is not finite it is left out, so that infinities
+// follow the formula.  For more rows of bf16 that was measured and is left out: the
 // gradient of 4096 x 11008 x 4096 takes 644 us, with the remainder 1335, with dP, W and A in fp16 by powers
 // of two 816; of 1000 x 4096 x 4096 100, 171 and 136.
 //
@@ -499,7 +500,7 @@ void few_gradient(const Call &c, const Plan &p, hipStream_t s) {
     else hipLaunchKernelGGL(few_da_kernel<2>, grid, dim3(256), 0, s, q);
     if (q.part) {
       const int64_t quads = (int64_t)m * ((k + 3) / 4);
-      hipLaunchKernelGGL((join_kernel<float, true>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
+      hipLaunchKernelGGL((join_kernel<float, true, 1>), dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)),
                          dim3(256), 0, s, m, k, parts.parts, q.part, q.ld, q.step, q.f);
     }
   }
@@ -601,8 +602,8 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       }
       rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     }
-    if (c.dw) A = operand16(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
-    if (c.da) W = operand16(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
+    if (c.dw) A = operand16<T>(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
+    if (c.da) W = operand16<T>(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
   }
   if (dp.sums) hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp);
   Args g{};
