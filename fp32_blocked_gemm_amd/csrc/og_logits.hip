@@ -78,6 +78,10 @@ __device__ __forceinline__ void count(const Problem &p, int64_t row, int v0, int
 struct Steps {
   float r, f, p;
   bool repetition, frequency, presence, bias;
+  // Whether a penalty changes a logit of count c.
+  __device__ __forceinline__ bool penalise(uint32_t c) const {
+    return (c && repetition) || ((c & ~kPrompt) && (frequency || presence));
+  }
   __device__ __forceinline__ float operator()(float x, uint32_t c, float b, uint32_t allowed) const {
     if (c) {
       if (repetition) x = x > 0 ? x / r : x * r;
@@ -134,6 +138,11 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
         if (!all) {
           if (!(c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7])) continue;
           now = *reinterpret_cast<const T8 *>(z + i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)  // (the others keep their bits, of a NaN too; stored one by one: up to 2 us more)
+            if (steps.penalise(c[e])) now[e] = (T)steps((float)now[e], c[e], 0.0f, 1);
+          *reinterpret_cast<T8 *>(o + i) = now;
+          continue;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -142,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
       } else {
         for (int k = i; k < size; ++k) {
           const uint32_t c = p.tokens ? counts[k] : 0;
-          if (!all && !c) continue;
+          if (!all && !steps.penalise(c)) continue;
           o[k] = (T)steps((float)z[k], c, bias ? bias[k] : 0.0f, mask ? mask[k >> 5] >> (k & 31) & 1 : 1);
         }
       }
@@ -170,7 +179,7 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
         const int i = i0 + q * kThreads;
         if (i >= size) continue;
         const uint32_t c = p.tokens ? counts[i] : 0;
-        if (!all && !c) continue;
+        if (!all && !steps.penalise(c)) continue;
         o[i] = (T)steps((float)(all ? in[q] : z[i]), c, b[q], bits[q]);
       }
     }

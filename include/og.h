@@ -539,8 +539,9 @@ int64_t og_grad_norm_workspace(void);
  * outside [0, v) (a padding's) not at all; nothing past a row's length is used.
  * A row whose mask has no bit set is -infinity throughout; a masked logit
  * is -infinity whatever it was.
- * O may be Z itself with the same stride; logits that no step changes are then
- * not written.  Otherwise O must not overlap an input.
+ * O may be Z itself with the same stride; with neither bias nor mask, logits that no
+ * penalty changes then keep their bits, and aligned runs of eight that hold none of the row's
+ * tokens are not written.  Otherwise O must not overlap an input.
  * Requirements: type OG_F32, OG_BF16 or OG_F16; n, v, t >= 0; ldz, ldo >=
  * max(1, v); ldt >= max(1, t); ldb 0 or >= v; ldm 0 or >= ceil(v/32); tokens
  * non-null where t > 0 and a penalty is given; n <= 2^24, v <= 2^28, t < 2^31
