@@ -191,11 +191,22 @@ void launch_rows(const Rows &p, hipStream_t s) {
 // kernel and tile product, W rotating through memory: 16 rows of bf16 on 11008 x 4096 27.4 and 26.9,
 // on 4096 x 4096 10.7 and 12.3; 32 there 17.7 and 12.9; 64 on 1531 x 1000 5.1 and 8.6, 128 6.4 and 8.5.
 // fp32: 64 rows on 11008 x 4096 101 and 148, 128 186 and 153; 128 on 1531 x 1000 12.9 and 15.8.
+//
+// A block takes its time however little of k there is, so that more of them than run at once (four a
+// compute unit) are for tiles, whose blocks are larger: 4096 x 4096 x 16 in bf16 359 and 17 us (fp32 166 and 27),
+// 2048 x 2048 x 32 81 and 10 (37 and 14), 65536 x 64 x 64 74 and 11, 14 x 58422 x 136 26 and 10; but not where
+// 16 rows have much of k each (a block's bytes then take longer), nor narrow fp32 products, for which tiles are
+// half empty and all of A is laid out first (65536 x 64 x 64 28 and 39).  (110 seeded products for each type of 1
+// to 65536 rows, 4 to 65536 columns and k of 4 to 16384: the chosen kernel takes 1.05 times the faster
+// one's time in the mean in bf16, 1.04 in fp32, 110 others 1.02 and 1.03; odd k of some thousands up to 2.9.)
 template <class T>
 bool few_rows(int64_t m, int64_t n, int64_t k) {
   constexpr bool wide = sizeof(T) == 4;
-  const int64_t weights = n * std::max<int64_t>(k, 1);
-  return m <= (wide ? 64 : 16) || (wide ? (m + 31) / 32 * weights <= (1 << 23) : (m + 15) / 16 * weights <= (1 << 24));
+  constexpr int64_t tile = wide ? 32 : 16, most = wide ? 1 << 23 : 1 << 24;
+  const int64_t down = (m + tile - 1) / tile, blocks = down * ((n + tile - 1) / tile);
+  const bool little = down * n * std::max<int64_t>(k, 1) <= most;
+  if constexpr (wide) return m <= 64 || (little && (n <= 64 || blocks <= 1024));
+  return blocks <= 1024 ? m <= 16 || little : m <= 16 && k >= 512;
 }
 
 // Tiles of a block: one of each up to 16 rows and for 16-bit types (11008 x 4096 bf16 by one row
