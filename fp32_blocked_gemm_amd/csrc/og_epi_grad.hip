@@ -35,11 +35,13 @@ namespace og::epi::grad {
 // A block of a sweep: 16 bytes of a row a lane, the rows by the waves in turn, one after another
 // (more of a wave's rows in flight at once cost the registers that more waves hide latency with:
 // dC and P of 4096 x 11008 in bf16, 42 us for their column sums; two rows 53, four 86).  Maxima take
-// more rows a block where there are many, for fewer atomics on a column's (all of the gradient,
-// 4096 x 1536 x 384: 32 rows 108 us, 64 104, without the atomics 97; 300 x 1001 x 3001: 68 and 78).
+// more rows a block where there are many, for fewer atomics on a column's (all of the gradient by 32 and
+// 64 rows a block, fp32: 16384 x 1536 x 384 293 and 280 us, 4096 of them 102 and 103, 300 x 1001 x 3001 65 and
+// 74; fp16: 153 and 140, 62 and 68, 71 and 94).
 constexpr int kWaves = 8, kRows = 32;
+template <class T>
 int rows_per(int64_t rows, bool held) {
-  return held && rows >= 2048 ? 2 * kRows : kRows;
+  return held && rows >= (kPlanes<T> == 2 ? 2048 : 8192) ? 2 * kRows : kRows;
 }
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
@@ -521,7 +523,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   const int fold = rounds && m <= kTwice ? 2 : 1;
   const bool held = P == 2 || (kPowers<T, true> && rounds);  // dP (fp32: A and W too) by powers of two
   Matrix dp{};
-  dp.rows_per = rows_per(m, held);
+  dp.rows_per = rows_per<T>(m, held);
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
@@ -545,7 +547,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       const int64_t total = tw + round_up(k, 64) - tops;
       auto of = [&](const void *x, int64_t ld, int64_t count, float *top, uint16_t *out) {
         Matrix a{};
-        a.rows_per = rows_per(count, true);
+        a.rows_per = rows_per<T>(count, true);
         a.x = x;
         a.ldx = ld;
         a.rows = (int)count;

@@ -49,8 +49,6 @@ struct Problem {
   int in_place;
 };
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 // What a block counts: how often each token of its segment is among the row's.
 __device__ __forceinline__ void count(const Problem &p, int64_t row, int v0, int size, uint32_t *counts) {
   const int tid = threadIdx.x;
