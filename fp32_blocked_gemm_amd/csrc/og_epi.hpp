@@ -188,10 +188,9 @@ Finish set_accesses(Finish f) {
   return f;
 }
 
-// Whether the operands of a product may be held by powers of two: fp32 ones, and fp16 ones of the
-// gradient (PLAIN).
+// Whether the operands of a product may be held by powers of two: fp32 ones, and the gradient's (PLAIN).
 template <class T, bool PLAIN>
-constexpr bool kPowers = kPlanes<T> == 2 || (PLAIN && std::is_same_v<T, _Float16>);
+constexpr bool kPowers = kPlanes<T> == 2 || PLAIN;
 
 template <class T, bool PLAIN>
 __device__ __forceinline__ void scale(const Finish &f, f32x4 &v, int mpower, const int (&npower)[4]) {
@@ -454,9 +453,10 @@ constexpr int kFold = PLAIN && kPlanes<T> == 1 ? 2 : 1;
 
 // The product, its k in parts where that is faster.  fold 2: the rows of A come twice, as a matrix
 // and its remainder below it (g.M rows in all), whose sums are added like parts.
-template <class T, bool TA, bool TB, bool PLAIN>
+// E: the operands' elements.
+template <class T, bool TA, bool TB, bool PLAIN, class E = Element<T>>
 void run_product(Args g, const Finish &f, char *ws, hipStream_t s, int fold = 1) {
-  using C = typename EpiTiles<Element<T>, kPlanes<T>, TA && TB>::type;
+  using C = typename EpiTiles<E, kPlanes<T>, TA && TB>::type;
   const int parts = parts_of<T, TA && TB>(g.M, g.N, g.K);
   StoreArgs e{f, nullptr, 0, 0};
   if (parts * fold > 1) {

@@ -6,22 +6,19 @@
 // (og_tile.hpp) do the rest, with W and A as operands whose rows run along k
 // (the transposing reads).
 //
-// 16-bit types: dP is rounded to the type once (where an activation changes it;
-// else dC is read where it lies), the sums dbias from it before that.  That
-// rounding and P's make errors of dA and dW 1.45 times those of a plain form in fp32
-// throughout, whose result is rounded once (0.0024 and 0.0017 in bf16).  Up to 128
-// rows, where single outputs hang on few roundings and the bytes of W bound the
-// time, what a smooth activation's dP leaves to its rounding is kept as a second matrix below the
-// first (A comes twice for it): 1.05 times; where W or A is not finite it is left out, so that infinities
-// follow the formula.  For more rows of bf16 that was measured and is left out: the
-// gradient of 4096 x 11008 x 4096 takes 644 us, with the remainder 1335, with dP, W and A in fp16 by powers
-// of two 816; of 1000 x 4096 x 4096 100, 171 and 136.
-//
-// fp16 holds a smooth activation's dP by powers of two, as below, so that neither
-// small values become subnormal nor large ones, times a slope above 1, infinite (256 x
-// 512 x 256 with dC of 1e-5: errors of dW 5.6e-3 with dP as it is, 3.1e-4 so, 2.4e-4 of the result's
-// rounding); W and A are as they lie.  The largest magnitudes cost a sweep: 4096 x 11008 x 4096 663 and
-// 804 us, 200 x 4096 x 4096 50 and 68.
+// 16-bit types: dP of no activation or ReLU is of the type, as dC is.  That of a smooth one has more bits; rounded
+// to bf16 it would give dA and dW 1.41 times the error of their own rounding (0.0023 and 0.0017).  So
+//   - bf16 up to 384 rows: what dP leaves to its rounding is a second matrix below the first (A comes twice for
+//     it); where W or A is not finite it is left out, so that infinities follow the formula;
+//   - bf16 of more rows: dP, W and A in fp16, whose 11 bits hold bf16's 8, by powers of two, as below: 1.01
+//     times (4096 x 11008 x 4096 833 us, rounded to bf16 657; 4096 x 1536 x 384 64 and 46);
+//   - fp16: dP by powers of two, so that neither small values become subnormal nor large ones, times a slope
+//     above 1, infinite (256 x 512 x 256 with dC of 1e-5: errors of dW 5.6e-3 with dP as it is, 3.1e-4 so, 2.4e-4 of
+//     the result's rounding); W and A are as they lie.  Up to 128 rows, where the bytes of W bound the time, with
+//     its remainder.  The largest magnitudes cost a sweep: 4096 x 11008 x 4096 663 and 804 us, 200 x 4096 x
+//     4096 50 and 68.
+// dbias sums dP before any of that.  (P's own rounding to the type leaves errors of 1.06 times a plain form's, which
+// keeps P in fp32.)
 //
 // fp32: two fp16 planes.  A product's powers of two belong to the indices that
 // it does not sum over, so that every row and column of a gradient keeps the bits
@@ -391,8 +388,14 @@ FewParts few_parts(int64_t n, int64_t k) {
   return FewParts{(int)std::max<int64_t>(1, (steps + per - 1) / per), (int)per};
 }
 
-// 16-bit types: rows up to which dP is held with its remainder.
-constexpr int kTwice = 128;
+// 16-bit types: rows up to which dP is held with its remainder.  bf16: as long as that is faster than fp16 by
+// powers of two (gradient by 256 rows of 4096 x 4096 81 and 79 us, by 384 105 and 90, of 11008 x 4096 191 and
+// 198, by 512 254 and 222, by 4096 1329 and 833; 512 x 1536 x 384 38 and 42, 2048 of it 52 and 50).
+template <class T>
+constexpr int kTwice = std::is_same_v<T, __bf16> ? 384 : 128;
+// Whether W and A are laid out by powers of two, too.
+template <class T>
+constexpr bool kAll = !std::is_same_v<T, _Float16>;
 
 struct Call {
   int64_t m, n, k;
@@ -424,10 +427,11 @@ Plan plan(int64_t m, int64_t n, int64_t k) {
     return p;
   }
   // (whatever the activation)
-  const int fold = P == 1 && m <= kTwice ? 2 : 1;
-  p.tops_at = r.take(kPowers<T, true> ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
+  const int fold = P == 1 && m <= kTwice<T> ? 2 : 1;
+  const bool held = fold == 1 || std::is_same_v<T, _Float16>;
+  p.tops_at = r.take(held ? (round_up(m, 64) + round_up(n, 64) + 2 * round_up(k, 64)) * 4 : 0);
   p.p_at = r.take(fold * P * m * p.np * 2);
-  p.pc_at = r.take(kPowers<T, true> ? fold * P * m * p.np * 2 : 0);
+  p.pc_at = r.take(held ? fold * P * m * p.np * 2 : 0);
   p.a_at = r.take(fold * P * m * p.kp * 2);
   p.w_at = r.take(P * n * p.kp * 2);
   p.sums_at = r.take((m + kRows - 1) / kRows * p.np * 4);
@@ -520,8 +524,9 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
   const bool rounds = P == 1 && m > 0 && c.act > OG_ACT_RELU;  // dP has more bits than the type
-  const int fold = rounds && m <= kTwice ? 2 : 1;
-  const bool held = P == 2 || (kPowers<T, true> && rounds);  // dP (fp32: A and W too) by powers of two
+  const int fold = rounds && m <= kTwice<T> ? 2 : 1;
+  // dP by powers of two
+  const bool held = P == 2 || (rounds && (fold == 1 || std::is_same_v<T, _Float16>));
   Matrix dp{};
   dp.rows_per = rows_per<T>(m, held);
   dp.x = c.dc;
@@ -563,12 +568,12 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       if (c.da) {
         dp.rtop = r;
         dp.out = at(p.p_at);
-        if (P == 2) mw = of(c.w, c.ldw, n, tw, at(p.w_at));
+        if (kAll<T>) mw = of(c.w, c.ldw, n, tw, at(p.w_at));
       }
       if (c.dw) {
         dp.ctop = t;
         dp.out_c = at(p.pc_at);
-        if (P == 2) ma = of(c.a, c.lda, m, ta, at(p.a_at));
+        if (kAll<T>) ma = of(c.a, c.lda, m, ta, at(p.a_at));
       }
       for (Matrix *x : {&dp, &ma, &mw}) x->blocks = sweep_blocks<T>(*x);
       const int blocks = dp.blocks + ma.blocks + mw.blocks;
@@ -584,7 +589,7 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       rows = Operand{at(p.p_at), P * p.np, 0};
       cols = Operand{at(p.pc_at), P * p.np, 0};
       rtop = r, ctop = t;
-      if (P == 2) {
+      if (kAll<T>) {
         A = Operand{at(p.a_at), P * p.kp, 0};
         W = Operand{at(p.w_at), P * p.kp, 0};
         atop = ta, wtop = tw;
@@ -604,19 +609,26 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
       }
       rows = cols = place ? Operand{static_cast<const uint16_t *>(c.dc), c.lddc, 0} : Operand{at(p.p_at), p.np, 0};
     }
-    if (c.dw) A = operand16<T>(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
-    if (c.da) W = operand16<T>(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
+    if (!held || !kAll<T>) {
+      if (c.dw) A = operand16<T>(c.a, c.lda, m, k, p.kp, c.ws + p.a_at, s, fold);
+      if (c.da) W = operand16<T>(c.w, c.ldw, n, k, p.kp, c.ws + p.w_at, s);
+    }
   }
   if (dp.sums) hipLaunchKernelGGL(bias_kernel<T>, dim3((n + 63) / 64), dim3(1024), 0, s, dp);
-  Args g{};
-  if (c.da && m > 0 && k > 0) {
-    g.a = rows, g.b = W, g.M = fold * m, g.N = k, g.K = n;
-    run_product<T, false, true, true>(g, output<T>(c.da, c.ldda, rtop, wtop), c.ws + p.parts_at, s, fold);
-  }
-  if (c.dw && n > 0 && k > 0) {
-    g.a = cols, g.b = A, g.M = n, g.N = k, g.K = fold * m;
-    run_product<T, true, true, true>(g, output<T>(c.dw, c.lddw, ctop, atop), c.ws + p.parts_at, s);
-  }
+  auto products = [&](auto element) {
+    using E = decltype(element);
+    Args g{};
+    if (c.da && m > 0 && k > 0) {
+      g.a = rows, g.b = W, g.M = fold * m, g.N = k, g.K = n;
+      run_product<T, false, true, true, E>(g, output<T>(c.da, c.ldda, rtop, wtop), c.ws + p.parts_at, s, fold);
+    }
+    if (c.dw && n > 0 && k > 0) {
+      g.a = cols, g.b = A, g.M = n, g.N = k, g.K = fold * m;
+      run_product<T, true, true, true, E>(g, output<T>(c.dw, c.lddw, ctop, atop), c.ws + p.parts_at, s);
+    }
+  };
+  if (held) products(_Float16());
+  else products(Element<T>());
 }
 
 }  // namespace og::epi::grad

@@ -458,11 +458,12 @@ int64_t og_gemm_nt_epi_workspace(int64_t m, int64_t n, int64_t k, int type);
  *     dA = dP W  (m x k, ldda),   dW = dP^T A  (n x k, lddw),   dbias_j = sum over i of dP_ij
  *
  * of `type` all, overwritten; each may be NULL (not wanted).  The slope of OG_ACT_RELU
- * is 1 where P > 0, else 0; of a NaN it is NaN.  16-bit types: dP is rounded to
- * the type for dA and dW (up to 128 rows with its remainder, rounded too), not for dbias;
- * that of OG_ACT_GELU to OG_ACT_SILU in fp16 by a power of two of its row (for dA) and of its
- * column (for dW), down to 2^-38 of the largest there, whatever its size.  Infinities and NaN of
- * 16-bit inputs follow the formula.  fp32: each row of dP and
+ * is 1 where P > 0, else 0; of a NaN it is NaN.  dP has more bits than a 16-bit type after
+ * OG_ACT_GELU to OG_ACT_SILU.  bf16 of up to 384 rows: it is rounded with its remainder, rounded too; of
+ * more rows it is held in fp16 by a power of two of its row (for dA) or column (for dW), and so are
+ * W (for dA) and A (for dW) by one of their columns, down to 2^-38 of the largest there.  fp16: dP is
+ * held by powers of two likewise, up to 128 rows with its remainder, W and A as they are.  Infinities
+ * and NaN of 16-bit inputs follow the formula.  fp32: each row of dP and
  * column of W (for dA), each column of dP and of A (for dW) is held as two fp16 planes by a power
  * of two of its own, as above; up to 32 rows take 24 bits.  dbias is summed in fp32
  * by 32 or 64 rows and in 64 bits over those.
