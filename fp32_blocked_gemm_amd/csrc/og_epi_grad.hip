@@ -37,8 +37,8 @@ namespace og::epi::grad {
 // 74; fp16: 153 and 140, 62 and 68, 71 and 94).
 constexpr int kWaves = 8, kRows = 32;
 template <class T>
-int rows_per(int64_t rows, bool held) {
-  return held && rows >= (kPlanes<T> == 2 ? 2048 : 8192) ? 2 * kRows : kRows;
+int rows_per(int64_t rows, bool tops) {
+  return tops && rows >= (kPlanes<T> == 2 ? 2048 : 8192) ? 2 * kRows : kRows;
 }
 template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // columns of a lane
@@ -523,12 +523,13 @@ void gradient(const Call &c, const Plan &p, hipStream_t s) {
   const int m = (int)c.m, n = (int)c.n, k = (int)c.k;
   auto at = [&](int64_t place) { return reinterpret_cast<uint16_t *>(c.ws + place); };
   const bool same = c.act == OG_ACT_NONE;
-  const bool rounds = P == 1 && m > 0 && c.act > OG_ACT_RELU;  // dP has more bits than the type
+  // a dP of more bits than the type, wanted as an operand
+  const bool rounds = P == 1 && m > 0 && c.act > OG_ACT_RELU && (c.da || c.dw);
   const int fold = rounds && m <= kTwice<T> ? 2 : 1;
   // dP by powers of two
   const bool held = P == 2 || (rounds && (fold == 1 || std::is_same_v<T, _Float16>));
   Matrix dp{};
-  dp.rows_per = rows_per<T>(m, held);
+  dp.rows_per = rows_per<T>(m, P == 2 || c.act > OG_ACT_RELU);  // (dbias is the same whatever else is wanted)
   dp.x = c.dc;
   dp.ldx = c.lddc;
   dp.pre = same ? nullptr : c.pre;
