@@ -7,10 +7,13 @@
 // every block takes one run.  Squares are added in 64 bits (those of 32-bit
 // values are exact there), by lane, wave, block and launch in a fixed order.
 //
-// 1.07 GB of bf16: the norm 185 us (5.8 TB/s, a part of it from the last-level cache), the
-// scaling 432 us (5.0 TB/s of reads and writes); 102 MB of fp32 in 55 tensors 25 and 42 us; 1 MB in
-// nine 4 and 4.  512 to 4096 blocks, 128 to 1024 threads and 1 to 8 loads a thread at once are
-// within 4 % of each other on the large ones.
+// Norm and scaling, kernels traced one by one: 1.08 GB of bf16 217 and 398 us (5.0 TB/s, 5.4 of reads and
+// writes; back to back 620 together), 102 MB of fp32 in 55 tensors 32 and 34, 1 MB in nine 4 and 4.  512 to
+// 4096 blocks, 128 to 1024 threads and 1 to 8 loads a thread at once are within 4 % of each other on the
+// large ones.
+// Tensors that do not begin on 16 bytes, and rows apart, go an element at a time: 500 MB of bf16 91 and 193 us
+// aligned, 460 and 504 from an odd element on; 16384 rows of fp32 42 and 104 dense (4096 columns), 148 and 206
+// apart (4095), of bf16 24 and 37, 117 and 139.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

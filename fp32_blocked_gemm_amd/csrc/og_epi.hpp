@@ -474,7 +474,8 @@ void run_product(Args g, const Finish &f, char *ws, hipStream_t s, int fold = 1)
                      e.part, e.ld, rows * e.ld, f);
 }
 
-// Whether the tile product can read a 16-bit matrix where it lies.
+// Whether the tile product can read a 16-bit matrix where it lies; else each call copies it first (64, 512 and
+// 4096 rows of bf16 on 11008 x 4096 27, 56 and 317 us, on 11008 x 4095 67, 96 and 361).
 inline bool readable(const void *p, int64_t cols, int64_t ld) {
   return cols % 8 == 0 && ld % 8 == 0 && ld <= (1 << 22) && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
