@@ -118,9 +118,30 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
     T8 in;
     f32x8 b;
     uint32_t bits = 0xFF;
+    if (!all) {
+      // only what a penalty changes; others of a vector keep their bits, of a NaN too (stored one by one: up to
+      // 2 us more)
+      if (!p.tokens) return;
+      count(p, row, v0, size, counts);
+      for (int i = 8 * tid; i < size; i += 8 * kThreads) {
+        if (i + 8 <= size) {
+          const u32x8 c = *reinterpret_cast<const u32x8 *>(counts + i);
+          if (!(c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7])) continue;
+          T8 now = *reinterpret_cast<const T8 *>(z + i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (steps.penalise(c[e])) now[e] = (T)steps((float)now[e], c[e], 0.0f, 1);
+          *reinterpret_cast<T8 *>(o + i) = now;
+        } else {
+          for (int k = i; k < size; ++k)
+            if (steps.penalise(counts[k])) o[k] = (T)steps((float)z[k], counts[k], 0.0f, 1);
+        }
+      }
+      return;
+    }
     auto load = [&](int i) __attribute__((always_inline)) {
       if (i + 8 > size) return;
-      if (all) in = *reinterpret_cast<const T8 *>(z + i);
+      in = *reinterpret_cast<const T8 *>(z + i);
       if (bias) b = *reinterpret_cast<const f32x8 *>(bias + i);
       if (mask) bits = reinterpret_cast<const uint8_t *>(mask)[i >> 3];
     };
@@ -134,15 +155,6 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
         load(i + 8 * kThreads);
         u32x8 c = {0, 0, 0, 0, 0, 0, 0, 0};
         if (p.tokens) c = *reinterpret_cast<const u32x8 *>(counts + i);
-        if (!all) {
-          if (!(c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7])) continue;
-          now = *reinterpret_cast<const T8 *>(z + i);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)  // (the others keep their bits, of a NaN too; stored one by one: up to 2 us more)
-            if (steps.penalise(c[e])) now[e] = (T)steps((float)now[e], c[e], 0.0f, 1);
-          *reinterpret_cast<T8 *>(o + i) = now;
-          continue;
-        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           now[e] = (T)steps((float)now[e], c[e], bias ? add[e] : 0.0f, allowed & (1u << e));
@@ -150,7 +162,6 @@ __global__ __launch_bounds__(kThreads, 8) void penalties_kernel(Problem p) {
       } else {
         for (int k = i; k < size; ++k) {
           const uint32_t c = p.tokens ? counts[k] : 0;
-          if (!all && !steps.penalise(c)) continue;
           o[k] = (T)steps((float)z[k], c, bias ? bias[k] : 0.0f, mask ? mask[k >> 5] >> (k & 31) & 1 : 1);
         }
       }
