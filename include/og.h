@@ -463,10 +463,10 @@ int64_t og_gemm_nt_epi_workspace(int64_t m, int64_t n, int64_t k, int type);
  * more rows it is held in fp16 by a power of two of its row (for dA) or column (for dW), and so are
  * W (for dA) and A (for dW) by one of their columns, down to 2^-38 of the largest there.  fp16: dP is
  * held by powers of two likewise, up to 128 rows with its remainder, W and A as they are.  Infinities
- * and NaN of 16-bit inputs follow the formula.  fp32: each row of dP and
- * column of W (for dA), each column of dP and of A (for dW) is held as two fp16 planes by a power
- * of two of its own, as above; up to 32 rows take 24 bits.  dbias is summed in fp32
- * by 32 or 64 rows and in 64 bits over those.
+ * and NaN of 16-bit inputs follow the formula (a value lost below its largest meets them as 0).
+ * fp32: each row of dP and column of W (for dA), each column of dP and of A (for dW) is held as two
+ * fp16 planes by a power of two of its own, as above; up to 32 rows take 24 bits.  dbias sums dP before
+ * all that, in fp32 by 32 or 64 rows and in 64 bits over those.
  * Requirements as above, with a workspace of og_gemm_nt_epi_grad_workspace(m, n, k, type)
  * bytes; W is read for dA only, A for dW only.  The outputs must not overlap the
  * inputs.  m == 0 clears dW and dbias, n == 0 dA.
