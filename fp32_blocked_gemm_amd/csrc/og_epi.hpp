@@ -376,8 +376,8 @@ struct Cost {
 
 // The tiles by planes and by whether both operands are transposed (dW).  Beside og_tile.hpp's squares
 // are oblong ones, which fill the compute units where squares leave a part of a round (512 x 11008
-// x 4096 fp32: 174 tiles of 192 x 192 168 us, 232 of 128 x 192 122).  Times measured on stages of k 1024
-// to 3072.  (144 seeded products of 65 to 11008 rows and columns, 24 of each kind: the chosen tile and
+// x 4096 fp32: 174 tiles of 192 x 192 168 us, 232 of 128 x 192 122).  Times measured on stages of k from 1024
+// on.  (144 seeded products of 65 to 11008 rows and columns, 24 of each kind: the chosen tile and
 // parts take 1.01 to 1.05 times the fastest listed ones' time in the mean, at most 1.20.)
 template <class E, int P, bool TT>
 struct EpiTiles {
